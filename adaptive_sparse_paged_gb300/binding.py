@@ -23,6 +23,8 @@ ASP_OK, ASP_EINVAL, ASP_EUNSUPPORTED, ASP_EWORKSPACE, ASP_ECUDA, ASP_EDEVICE = 0
 ASP_SUMMARIZE_BULK, ASP_SUMMARIZE_APPEND = 0, 1
 ASP_DEVERR_PAGE_RANGE, ASP_DEVERR_LIST_RANGE, ASP_DEVERR_LEN_RANGE = 0x1, 0x2, 0x4
 ASP_DEVERR_SEQ_RANGE, ASP_DEVERR_TIMEOUT = 0x8, 0x10
+ASP_DEVERR_OFFSET_RANGE = 0x20
+ASP_MAX_NEW_TOKENS = 1 << 22
 
 #: every symbol include/asp.h declares
 EXPORTED = (
@@ -39,6 +41,11 @@ EXPORTED = (
     "asp_get_device_error",
     "asp_coverage_select_noalloc",
     "asp_selftest_wait_timeout",
+    "asp_norm_rotate_append",
+    "asp_chunk_attention",
+    "asp_chunk_weights",
+    "asp_decode_weights",
+    "asp_weight_evict",
 )
 
 
@@ -98,6 +105,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "asp_get_device_error": ([vp, u32p, vp], i32),
             "asp_coverage_select_noalloc": ([kvp, vp, ctypes.c_float, i32, vp, vp, vp, vp], i32),
             "asp_selftest_wait_timeout": ([vp, sz, vp], i32),
+            "asp_norm_rotate_append": ([kvp, vp, vp, i32, vp, vp, vp, ctypes.c_float, vp, i32, i32,
+                                        vp, vp, vp, sz, vp], i32),
+            "asp_chunk_attention": ([kvp, vp, vp, i32, ctypes.c_float, vp, vp, vp, sz, vp], i32),
+            "asp_chunk_weights": ([kvp, vp, vp, i32, vp, ctypes.c_float, ctypes.c_float, vp, vp,
+                                   vp, sz, vp], i32),
+            "asp_decode_weights": ([kvp, vp, vp, vp, vp, ctypes.c_float, ctypes.c_float, vp, vp,
+                                    vp, sz, vp], i32),
+            "asp_weight_evict": ([kvp, vp, i32, i32, vp, vp, vp, vp, vp, sz, vp], i32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)
@@ -313,6 +328,143 @@ def asp_coverage_select_noalloc(kv: PagedKV, q: torch.Tensor, gamma: float, budg
             kv.ref, q.data_ptr(), ctypes.c_float(gamma), int(budget), lists.data_ptr(),
             lens.data_ptr(), err_ptr, _stream_ptr(kv.device, stream)),
             "asp_coverage_select_noalloc")
+
+
+def _weights_shape(kv: PagedKV):
+    return (kv.batch, kv.num_kv_heads, kv.max_pages * kv.page_size)
+
+
+def new_weights(kv: PagedKV) -> torch.Tensor:
+    """Zeroed attention weights [B, Hkv, max_pages * P] fp32 for this cache."""
+    return torch.zeros(_weights_shape(kv), dtype=torch.float32, device=kv.device)
+
+
+def _need_rows(kv: PagedKV, t: torch.Tensor, name: str, heads: int) -> int:
+    """Packed bf16 rows [num_tokens, heads, d]; returns num_tokens."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a tensor [num_tokens, {heads}, {kv.head_dim}]")
+    _need(t, name, torch.bfloat16, kv.device, (t.shape[0], heads, kv.head_dim))
+    return int(t.shape[0])
+
+
+def _need_weights(kv: PagedKV, w_in, w_out) -> int | None:
+    _need(w_out, "w_out", torch.float32, kv.device, _weights_shape(kv))
+    if w_in is None:
+        return None
+    _need(w_in, "w_in", torch.float32, kv.device, _weights_shape(kv))
+    return w_in.data_ptr()
+
+
+def asp_norm_rotate_append(kv: PagedKV, qkv: torch.Tensor, q_offsets, positions, q_weight, k_weight,
+                           eps: float, inv_freq, interleaved: bool, q_out: torch.Tensor,
+                           ws: torch.Tensor, stream=None) -> None:
+    """Norms, rotates and writes the new tokens' rows qkv (bf16 [N, Hq + 2 Hkv, d]).
+
+    q_offsets: int32 [B + 1], or None for one row per request; positions: int32
+    [N] or None (the slots); q_weight, k_weight: bf16 [d] or None (not normed);
+    inv_freq: fp32 [rotary_dim / 2] or None (no rotation); q_out: bf16 or fp32
+    [N, Hq, d], the normed and rotated queries."""
+    n = _need_rows(kv, qkv, "qkv", kv.num_q_heads + 2 * kv.num_kv_heads)
+    if q_offsets is not None:
+        _need(q_offsets, "q_offsets", torch.int32, kv.device, (kv.batch + 1,))
+    if positions is not None:
+        _need(positions, "positions", torch.int32, kv.device, (n,))
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, name, torch.bfloat16, kv.device, (kv.head_dim,))
+    if inv_freq is not None:
+        _need(inv_freq, "inv_freq", torch.float32, kv.device, (inv_freq.numel(),))
+    if not isinstance(q_out, torch.Tensor) or q_out.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("q_out must be a torch.bfloat16 or torch.float32 tensor")
+    _need(q_out, "q_out", q_out.dtype, kv.device, (n, kv.num_q_heads, kv.head_dim))
+    _need(ws, "ws", torch.uint8, kv.device)
+
+    def ptr(t):
+        return None if t is None else t.data_ptr()
+
+    half = q_out.dtype == torch.bfloat16
+    with torch.cuda.device(kv.device):
+        _check(load_library().asp_norm_rotate_append(
+            kv.ref, _rows_ptr(qkv), ptr(q_offsets), n, ptr(positions), ptr(q_weight),
+            ptr(k_weight), ctypes.c_float(eps), ptr(inv_freq),
+            0 if inv_freq is None else 2 * inv_freq.numel(), int(bool(interleaved)),
+            _rows_ptr(q_out) if half else None, None if half else _rows_ptr(q_out), ws.data_ptr(),
+            ws.numel(), _stream_ptr(kv.device, stream)), "asp_norm_rotate_append")
+
+
+def _rows_ptr(t: torch.Tensor) -> int:
+    """data_ptr of packed rows; a tensor without rows has none, and the library
+    wants an aligned non-null one that it never reads."""
+    return t.data_ptr() if t.numel() else 256
+
+
+def asp_chunk_attention(kv: PagedKV, q: torch.Tensor, q_offsets: torch.Tensor, sm_scale: float,
+                        out: torch.Tensor, lse: torch.Tensor, ws: torch.Tensor,
+                        stream=None) -> None:
+    """Causal attention of the new tokens' rows q (bf16 [N, Hq, d]) over the cache."""
+    n = _need_rows(kv, q, "q", kv.num_q_heads)
+    _need(q_offsets, "q_offsets", torch.int32, kv.device, (kv.batch + 1,))
+    _need(out, "out", torch.bfloat16, kv.device, (n, kv.num_q_heads, kv.head_dim))
+    _need(lse, "lse", torch.float32, kv.device, (n, kv.num_q_heads))
+    _need(ws, "ws", torch.uint8, kv.device)
+    with torch.cuda.device(kv.device):
+        _check(load_library().asp_chunk_attention(
+            kv.ref, _rows_ptr(q), q_offsets.data_ptr(), n, ctypes.c_float(sm_scale),
+            _rows_ptr(out), _rows_ptr(lse), ws.data_ptr(), ws.numel(),
+            _stream_ptr(kv.device, stream)), "asp_chunk_attention")
+
+
+def asp_chunk_weights(kv: PagedKV, q: torch.Tensor, q_offsets: torch.Tensor, lse: torch.Tensor,
+                      sm_scale: float, decay: float, w_in, w_out: torch.Tensor, ws: torch.Tensor,
+                      stream=None) -> None:
+    """w_out = decay * w_in + the attention weight each cached token got from the rows q."""
+    n = _need_rows(kv, q, "q", kv.num_q_heads)
+    _need(q_offsets, "q_offsets", torch.int32, kv.device, (kv.batch + 1,))
+    _need(lse, "lse", torch.float32, kv.device, (n, kv.num_q_heads))
+    w_ptr = _need_weights(kv, w_in, w_out)
+    _need(ws, "ws", torch.uint8, kv.device)
+    with torch.cuda.device(kv.device):
+        _check(load_library().asp_chunk_weights(
+            kv.ref, _rows_ptr(q), q_offsets.data_ptr(), n, _rows_ptr(lse),
+            ctypes.c_float(sm_scale), ctypes.c_float(decay), w_ptr, w_out.data_ptr(),
+            ws.data_ptr(), ws.numel(), _stream_ptr(kv.device, stream)), "asp_chunk_weights")
+
+
+def asp_decode_weights(kv: PagedKV, q: torch.Tensor, lists, lens, lse: torch.Tensor,
+                       sm_scale: float, decay: float, w_in, w_out: torch.Tensor, ws: torch.Tensor,
+                       stream=None) -> None:
+    """w_out = decay * w_in + the attention weight of a decode step (lists and lens None: every page)."""
+    _need(q, "q", torch.float32, kv.device, (kv.batch, kv.num_q_heads, kv.head_dim))
+    lists_ptr = lens_ptr = None
+    if lists is not None or lens is not None:
+        _need(lists, "lists", torch.int32, kv.device, (kv.batch, kv.num_kv_heads, kv.max_pages))
+        _need(lens, "lens", torch.int32, kv.device, (kv.batch, kv.num_kv_heads))
+        lists_ptr, lens_ptr = lists.data_ptr(), lens.data_ptr()
+    _need(lse, "lse", torch.float32, kv.device, (kv.batch, kv.num_q_heads))
+    w_ptr = _need_weights(kv, w_in, w_out)
+    _need(ws, "ws", torch.uint8, kv.device)
+    with torch.cuda.device(kv.device):
+        _check(load_library().asp_decode_weights(
+            kv.ref, q.data_ptr(), lists_ptr, lens_ptr, lse.data_ptr(), ctypes.c_float(sm_scale),
+            ctypes.c_float(decay), w_ptr, w_out.data_ptr(), ws.data_ptr(), ws.numel(),
+            _stream_ptr(kv.device, stream)), "asp_decode_weights")
+
+
+def asp_weight_evict(kv: PagedKV, weights: torch.Tensor, keep: int, recent: int,
+                     dst_table: torch.Tensor, w_out: torch.Tensor, kept: torch.Tensor,
+                     new_lens: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """Keeps the `recent` newest and the heaviest other tokens of every head, `keep` in all."""
+    _need(weights, "weights", torch.float32, kv.device, _weights_shape(kv))
+    _need(dst_table, "dst_table", torch.int32, kv.device, (kv.batch, kv.max_pages))
+    _need(w_out, "w_out", torch.float32, kv.device, _weights_shape(kv))
+    _need(kept, "kept", torch.int32, kv.device, (kv.batch, kv.num_kv_heads, int(keep)))
+    _need(new_lens, "new_lens", torch.int32, kv.device, (kv.batch,))
+    _need(ws, "ws", torch.uint8, kv.device)
+    with torch.cuda.device(kv.device):
+        _check(load_library().asp_weight_evict(
+            kv.ref, weights.data_ptr(), int(keep), int(recent), dst_table.data_ptr(),
+            w_out.data_ptr(), kept.data_ptr(), new_lens.data_ptr(), ws.data_ptr(), ws.numel(),
+            _stream_ptr(kv.device, stream)), "asp_weight_evict")
 
 
 def asp_selftest_wait_timeout(ws: torch.Tensor, stream=None) -> None:

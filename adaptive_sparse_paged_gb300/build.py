@@ -21,7 +21,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libasp.so")
 SOURCES = ["abi.cu", "summarize.cu", "select.cu", "select_cluster.cu", "decode.cu",
-           "noalloc.cu"]
+           "noalloc.cu", "norm_rotate.cu", "chunk_attention.cu", "weights.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

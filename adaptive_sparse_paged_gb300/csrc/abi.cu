@@ -49,6 +49,22 @@ asp_status check_ws(const asp_paged_kv* kv, void* ws, size_t ws_bytes, WsLayout*
   return ASP_OK;
 }
 
+bool misaligned(const void* p, uintptr_t bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
+}
+
+// The packed rows of new tokens: bf16, 16-byte aligned.
+asp_status check_rows(int32_t num_tokens, const uint16_t* rows) {
+  if (num_tokens < 0 || !rows || misaligned(rows, 16)) return ASP_EINVAL;
+  return num_tokens > ASP_MAX_NEW_TOKENS ? ASP_EUNSUPPORTED : ASP_OK;
+}
+
+asp_status check_weights(float sm_scale, float decay, const float* w_in, const float* w_out) {
+  if (!(sm_scale > 0.0f) || !std::isfinite(sm_scale)) return ASP_EINVAL;
+  if (!(decay >= 0.0f) || !std::isfinite(decay)) return ASP_EINVAL;
+  return misaligned(w_in, 16) || misaligned(w_out, 16) ? ASP_EINVAL : ASP_OK;
+}
+
 asp_status from_cuda(cudaError_t e) { return e == cudaSuccess ? ASP_OK : ASP_ECUDA; }
 
 // One warp; thread 0 waits on a barrier that expects one arrival which never
@@ -250,6 +266,104 @@ asp_status asp_sparse_decode(const asp_paged_kv* kv, const float* q, const int32
                reinterpret_cast<int32_t*>(w + lay.arrivals_off), reinterpret_cast<uint32_t*>(w),
                lay.decode_grid, lay.slot_floats};
   return from_cuda(launch_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+asp_status asp_norm_rotate_append(const asp_paged_kv* kv, const uint16_t* qkv,
+                                  const int32_t* q_offsets, int32_t num_tokens,
+                                  const int32_t* positions, const uint16_t* q_weight,
+                                  const uint16_t* k_weight, float eps, const float* inv_freq,
+                                  int32_t rotary_dim, int32_t interleaved, uint16_t* q_out,
+                                  float* q_out_f32, void* ws, size_t ws_bytes, asp_stream stream) {
+  NvtxRange range("asp_norm_rotate_append");
+  asp_status st = check_kv(kv);
+  if (st != ASP_OK) return st;
+  if ((st = check_rows(num_tokens, qkv)) != ASP_OK) return st;
+  if (!q_offsets && num_tokens != kv->batch) return ASP_EINVAL;
+  if (!q_out && !q_out_f32) return ASP_EINVAL;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return ASP_EINVAL;
+  if (rotary_dim < 0 || rotary_dim > kv->head_dim || rotary_dim % 8 != 0) return ASP_EINVAL;
+  if (rotary_dim > 0 && !inv_freq) return ASP_EINVAL;
+  if (interleaved != 0 && interleaved != 1) return ASP_EINVAL;
+  if (misaligned(q_out, 16) || misaligned(q_out_f32, 16) || misaligned(q_weight, 8) ||
+      misaligned(k_weight, 8) || misaligned(inv_freq, 4))
+    return ASP_EINVAL;
+  WsLayout lay;
+  if ((st = check_ws(kv, ws, ws_bytes, &lay)) != ASP_OK) return st;
+  if (num_tokens == 0) return ASP_OK;
+  NormRotateArgs a{kv, qkv, q_offsets, num_tokens, positions, q_weight, k_weight, eps, inv_freq,
+                   rotary_dim, interleaved, q_out, q_out_f32, static_cast<uint32_t*>(ws),
+                   current_device_sm_count()};
+  return from_cuda(launch_norm_rotate(a, static_cast<cudaStream_t>(stream)));
+}
+
+asp_status asp_chunk_attention(const asp_paged_kv* kv, const uint16_t* q,
+                               const int32_t* q_offsets, int32_t num_tokens, float sm_scale,
+                               uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                               asp_stream stream) {
+  NvtxRange range("asp_chunk_attention");
+  asp_status st = check_kv(kv);
+  if (st != ASP_OK) return st;
+  if ((st = check_rows(num_tokens, q)) != ASP_OK) return st;
+  if (!q_offsets || !out || !lse || misaligned(out, 16)) return ASP_EINVAL;
+  if (!(sm_scale > 0.0f) || !std::isfinite(sm_scale)) return ASP_EINVAL;
+  WsLayout lay;
+  if ((st = check_ws(kv, ws, ws_bytes, &lay)) != ASP_OK) return st;
+  if (num_tokens == 0) return ASP_OK;
+  ChunkAttentionArgs a{kv, q, q_offsets, num_tokens, sm_scale, out, lse,
+                       static_cast<uint32_t*>(ws)};
+  return from_cuda(launch_chunk_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
+asp_status asp_chunk_weights(const asp_paged_kv* kv, const uint16_t* q, const int32_t* q_offsets,
+                             int32_t num_tokens, const float* lse, float sm_scale, float decay,
+                             const float* w_in, float* w_out, void* ws, size_t ws_bytes,
+                             asp_stream stream) {
+  NvtxRange range("asp_chunk_weights");
+  asp_status st = check_kv(kv);
+  if (st != ASP_OK) return st;
+  if ((st = check_rows(num_tokens, q)) != ASP_OK) return st;
+  if (!q_offsets || !lse || !w_out) return ASP_EINVAL;
+  if ((st = check_weights(sm_scale, decay, w_in, w_out)) != ASP_OK) return st;
+  WsLayout lay;
+  if ((st = check_ws(kv, ws, ws_bytes, &lay)) != ASP_OK) return st;
+  WeightArgs a{kv, q, q_offsets, num_tokens, nullptr, nullptr, nullptr, lse, sm_scale, decay,
+               w_in, w_out, static_cast<uint32_t*>(ws)};
+  return from_cuda(launch_chunk_weights(a, static_cast<cudaStream_t>(stream)));
+}
+
+asp_status asp_decode_weights(const asp_paged_kv* kv, const float* q, const int32_t* lists,
+                              const int32_t* lens, const float* lse, float sm_scale, float decay,
+                              const float* w_in, float* w_out, void* ws, size_t ws_bytes,
+                              asp_stream stream) {
+  NvtxRange range("asp_decode_weights");
+  asp_status st = check_kv(kv);
+  if (st != ASP_OK) return st;
+  if (!q || !lse || !w_out || misaligned(q, 16)) return ASP_EINVAL;
+  if ((lists == nullptr) != (lens == nullptr)) return ASP_EINVAL;
+  if ((st = check_weights(sm_scale, decay, w_in, w_out)) != ASP_OK) return st;
+  WsLayout lay;
+  if ((st = check_ws(kv, ws, ws_bytes, &lay)) != ASP_OK) return st;
+  WeightArgs a{kv, nullptr, nullptr, kv->batch, q, lists, lens, lse, sm_scale, decay, w_in, w_out,
+               static_cast<uint32_t*>(ws)};
+  return from_cuda(launch_decode_weights(a, static_cast<cudaStream_t>(stream)));
+}
+
+asp_status asp_weight_evict(const asp_paged_kv* kv, const float* weights, int32_t keep,
+                            int32_t recent, const int32_t* dst_table, float* w_out, int32_t* kept,
+                            int32_t* new_lens, void* ws, size_t ws_bytes, asp_stream stream) {
+  NvtxRange range("asp_weight_evict");
+  asp_status st = check_kv(kv);
+  if (st != ASP_OK) return st;
+  if (!weights || !dst_table || !w_out || !kept || !new_lens) return ASP_EINVAL;
+  if (new_lens == kv->seq_lens) return ASP_EINVAL;
+  if (misaligned(weights, 16) || misaligned(w_out, 16)) return ASP_EINVAL;
+  if (keep < 1 || (long long)keep > (long long)kv->max_pages * kv->page_size) return ASP_EINVAL;
+  if (recent < 0 || recent > keep) return ASP_EINVAL;
+  WsLayout lay;
+  if ((st = check_ws(kv, ws, ws_bytes, &lay)) != ASP_OK) return st;
+  EvictArgs a{kv, weights, keep, recent, dst_table, w_out, kept, new_lens,
+              static_cast<uint32_t*>(ws)};
+  return from_cuda(launch_evict(a, static_cast<cudaStream_t>(stream)));
 }
 
 asp_status asp_selftest_wait_timeout(void* ws, size_t ws_bytes, asp_stream stream) {

@@ -101,6 +101,32 @@ __device__ __forceinline__ int clamp_seq_len(int T, int max_pages, int P, uint32
   return T;
 }
 
+// Request b's rows of a packed batch of new tokens: [row0, row0 + n), the last
+// n of its T cached tokens. q_offsets null: one row per request. Offsets that
+// do not ascend within [0, num_tokens], or that give more rows than T, set
+// ASP_DEVERR_OFFSET_RANGE and leave the request without rows.
+struct NewRows {
+  int row0, n;
+};
+__device__ __forceinline__ NewRows new_rows(const int32_t* q_offsets, int b, int T, int num_tokens,
+                                            uint32_t* err) {
+  NewRows r{b, 1};
+  if (q_offsets) {
+    r.row0 = q_offsets[b];
+    const int end = q_offsets[b + 1];
+    r.n = end - r.row0;
+    if (r.row0 < 0 || end < r.row0 || end > num_tokens) {
+      report(err, ASP_DEVERR_OFFSET_RANGE);
+      return NewRows{0, 0};
+    }
+  }
+  if (r.n > T) {
+    if (q_offsets) report(err, ASP_DEVERR_OFFSET_RANGE);  // an empty request has no row to skip
+    return NewRows{0, 0};
+  }
+  return r;
+}
+
 // ------------------------------------------------------------------ mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));
@@ -368,6 +394,69 @@ struct DecodeArgs {
   int slot_floats;
 };
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
+
+// New tokens of a packed batch: rows q_offsets[b] .. q_offsets[b + 1] - 1 belong
+// to request b and are the last of its seq_lens[b] tokens. q_offsets null: one
+// row per request.
+struct NormRotateArgs {
+  const asp_paged_kv* kv;
+  const uint16_t* qkv;
+  const int32_t* q_offsets;
+  int num_tokens;
+  const int32_t* positions;
+  const uint16_t* q_weight;
+  const uint16_t* k_weight;
+  float eps;
+  const float* inv_freq;
+  int rotary_dim;
+  int interleaved;
+  uint16_t* q_out;
+  float* q_out_f32;
+  uint32_t* err;
+  int num_sms;
+};
+cudaError_t launch_norm_rotate(const NormRotateArgs& a, cudaStream_t stream);
+
+struct ChunkAttentionArgs {
+  const asp_paged_kv* kv;
+  const uint16_t* q;
+  const int32_t* q_offsets;
+  int num_tokens;
+  float sm_scale;
+  uint16_t* out;
+  float* lse;
+  uint32_t* err;
+};
+cudaError_t launch_chunk_attention(const ChunkAttentionArgs& a, cudaStream_t stream);
+
+struct WeightArgs {
+  const asp_paged_kv* kv;
+  const uint16_t* q;           // chunk form
+  const int32_t* q_offsets;
+  int num_tokens;
+  const float* q_f32;          // decode form
+  const int32_t* lists;        // null: every page
+  const int32_t* lens;
+  const float* lse;
+  float sm_scale, decay;
+  const float* w_in;           // null: no weight before this call
+  float* w_out;
+  uint32_t* err;
+};
+cudaError_t launch_chunk_weights(const WeightArgs& a, cudaStream_t stream);
+cudaError_t launch_decode_weights(const WeightArgs& a, cudaStream_t stream);
+
+struct EvictArgs {
+  const asp_paged_kv* kv;
+  const float* weights;
+  int keep, recent;
+  const int32_t* dst_table;
+  float* w_out;
+  int32_t* kept;
+  int32_t* new_lens;
+  uint32_t* err;
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 
 // A 2-D bf16 tensor map over [rows, inner] (row stride inner * 2 bytes) with
 // boxes of [box_rows, box_inner] elements, the 128-byte swizzle and zero

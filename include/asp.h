@@ -70,6 +70,7 @@ typedef enum asp_status {
 #define ASP_DEVERR_LEN_RANGE 0x4u  /* lens[b,h] outside [0, N_b]: clamped */
 #define ASP_DEVERR_SEQ_RANGE 0x8u  /* seq_lens[b] outside [0, max_pages*P]: clamped */
 #define ASP_DEVERR_TIMEOUT 0x10u   /* a bounded on-chip wait ran out: the kernel stopped early */
+#define ASP_DEVERR_OFFSET_RANGE 0x20u /* q_offsets not ascending in [0, num_tokens], or more new rows than seq_lens: request skipped */
 
 /* A cudaStream_t, passed as an opaque pointer. NULL is the legacy default stream. */
 typedef void* asp_stream;
@@ -253,6 +254,150 @@ asp_status asp_sparse_decode(const asp_paged_kv* kv, const float* q,
                              const int32_t* lists, const int32_t* lens, float sm_scale,
                              float* out, float* lse,
                              void* ws, size_t ws_bytes, asp_stream stream);
+
+/*
+ * ------------------------------------------------------------------------
+ * New tokens in bulk, and eviction. The pages describe decoding only; these
+ * calls are the rest of a cache's life: a prompt's tokens are normed, rotated
+ * and written (asp_norm_rotate_append), attend over the cache
+ * (asp_chunk_attention), leave the attention weight that every cached token
+ * received (asp_chunk_weights, asp_decode_weights), and a cache that has
+ * grown too long keeps its heaviest and newest tokens (asp_weight_evict).
+ *
+ * Packed batches: the new tokens of all requests lie behind one another in
+ * rows 0 .. num_tokens - 1. q_offsets is int32 [batch + 1] on the device: rows
+ * q_offsets[b] .. q_offsets[b + 1] - 1 belong to request b (none is fine) and
+ * are the LAST of its seq_lens[b] tokens, which already count them. Rows
+ * outside [q_offsets[0], q_offsets[batch]) are neither read nor written.
+ * Offsets that do not ascend within [0, num_tokens], or that give a request
+ * more rows than seq_lens[b], set ASP_DEVERR_OFFSET_RANGE: that request is
+ * skipped, and others of the call may be. num_tokens may be 0; at most ASP_MAX_NEW_TOKENS.
+ * ------------------------------------------------------------------------
+ */
+#define ASP_MAX_NEW_TOKENS (1 << 22)
+
+/*
+ * New tokens into the cache: per-head norms of queries and keys, position
+ * rotation, the write of K and V into their pages and the fold of the keys
+ * into the page summaries, in one kernel.
+ *   y = x * rsqrt(mean(x^2) + eps) * weight      q and k heads; fp32
+ *   pairs (i, i + rotary_dim/2), or (2i, 2i + 1) when interleaved, i <
+ *   rotary_dim/2, turn by positions[row] * inv_freq[i]; the angle is reduced
+ *   exactly, so far positions keep their precision.
+ * qkv        : bf16 [num_tokens, Hq + 2*Hkv, d]: the row's query heads, then its
+ *              key heads, then its value heads. 16-byte aligned.
+ * q_offsets  : see above, or NULL: one row per request (num_tokens = batch;
+ *              requests with T_b = 0 are skipped).
+ * positions  : int32 [num_tokens], or NULL: each token's slot in its request.
+ *              A cache that was evicted from has fewer slots than positions.
+ * q_weight, k_weight : bf16 [d], 8-byte aligned; NULL: that side is not normed.
+ * inv_freq   : fp32 [rotary_dim / 2]; may be NULL when rotary_dim is 0.
+ * rotary_dim : 0 (no rotation) to d, a multiple of 8.
+ * q_out, q_out_f32 : [num_tokens, Hq, d] out, in bf16 (for asp_chunk_attention)
+ *              or fp32 (for asp_coverage_select and asp_sparse_decode); either
+ *              may be NULL, not both. 16-byte aligned.
+ * K (rounded once to bf16) and V go to slot (T_b - n_b + i) of their request;
+ * a page whose slot 0 is among them starts its summary afresh, the others fold
+ * into theirs. Idempotent. A physical page that takes new tokens belongs to one
+ * request only. Out-of-range table entries set ASP_DEVERR_PAGE_RANGE: their K
+ * and V are skipped, the queries are still written.
+ */
+asp_status asp_norm_rotate_append(const asp_paged_kv* kv, const uint16_t* qkv,
+                                  const int32_t* q_offsets, int32_t num_tokens,
+                                  const int32_t* positions, const uint16_t* q_weight,
+                                  const uint16_t* k_weight, float eps, const float* inv_freq,
+                                  int32_t rotary_dim, int32_t interleaved, uint16_t* q_out,
+                                  float* q_out_f32, void* ws, size_t ws_bytes, asp_stream stream);
+
+/*
+ * Causal attention of each request's new tokens over its whole cache (the new
+ * tokens' K and V included: append them first).
+ *   out[r,h,:] = sum_{s <= t} softmax_s(sm_scale * q[r,h].k_s) v_s
+ *   lse[r,h]   = log sum_{s <= t} exp(sm_scale * q[r,h].k_s)
+ * with t = T_b - n_b + i the slot of row r = q_offsets[b] + i.
+ * q   : bf16 [num_tokens, Hq, d], 16-byte aligned.
+ * out : bf16 [num_tokens, Hq, d], 16-byte aligned; lse : fp32 [num_tokens, Hq]
+ *       (natural log).
+ * Slots past T_b are never used, whatever they hold; pages with an
+ * out-of-range table entry are skipped (ASP_DEVERR_PAGE_RANGE); a row that
+ * sees no valid page gets out = 0, lse = -inf. V of the request's own tokens
+ * has to be finite: a later token's non-finite V row can reach earlier rows of
+ * the same chunk. Products run on tensor cores with fp32 accumulation; the
+ * probabilities are rounded to bf16 for the P.V product. The result does not
+ * depend on timing.
+ */
+asp_status asp_chunk_attention(const asp_paged_kv* kv, const uint16_t* q,
+                               const int32_t* q_offsets, int32_t num_tokens, float sm_scale,
+                               uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                               asp_stream stream);
+
+/*
+ * Attention weight that each cached token receives from the new tokens' rows,
+ * summed over the rows and over the query heads of its KV head:
+ *   w_out[b,h,s] = decay * w_in[b,h,s] + sum_{rows r with t_r >= s, heads of h}
+ *                  exp(sm_scale * q[r,head].k_s - lse[r,head])
+ * for every s < T_b; entries from T_b on are untouched. The chunk's own tokens
+ * (s >= T_b - n_b) had no weight before: w_in is not read there. A row whose
+ * lse is -inf adds nothing.
+ * q, q_offsets : as asp_chunk_attention; lse as it wrote it.
+ * decay : >= 0 and finite; 1 sums over all rows ever seen.
+ * w_in, w_out : fp32 [B, Hkv, max_pages * P], 16-byte aligned. w_in may be NULL
+ *               (nothing before) or the same buffer as w_out.
+ * Tokens of pages with an out-of-range table entry get nothing added. Sums are
+ * in fp32 and in a fixed order.
+ */
+asp_status asp_chunk_weights(const asp_paged_kv* kv, const uint16_t* q, const int32_t* q_offsets,
+                             int32_t num_tokens, const float* lse, float sm_scale, float decay,
+                             const float* w_in, float* w_out, void* ws, size_t ws_bytes,
+                             asp_stream stream);
+
+/*
+ * The same for a decode step (one token per request, the last of T_b):
+ *   w_out[b,h,s] = decay * w_in[b,h,s] + sum_{heads of h} exp(sm_scale * q.k_s - lse)
+ * for the tokens s < T_b of the listed pages, and decay * w_in for the others;
+ * w_in is not read for the token being decoded (s = T_b - 1).
+ * q    : fp32 [B, Hq, d], 16-byte aligned; lse : fp32 [B, Hq], as
+ *        asp_sparse_decode wrote it over the same lists.
+ * lists, lens : as written by asp_coverage_select; each page at most once in a
+ *        list. Both NULL: every page.
+ * Other arguments and conditions as for asp_chunk_weights.
+ */
+asp_status asp_decode_weights(const asp_paged_kv* kv, const float* q, const int32_t* lists,
+                              const int32_t* lens, const float* lse, float sm_scale, float decay,
+                              const float* w_in, float* w_out, void* ws, size_t ws_bytes,
+                              asp_stream stream);
+
+/*
+ * Eviction by accumulated attention weight. Per request b and KV head h, with
+ * n = min(T_b, keep): T_b <= keep keeps every token; otherwise the last
+ * `recent` tokens stay and, of the others, the keep - recent with the largest
+ * weight (equal weights: the lower slot stays; NaN counts as the largest). The
+ * kept tokens move, in ascending order of their old slots, to slots 0 .. n - 1:
+ *   kept[b,h,i]  = old slot of new slot i
+ *   K, V         slot i of dst_table's pages = old slot kept[b,h,i]
+ *   w_out[b,h,i] = weights[b,h,kept[b,h,i]]
+ *   summaries    of logical pages 0 .. ceil(n/P) - 1 recomputed
+ *   new_lens[b]  = n
+ * Every head and layer of a request ends with the same number of tokens, so one
+ * block table and one length serve them all: call this once per layer, then
+ * replace seq_lens by new_lens and the block table by dst_table, and give back
+ * the pages that are left over.
+ * weights   : fp32 [B, Hkv, max_pages * P]; entries past T_b are not read.
+ * keep      : >= 1, at most max_pages * P; recent : 0 .. keep.
+ * dst_table : int32 [B, max_pages], of which ceil(n/P) entries a request are
+ *             read. Either kv->block_table itself (in place) or a table whose
+ *             pages kv->block_table does not use. No page may belong to two
+ *             requests.
+ * w_out     : fp32 [B, Hkv, max_pages * P]; entries from n on are untouched. May
+ *             be the same buffer as weights.
+ * kept      : int32 [B, Hkv, keep] out; entries from n on are untouched.
+ * new_lens  : int32 [B] out; not the seq_lens buffer.
+ * An out-of-range entry of either table sets ASP_DEVERR_PAGE_RANGE; the rows it
+ * holds are not moved.
+ */
+asp_status asp_weight_evict(const asp_paged_kv* kv, const float* weights, int32_t keep,
+                            int32_t recent, const int32_t* dst_table, float* w_out, int32_t* kept,
+                            int32_t* new_lens, void* ws, size_t ws_bytes, asp_stream stream);
 
 /*
  * asp_coverage_select without a workspace. The paper has no counterpart: this

@@ -1,0 +1,167 @@
+"""asp_weight_evict against its definition: kept slots, moved rows, weights and summaries exactly."""
+
+import math
+
+import pytest
+import torch
+
+from adaptive_sparse_paged_gb300 import binding as B
+from tests import guards
+from tests import prompt_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+def same(x, y):
+    return torch.equal(x.view(torch.int16), y.view(torch.int16))
+
+
+def run(dev, tokens, Hkv, d, P, keep, recent, in_place, weights=None, seed=0, same_w=False):
+    batch = R.Batch(dev, tokens, [0] * len(tokens), Hkv, Hkv, d, P, seed=seed)
+    pages_out = [-(-min(t, keep) // P) for t in tokens]
+    dst = batch.table.clone()
+    if not in_place:  # pages of their own behind the batch's
+        grow = sum(pages_out)
+        for name in ("k", "v"):
+            c = getattr(batch, name)
+            more = torch.full((grow, Hkv, P, d), 3.0, dtype=torch.bfloat16)
+            setattr(batch, name, torch.cat([c, more]))
+        dst.fill_(-1)
+        order = torch.randperm(grow, generator=batch.gen) + batch.n_phys
+        at = 0
+        for b, n in enumerate(pages_out):
+            dst[b, :n] = order[at:at + n].to(torch.int32)
+            at += n
+        batch.n_phys += grow
+    kv = batch.to_device()
+    slots = batch.max_pages * P
+    w = torch.rand((batch.B, Hkv, slots), generator=batch.gen) if weights is None else \
+        weights(batch, slots)
+    for b, t in enumerate(tokens):
+        w[b, :, t:] = math.nan  # not read
+    w_dev = guards.guarded_like(w.to(dev), "weights")
+    w_out = w_dev if same_w else guards.guarded(w.shape, torch.float32, dev, fill=5.0, what="w_out")
+    kept = guards.guarded((batch.B, Hkv, keep), torch.int32, dev, fill=-3, what="kept")
+    lens = guards.guarded((batch.B,), torch.int32, dev, fill=-3, what="new_lens")
+    dst_dev = batch.table_dev if in_place else dst.to(dev)
+    B.asp_weight_evict(kv, w_dev, keep, recent, dst_dev, w_out, kept, lens, batch.ws)
+    assert B.asp_get_device_error(batch.ws) == 0
+    # the definition
+    k_want, v_want = batch.k.clone(), batch.v.clone()
+    summ_want = torch.zeros_like(batch.summ_dev).cpu()
+    w_want = w.clone() if same_w else torch.full_like(w, 5.0)
+    kept_want = torch.full_like(kept, -3).cpu()
+    for b, t in enumerate(tokens):
+        n = min(t, keep)
+        k_rows, v_rows = batch.rows(batch.k, b), batch.rows(batch.v, b)
+        for h in range(Hkv):
+            ids = torch.tensor(R.evict_ids(w[b, h], t, keep, recent), dtype=torch.long)
+            kept_want[b, h, :n] = ids.to(torch.int32)
+            w_want[b, h, :n] = w[b, h][ids]
+            i = torch.arange(n)
+            pages = dst[b, i // P].long()
+            k_want[pages, h, i % P] = k_rows[ids, h]
+            v_want[pages, h, i % P] = v_rows[ids, h]
+            for p in range(-(-n // P)):
+                part = k_rows[ids, h][p * P:(p + 1) * P].float()
+                summ_want[b, h, p, 0], summ_want[b, h, p, 1] = part.amin(0), part.amax(0)
+    assert lens.tolist() == [min(t, keep) for t in tokens]
+    assert torch.equal(kept.cpu(), kept_want), "kept"
+    assert torch.equal(w_out.cpu().view(torch.int32), w_want.view(torch.int32)), "weights"
+    assert same(batch.k_dev.cpu(), k_want), "k"
+    assert same(batch.v_dev.cpu(), v_want), "v"
+    assert torch.equal(batch.summ_dev.cpu(), summ_want), "summaries"
+
+
+@pytest.mark.parametrize("Hkv,d,P", [(2, 64, 16), (8, 128, 16), (1, 128, 64), (4, 64, 32),
+                                     (2, 64, 64), (2, 128, 32)])
+@pytest.mark.parametrize("tokens,keep,recent", [
+    ([1], 1, 0), ([300, 0, 17, 256], 100, 16), ([2049, 900, 128], 600, 600),
+    ([1500, 1499], 1498, 0), ([700], 1, 1), ([130, 64], 700, 3)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_shapes(cuda_device, Hkv, d, P, tokens, keep, recent, in_place):
+    keep = min(keep, -(-max(tokens) // P) * P)
+    run(cuda_device, tokens, Hkv, d, P, keep, min(recent, keep), in_place, seed=keep,
+        same_w=in_place)
+
+
+@pytest.mark.parametrize("kind", ["equal", "zeros", "few values", "signed zeros", "special", "spread",
+                                  "ascending", "descending"])
+@pytest.mark.parametrize("T", [1000, 5000])
+def test_weights_that_tie_or_stretch(cuda_device, kind, T):
+    def weights(batch, slots):
+        u = torch.rand((batch.B, batch.Hkv, slots), generator=batch.gen)
+        if kind == "equal":
+            return torch.full_like(u, 0.25)
+        if kind == "zeros":
+            return torch.where(u < 0.1, u, torch.zeros_like(u))
+        if kind == "few values":
+            return (u * 4).floor()
+        if kind == "signed zeros":
+            return torch.where(u < 0.5, torch.zeros_like(u), -torch.zeros_like(u))
+        if kind == "special":
+            w = torch.randn((batch.B, batch.Hkv, slots), generator=batch.gen)
+            w[u < 0.3] = math.nan
+            w[(u > 0.3) & (u < 0.4)] = math.inf
+            w[(u > 0.4) & (u < 0.5)] = -math.inf
+            return w
+        if kind == "spread":
+            return torch.exp(60 * (u - 0.5))
+        line = torch.arange(slots, dtype=torch.float32).expand_as(u)
+        return (line if kind == "ascending" else slots - line).contiguous()
+    for in_place in (False, True):
+        run(cuda_device, [T, T // 2 + 7], 2, 64, 16, T // 3, 33, in_place, weights, seed=T,
+            same_w=not in_place)
+
+
+def test_long_segments(cuda_device):
+    run(cuda_device, [40000, 70001], 1, 64, 16, 30000, 1024, True, seed=3)
+    run(cuda_device, [40000, 70001], 1, 64, 64, 39999, 5, False, seed=4)
+
+
+def test_many_segments(cuda_device):
+    tokens = [20 + (i * 13) % 150 for i in range(150)]
+    run(cuda_device, tokens, 8, 64, 16, 64, 10, True, seed=5)
+
+
+def test_bad_pages(cuda_device):
+    batch = R.Batch(cuda_device, [200], [0], 2, 2, 64, 16, seed=6)
+    kv = batch.to_device()
+    w = torch.rand((1, 2, batch.max_pages * 16), device=cuda_device)
+    kept = torch.zeros((1, 2, 100), dtype=torch.int32, device=cuda_device)
+    lens = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    batch.table_dev[0, 5] = -1
+    B.asp_weight_evict(kv, w, 100, 100, batch.table_dev, w, kept, lens, batch.ws)
+    assert B.asp_get_device_error(batch.ws) == B.ASP_DEVERR_PAGE_RANGE
+    assert kept[0, 0].tolist() == list(range(100, 200))
+
+
+def test_graph_replay(cuda_device):
+    """Into other pages the call can be repeated: a graph of it, replayed, leaves the same."""
+    batch = R.Batch(cuda_device, [500, 300], [0, 0], 2, 2, 64, 16, seed=7, max_pages=64)
+    dst = torch.arange(batch.n_phys, batch.n_phys + 2 * 13, dtype=torch.int32)
+    for name in ("k", "v"):
+        c = getattr(batch, name)
+        setattr(batch, name, torch.cat([c, torch.zeros((26, 2, 16, 64), dtype=torch.bfloat16)]))
+    batch.n_phys += 26
+    kv = batch.to_device()
+    table = torch.full((2, 64), -1, dtype=torch.int32, device=cuda_device)
+    table[:, :13] = dst.view(2, 13).to(cuda_device)
+    w = torch.rand((2, 2, 64 * 16), device=cuda_device)
+    w_out = torch.zeros_like(w)
+    kept = torch.zeros((2, 2, 200), dtype=torch.int32, device=cuda_device)
+    lens = torch.zeros(2, dtype=torch.int32, device=cuda_device)
+    args = (kv, w, 200, 50, table, w_out, kept, lens, batch.ws)
+    B.asp_weight_evict(*args)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (batch.k_dev, batch.v_dev, batch.summ_dev, w_out, kept, lens)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.asp_weight_evict(*args)
+    for t in (w_out, kept, lens, batch.summ_dev):
+        t.zero_()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    for x, y in zip(want, (batch.k_dev, batch.v_dev, batch.summ_dev, w_out, kept, lens)):
+        assert torch.equal(x.nan_to_num(7), y.nan_to_num(7)) if x.is_floating_point() else torch.equal(x, y)
