@@ -46,6 +46,7 @@ def build(verbose: bool = False, force: bool = False) -> str:
     nvcc = _nvcc()
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
     deps = srcs + [os.path.join(CSRC, "asp_internal.cuh"), os.path.join(CSRC, "score_common.cuh"),
+                   os.path.join(CSRC, "tc.cuh"), os.path.join(CSRC, "chunk_plan.cuh"),
                    os.path.join(INCLUDE, "asp.h"), os.path.abspath(__file__)]
     if not force and os.path.exists(LIB_PATH):
         built = os.path.getmtime(LIB_PATH)

@@ -309,8 +309,11 @@ asp_status asp_chunk_attention(const asp_paged_kv* kv, const uint16_t* q,
   WsLayout lay;
   if ((st = check_ws(kv, ws, ws_bytes, &lay)) != ASP_OK) return st;
   if (num_tokens == 0) return ASP_OK;
+  uint8_t* w = static_cast<uint8_t*>(ws);
   ChunkAttentionArgs a{kv, q, q_offsets, num_tokens, sm_scale, out, lse,
-                       static_cast<uint32_t*>(ws)};
+                       reinterpret_cast<ChunkJoin*>(w + lay.joins_off),
+                       reinterpret_cast<float*>(w + lay.chunk_off), reinterpret_cast<uint32_t*>(w),
+                       current_device_sm_count()};
   return from_cuda(launch_chunk_attention(a, static_cast<cudaStream_t>(stream)));
 }
 

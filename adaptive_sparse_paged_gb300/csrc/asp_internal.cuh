@@ -44,18 +44,33 @@ constexpr int kMaxGroup = 8;           // query heads per KV head (padded mma wi
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // a bounded on-chip wait gives up after 2 s
 
 // ----------------------------------------------------------------- workspace
-// [ header 256 B | arrivals int32[S] | scores f32[S*max_pages] | partials ]
+// [ header 256 B | arrivals int32[S] | scores f32[S*max_pages] | partials |
+//   chunk joins | chunk partials ]
 // arrivals[s] counts the decode CTAs done with split segment s; the CTA that
 // completes it merges s and puts the count back to zero.
-// header word 0 is the sticky device error mask.
+// header word 0 is the sticky device error mask. A CTA of the chunk attention
+// leaves at most two partials (its first and its last piece), of up to
+// kChunkRows query rows each, and at most one join: where the pieces of the
+// item that its last piece begins lie.
+constexpr int kChunkRows = 256;
+struct ChunkJoin {
+  int b, h, qt, pieces;  // pieces 0: no item begins here that other CTAs end
+};
 struct WsLayout {
   size_t arrivals_off = 0;
   size_t scores_off = 0;
   size_t partials_off = 0;
+  size_t joins_off = 0;
+  size_t chunk_off = 0;
   size_t total = 0;
   int decode_grid = 0;   // CTAs of the decode kernel
   int slot_floats = 0;   // floats per partial slot: m[8], l[8], o[8][d]
 };
+
+// floats of one chunk partial: m[kChunkRows], l[kChunkRows], o[kChunkRows][d]
+__host__ __device__ inline size_t chunk_slot_floats(int head_dim) {
+  return size_t(kChunkRows) * (2 + head_dim);
+}
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -67,8 +82,11 @@ inline WsLayout ws_layout(const asp_paged_kv& kv, int num_sms) {
   w.arrivals_off = 256;
   w.scores_off = align256(w.arrivals_off + S * sizeof(int32_t));
   w.partials_off = align256(w.scores_off + S * size_t(kv.max_pages) * sizeof(float));
-  w.total = align256(w.partials_off +
-                     (S + size_t(w.decode_grid)) * size_t(w.slot_floats) * sizeof(float));
+  w.joins_off = align256(w.partials_off +
+                         (S + size_t(w.decode_grid)) * size_t(w.slot_floats) * sizeof(float));
+  w.chunk_off = align256(w.joins_off + size_t(num_sms) * sizeof(ChunkJoin));
+  w.total = align256(w.chunk_off + 2 * size_t(num_sms) * chunk_slot_floats(kv.head_dim) *
+                                       sizeof(float));
   return w;
 }
 
@@ -425,7 +443,10 @@ struct ChunkAttentionArgs {
   float sm_scale;
   uint16_t* out;
   float* lse;
+  ChunkJoin* joins;
+  float* partials;
   uint32_t* err;
+  int num_sms;
 };
 cudaError_t launch_chunk_attention(const ChunkAttentionArgs& a, cudaStream_t stream);
 
@@ -463,6 +484,10 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 // fill out of bounds (decode.cu). box_inner * 2 must be 128.
 cudaError_t encode_bf16_2d_swizzled(CUtensorMap* map, const void* base, unsigned long long inner,
                                     unsigned long long rows, unsigned box_inner, unsigned box_rows);
+// The same over a dense [outer, mid, inner] tensor.
+cudaError_t encode_bf16_3d_swizzled(CUtensorMap* map, const void* base, unsigned long long inner,
+                                    unsigned long long mid, unsigned long long outer,
+                                    unsigned box_inner, unsigned box_mid, unsigned box_outer);
 
 // Per-device helpers (abi.cu).
 int current_device_sm_count();
