@@ -329,8 +329,11 @@ asp_status asp_chunk_weights(const asp_paged_kv* kv, const uint16_t* q, const in
   if ((st = check_weights(sm_scale, decay, w_in, w_out)) != ASP_OK) return st;
   WsLayout lay;
   if ((st = check_ws(kv, ws, ws_bytes, &lay)) != ASP_OK) return st;
+  uint8_t* w = static_cast<uint8_t*>(ws);
   WeightArgs a{kv, q, q_offsets, num_tokens, nullptr, nullptr, nullptr, lse, sm_scale, decay,
-               w_in, w_out, static_cast<uint32_t*>(ws)};
+               w_in, w_out, reinterpret_cast<ChunkJoin*>(w + lay.joins_off),
+               reinterpret_cast<float*>(w + lay.chunk_off), reinterpret_cast<uint32_t*>(w),
+               current_device_sm_count()};
   return from_cuda(launch_chunk_weights(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -347,7 +350,7 @@ asp_status asp_decode_weights(const asp_paged_kv* kv, const float* q, const int3
   WsLayout lay;
   if ((st = check_ws(kv, ws, ws_bytes, &lay)) != ASP_OK) return st;
   WeightArgs a{kv, nullptr, nullptr, kv->batch, q, lists, lens, lse, sm_scale, decay, w_in, w_out,
-               static_cast<uint32_t*>(ws)};
+               nullptr, nullptr, static_cast<uint32_t*>(ws), current_device_sm_count()};
   return from_cuda(launch_decode_weights(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -54,7 +54,7 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // a bounded on-chip wait give
 // item that its last piece begins lie.
 constexpr int kChunkRows = 256;
 struct ChunkJoin {
-  int b, h, qt, pieces;  // pieces 0: no item begins here that other CTAs end
+  int b, h, item, pieces;  // pieces 0: no item begins here that other CTAs end
 };
 struct WsLayout {
   size_t arrivals_off = 0;
@@ -462,7 +462,10 @@ struct WeightArgs {
   float sm_scale, decay;
   const float* w_in;           // null: no weight before this call
   float* w_out;
+  ChunkJoin* joins;            // chunk form
+  float* partials;
   uint32_t* err;
+  int num_sms;
 };
 cudaError_t launch_chunk_weights(const WeightArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_weights(const WeightArgs& a, cudaStream_t stream);

@@ -58,6 +58,22 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= 512, "the tail of the dynamic shared memory");
 
+// The current piece's tokens of the chunk, [tok0, last), and the units that its
+// two tiles of rows need.
+struct Piece {
+  int tok0, last, n[2];
+  __device__ __forceinline__ Piece(const ChunkWalk<RowCut>& w, int tile_tokens) {
+    tok0 = w.item * 2 * tile_tokens;
+    last = min(w.r.n, tok0 + 2 * tile_tokens);
+    for (int t = 0; t < 2; ++t) {
+      const int end = min(last, tok0 + (t + 1) * tile_tokens);
+      n[t] = end > tok0 + t * tile_tokens
+                 ? max(0, min(w.u1, RowCut::units_to(w.r, end - 1)) - w.u0)
+                 : 0;
+    }
+  }
+};
+
 struct Params {
   ChunkDims c;
   const int32_t* bt;
@@ -109,9 +125,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   pdl_wait_predecessor();
   const uint32_t tmem = sh.tmem;
-  chunk_plan(p.c, &sh.start, sh.scratch, p.err);
-  ChunkWalk walk(p.c, sh.start);
-  const int g = p.c.g, tile_tokens = 128 / g;
+  chunk_plan<RowCut>(p.c, &sh.start, sh.scratch, p.err);
+  ChunkWalk<RowCut> walk(p.c, sh.start);
+  const int g = p.c.g, tile_tokens = kTileRows / g;
   auto fail = [&] {
     report(p.err, ASP_DEVERR_TIMEOUT);
     *(volatile int*)&sh.failed = 1;
@@ -132,10 +148,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t masks = 0;
     for (; ok && walk.more(); walk.next(), ++piece) {
-      const int last = walk.tok0 + walk.ntok;
-      const int n = max(walk.units_for(walk.tok0, min(last, walk.tok0 + tile_tokens)),
-                        walk.units_for(walk.tok0 + tile_tokens, last));
-      const bool two = walk.ntok > tile_tokens;
+      const Piece pc(walk, tile_tokens);
+      const int n = max(pc.n[0], pc.n[1]);
+      const bool two = pc.last - pc.tok0 > tile_tokens;
       ok = __all_sync(kFull, mbar_wait(&sh.q_empty, (piece & 1) ^ 1));
       if (!ok) break;
       if (lane == 0) {
@@ -143,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < (two ? 2 : 1); ++t)
           for (int hf = 0; hf < C::kHalves; ++hf)
             tma_load_3d(q_tiles + t * C::kTileBytes + hf * 16384, &tmQ, hf * 64, walk.h * g,
-                        walk.r.row0 + walk.tok0 + t * tile_tokens, &sh.q_full);
+                        walk.r.row0 + pc.tok0 + t * tile_tokens, &sh.q_full);
       }
       const int n_pages = ceil_div(walk.r.T, P);
       const int32_t* bt = p.bt + (size_t)walk.b * p.c.max_pages;
@@ -208,17 +223,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                  smem_desc(r0 + st * C::kTileBytes + k * 2048, 16384), kDescO, add || k > 0);
       };
       for (; ok && walk.more(); walk.next(), ++piece) {
-        const int last = walk.tok0 + walk.ntok;
-        const int nt[2] = {walk.units_for(walk.tok0, min(last, walk.tok0 + tile_tokens)),
-                           walk.units_for(walk.tok0 + tile_tokens, last)};
-        const int n = max(nt[0], nt[1]);
+        const Piece pc(walk, tile_tokens);
+        const int n = max(pc.n[0], pc.n[1]);
         uint32_t st = tile % C::kStages;
         ok = mbar_wait(&sh.q_full, piece & 1) &&
              mbar_wait(&sh.full[st], (tile / C::kStages) & 1);
         if (!ok) break;
         tc_fence_after();
         for (int t = 0; t < 2; ++t)
-          if (nt[t] > 0) product_s(t, st);
+          if (pc.n[t] > 0) product_s(t, st);
         mma_commit(&sh.empty[st]);
         if (n == 1) mma_commit(&sh.q_empty);
         for (int j = 0; j < n; ++j, tile += 2) {
@@ -226,13 +239,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait(&sh.full[sv], ((tile + 1) / C::kStages) & 1);
           if (ok && j + 1 < n) ok = mbar_wait(&sh.full[sk], ((tile + 2) / C::kStages) & 1);
           for (int t = 0; t < 2 && ok; ++t) {
-            if (j >= nt[t]) continue;
+            if (j >= pc.n[t]) continue;
             ok = mbar_wait(&sh.p_full[t], np[t] & 1);
             ++np[t];
             if (!ok) break;
             tc_fence_after();
             product_o(t, sv, j > 0);
-            if (j + 1 < nt[t]) product_s(t, sk);
+            if (j + 1 < pc.n[t]) product_s(t, sk);
             else mma_commit(&sh.o_full[t]);
           }
           if (!ok) break;
@@ -257,13 +270,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     if (tid == 0) p.joins[blockIdx.x].pieces = 0;
     for (; ok && walk.more(); walk.next()) {
-      const int last = walk.tok0 + walk.ntok;
-      const int n0 = walk.units_for(walk.tok0, min(last, walk.tok0 + tile_tokens));
-      const int n1 = walk.units_for(walk.tok0 + tile_tokens, last);
-      const int n = t == 0 ? n0 : n1;
-      const int tok = walk.tok0 + t * tile_tokens + row / g;
+      const Piece pc(walk, tile_tokens);
+      const int n = pc.n[t];
+      const int tok = pc.tok0 + t * tile_tokens + row / g;
       // rows past the item's last take any slot that keeps them off the masked path
-      const bool mine = tok < last;
+      const bool mine = tok < pc.last;
       const int pos = mine ? walk.r.T - walk.r.n + tok : walk.r.T - 1;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
@@ -354,9 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sh.p_full[t]);
       }
       if (!ok) break;
-      units_seen += max(n0, n1);
+      units_seen += max(pc.n[0], pc.n[1]);
       // ---- the piece's end: the whole item goes out, a part of it into the workspace
-      const bool whole = walk.u0 == 0 && walk.u1 == walk.units;
+      const bool whole = walk.whole();
       if (n > 0) {
         ok = __all_sync(kFull, mbar_wait(&sh.o_full[t], phase_o & 1));
         if (!ok) break;
@@ -411,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (tid == 0 && walk.u0 == 0) {
           const int end = chunk_share_of(sh.start.total, gridDim.x, walk.at + walk.units - 1);
-          p.joins[blockIdx.x] = ChunkJoin{walk.b, walk.h, walk.qt, end - (int)blockIdx.x + 1};
+          p.joins[blockIdx.x] = ChunkJoin{walk.b, walk.h, walk.item, end - (int)blockIdx.x + 1};
         }
       }
       tc_fence_before();  // the next piece's first product writes O after the next P arrives
@@ -432,12 +443,12 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const Params p) {
   const ChunkJoin jn = p.joins[blockIdx.x];
   if (jn.pieces < 2) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = p.c.g, tpi = kItemRows / g;
+  const int g = p.c.g, tpi = kChunkRows / g;
   const ChunkRequest r = chunk_request(p.c, jn.b, nullptr);
   const size_t slot_floats = chunk_slot_floats(D);
   for (int i = 0; i < 4; ++i) {
     const int row = blockIdx.y * 32 + i * 8 + warp;
-    const int tok = jn.qt * tpi + row / g;
+    const int tok = jn.item * tpi + row / g;
     if (tok >= r.n) return;
     const float* first = p.partials + (size_t)(2 * blockIdx.x + 1) * slot_floats;
     const float* rest = p.partials + (size_t)(2 * blockIdx.x) * slot_floats;

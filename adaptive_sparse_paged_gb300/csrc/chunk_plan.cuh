@@ -1,12 +1,14 @@
-// chunk_plan.cuh - how a packed batch of new tokens is cut into tiles and
-// shared out over the CTAs, on the device: the host knows neither lengths nor
-// offsets, so a call can be captured and replayed as they change.
+// chunk_plan.cuh - how the work on a packed batch of new tokens is cut into
+// items and units and shared out over the CTAs, on the device: the host knows
+// neither lengths nor offsets, so a call can be captured and replayed as they
+// change.
 //
-// An item is (request, KV head, up to 256 query rows); a row is one
-// (token, head of the group), token-major, so an item holds 256 / g tokens. A
-// unit is one item against one tile of 128 keys; causality gives the item
-// (t_last / 128 + 1) units. The items in order (request, head, tile) form one
-// sequence of units, of which every CTA takes an equal, contiguous share.
+// A cut says how many items a head of a request has and how many units an item:
+//   RowCut   item: up to 256 query rows, a row being one (token, head of the
+//            group), token-major; unit: those rows against 128 keys that they see.
+//   KeyCut   item: 128 keys; unit: those keys against 128 query rows.
+// The items in order (request, head, item) form one sequence of units, of which
+// every CTA takes an equal, contiguous share.
 #pragma once
 
 #include "asp_internal.cuh"
@@ -14,7 +16,7 @@
 namespace asp {
 
 constexpr int kTileKeys = 128;
-constexpr int kItemRows = kChunkRows;
+constexpr int kTileRows = 128;
 
 struct ChunkDims {
   const int32_t* q_offsets;
@@ -22,7 +24,7 @@ struct ChunkDims {
   int B, Hkv, g, max_pages, P, num_tokens;
 };
 
-// One request: its rows and its tokens.
+// One request: its tokens, and its rows.
 struct ChunkRequest {
   int T, n, row0;
 };
@@ -31,36 +33,70 @@ __device__ __forceinline__ ChunkRequest chunk_request(const ChunkDims& c, int b,
   const NewRows r = new_rows(c.q_offsets, b, T, c.num_tokens, err);
   return ChunkRequest{T, r.n, r.row0};
 }
-__device__ __forceinline__ int chunk_items(const ChunkRequest& r, int tokens_per_item) {
-  return ceil_div(r.n, tokens_per_item);
-}
-// Units of the item whose last token is `last` (counted in the chunk).
-__device__ __forceinline__ int chunk_units(const ChunkRequest& r, int last) {
-  return (r.T - r.n + last) / kTileKeys + 1;
-}
-// Units of a head's first m items.
-__device__ __forceinline__ long long chunk_units_before(const ChunkRequest& r, int tpi, int m) {
-  const int items = chunk_items(r, tpi);
-  long long sum = 0;
-  const int whole = m < items ? m : items - 1;  // items that end on their last possible token
-  if (whole > 0) {
-    // item i of them has floor((a + tpi (i + 1) - 1) / 128) + 1 units; the floors
-    // repeat, plus one, every `period` items
-    const int a = r.T - r.n, period = tpi < kTileKeys ? kTileKeys / tpi : 1;
-    const int step = tpi < kTileKeys ? 1 : tpi / kTileKeys;
-    for (int s = 0; s < period; ++s) {
-      const long long cnt = (whole - s + period - 1) / period;
-      if (cnt <= 0) break;
-      sum += cnt * ((a + tpi * (s + 1) - 1) / kTileKeys + 1) + step * cnt * (cnt - 1) / 2;
-    }
-  }
-  if (m == items && items > 0) sum += chunk_units(r, r.n - 1);
-  return sum;
-}
 
-// Where a CTA's share begins: item (b, h, qt), its unit `u`; and how many units it takes.
+struct RowCut {
+  // Units of rows whose last token is `last` (counted in the chunk).
+  static __device__ __forceinline__ int units_to(const ChunkRequest& r, int last) {
+    return (r.T - r.n + last) / kTileKeys + 1;
+  }
+  static __device__ __forceinline__ int items(const ChunkRequest& r, int g) {
+    return ceil_div(r.n, kChunkRows / g);
+  }
+  static __device__ __forceinline__ int units(const ChunkRequest& r, int g, int item) {
+    return units_to(r, min(r.n, (item + 1) * (kChunkRows / g)) - 1);
+  }
+  // Units of a head's first m items.
+  static __device__ __forceinline__ long long before(const ChunkRequest& r, int g, int m) {
+    const int tpi = kChunkRows / g, all = items(r, g);
+    const int whole = m < all ? m : all - 1;  // items that end on their last possible token
+    long long sum = 0;
+    if (whole > 0) {
+      // item i of them has floor((a + tpi (i + 1) - 1) / 128) + 1 units; the floors
+      // repeat, plus `step`, every `period` items
+      const int a = r.T - r.n, period = tpi < kTileKeys ? kTileKeys / tpi : 1;
+      const int step = tpi < kTileKeys ? 1 : tpi / kTileKeys;
+      for (int s = 0; s < period; ++s) {
+        const long long cnt = (whole - s + period - 1) / period;
+        if (cnt <= 0) break;
+        sum += cnt * ((a + tpi * (s + 1) - 1) / kTileKeys + 1) + step * cnt * (cnt - 1) / 2;
+      }
+    }
+    if (m == all && all > 0) sum += units_to(r, r.n - 1);
+    return sum;
+  }
+};
+
+struct KeyCut {
+  static __device__ __forceinline__ int items(const ChunkRequest& r, int) {
+    return ceil_div(r.T, kTileKeys);
+  }
+  // First tile of rows that sees a key of the item.
+  static __device__ __forceinline__ int first_tile(const ChunkRequest& r, int g, int item) {
+    return max(0, item * kTileKeys - (r.T - r.n)) / (kTileRows / g);
+  }
+  static __device__ __forceinline__ int tiles(const ChunkRequest& r, int g) {
+    return ceil_div(r.n, kTileRows / g);
+  }
+  // A request without new rows still has its weights carried over: one empty unit.
+  static __device__ __forceinline__ int units(const ChunkRequest& r, int g, int item) {
+    return r.n == 0 ? 1 : tiles(r, g) - first_tile(r, g, item);
+  }
+  static __device__ __forceinline__ long long before(const ChunkRequest& r, int g, int m) {
+    if (r.n == 0) return m;
+    const int a = r.T - r.n, nq = tiles(r, g);
+    const int full = min(m, a / kTileKeys + 1);  // items that every tile of rows sees
+    long long sum = (long long)full * nq;
+    const long long cut = m - full;              // the others: g tiles fewer each time
+    if (cut > 0)
+      sum += cut * (nq - (kTileKeys * (a / kTileKeys + 1) - a) / (kTileRows / g)) -
+             g * (cut * (cut - 1) / 2);
+    return sum;
+  }
+};
+
+// Where a CTA's share begins: unit `u` of item (b, h, item); and the share.
 struct ChunkStart {
-  int b, h, qt, u;
+  int b, h, item, u;
   long long first, count, total;
 };
 
@@ -76,15 +112,15 @@ __device__ __forceinline__ int chunk_share_of(long long total, int G, long long 
 
 // Fills *start (shared memory) for this CTA; every thread of the block calls it.
 // scratch: one long long for each warp.
+template <typename Cut>
 __device__ __forceinline__ void chunk_plan(const ChunkDims& c, ChunkStart* start, long long* scratch,
                                            uint32_t* err) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  const int tpi = kItemRows / c.g;
   const int per = ceil_div(c.B, nt), b0 = min(c.B, tid * per), b1 = min(c.B, b0 + per);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     const ChunkRequest r = chunk_request(c, b, blockIdx.x == 0 ? err : nullptr);
-    mine += (long long)c.Hkv * chunk_units_before(r, tpi, chunk_items(r, tpi));
+    mine += (long long)c.Hkv * Cut::before(r, c.g, Cut::items(r, c.g));
   }
   long long x = mine;
 #pragma unroll
@@ -107,8 +143,8 @@ __device__ __forceinline__ void chunk_plan(const ChunkDims& c, ChunkStart* start
     long long at = before;
     for (int b = b0; b < b1; ++b) {
       const ChunkRequest r = chunk_request(c, b, nullptr);
-      const int items = chunk_items(r, tpi);
-      const long long head = chunk_units_before(r, tpi, items);
+      const int items = Cut::items(r, c.g);
+      const long long head = Cut::before(r, c.g, items);
       if (first >= at + c.Hkv * head) {
         at += c.Hkv * head;
         continue;
@@ -119,9 +155,9 @@ __device__ __forceinline__ void chunk_plan(const ChunkDims& c, ChunkStart* start
       int lo = 0, hi = items - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (chunk_units_before(r, tpi, mid) <= in_h) lo = mid; else hi = mid - 1;
+        if (Cut::before(r, c.g, mid) <= in_h) lo = mid; else hi = mid - 1;
       }
-      *start = ChunkStart{b, h, lo, (int)(in_h - chunk_units_before(r, tpi, lo)), first, count, total};
+      *start = ChunkStart{b, h, lo, (int)(in_h - Cut::before(r, c.g, lo)), first, count, total};
       break;
     }
   }
@@ -129,54 +165,48 @@ __device__ __forceinline__ void chunk_plan(const ChunkDims& c, ChunkStart* start
 }
 
 // Walks a CTA's pieces: piece = units [u0, u1) of one item.
+template <typename Cut>
 struct ChunkWalk {
-  ChunkDims c;
+  const ChunkDims& c;
   ChunkRequest r;
   long long left, at;   // units still to take, global index of the piece's first unit
-  int b, h, qt, tpi, items;
+  int b, h, item, items;
   int u0, u1, units;    // the piece, and the whole item's units
-  int tok0, ntok;       // the item's first token of the chunk, and its tokens
 
   __device__ __forceinline__ ChunkWalk(const ChunkDims& dims, const ChunkStart& s)
-      : c(dims), left(s.count), at(s.first), b(s.b), h(s.h), qt(s.qt), tpi(kItemRows / dims.g) {
+      : c(dims), left(s.count), at(s.first), b(s.b), h(s.h), item(s.item) {
     if (left <= 0) return;
     r = chunk_request(c, b, nullptr);
-    items = chunk_items(r, tpi);
+    items = Cut::items(r, c.g);
     u0 = s.u;
     set();
   }
   __device__ __forceinline__ void set() {
-    tok0 = qt * tpi;
-    ntok = min(tpi, r.n - tok0);
-    units = chunk_units(r, tok0 + ntok - 1);
+    units = Cut::units(r, c.g, item);
     u1 = (int)min((long long)units, u0 + left);
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units; }
   __device__ __forceinline__ void next() {
     left -= u1 - u0;
     at += u1 - u0;
     if (left <= 0) return;
     u0 = 0;
-    if (++qt >= items) {
-      qt = 0;
+    if (++item >= items) {
+      item = 0;
       if (++h >= c.Hkv) {
         h = 0;
-        do {  // the total counts units that are still to come: some later request has rows
+        do {  // the total counts units that are still to come: some later request has items
           if (++b >= c.B) {
             left = 0;
             return;
           }
           r = chunk_request(c, b, nullptr);
-        } while (r.n == 0);
-        items = chunk_items(r, tpi);
+          items = Cut::items(r, c.g);
+        } while (items == 0);
       }
     }
     set();
-  }
-  // Units of this piece that the rows of tokens [t0, t1) of the chunk need.
-  __device__ __forceinline__ int units_for(int t0, int t1) const {
-    if (t1 <= t0) return 0;
-    return max(0, min(u1, chunk_units(r, t1 - 1)) - u0);
   }
 };
 

@@ -2,127 +2,781 @@
 // over query rows and over the query heads of its KV head:
 //   w_out[s] = decay * w_in[s] + sum_{t >= s} exp(c q_t.k_s - lse_t).
 //
-// One warp per cached token holds its key row (d / 32 channels a lane) and
-// walks the query rows that see it.
-#include "asp_internal.cuh"
+// The products run transposed on the tensor cores, S^T = K Q^T with 128 keys as
+// rows, so that a thread owns one key: its sum over the query rows needs no
+// exchange and no atomics, and comes out in a fixed order.
+//
+// Chunk form (chunk_weights_kernel): a persistent CTA per SM takes an equal share
+// of the units (128 keys x 128 query rows, chunk_plan.cuh); a key tile stays in
+// shared memory while the query tiles that see it stream past. Two warpgroups
+// take the products' results in turn, four of which are in tensor memory at
+// once. An item that several CTAs share leaves its partial sums in the
+// workspace; a second, small kernel adds them up.
+//
+// Decode form (decode_weights_kernel): one token a request, fp32 queries, page
+// lists. The keys are read once and the kernel is bound by HBM, so the tiles of
+// all lists form one sequence, two CTAs an SM take equal shares of it, and the
+// queries (at most 8 heads of a group, each as three bf16 terms that add up to
+// its 24 bits) ride along as 32 columns.
+#include "chunk_plan.cuh"
+#include "tc.cuh"
 
 namespace asp {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+constexpr float kLog2e = 1.4426950408889634f;
 
-struct Params {
-  const uint16_t* q;
-  const int32_t* q_offsets;
-  const float* q_f32;
-  const int32_t* lists;
-  const int32_t* lens;
+// ================================================================ chunk form
+constexpr int kThreads = 384;  // two summing warpgroups; loader, issuer, two idle warps
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kKeyBufs = 3, kRowBufs = 3, kSumBufs = 4;
+constexpr int kLseRing = 16;   // tiles of rows whose lse is kept: more than are in flight
+constexpr int kMaskRing = 16;
+constexpr uint32_t kTmemCols = 128 * kSumBufs;
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTileBytes = kHalves * 128 * 128;
+};
+
+struct ChunkShared {
+  float lse[kLseRing][kTileRows];  // -lse * log2(e); -inf: the row adds nothing
+  float acc[2][kTileKeys];
+  uint64_t k_full[kKeyBufs], k_empty[kKeyBufs], r_full[kRowBufs], r_empty[kRowBufs];
+  uint64_t s_full[kSumBufs], s_empty[kSumBufs], drain;
+  ChunkStart start;
+  long long scratch[kThreads / 32];
+  uint32_t page_mask[kMaskRing];
+  uint32_t row_flag[kLseRing];     // some row of the tile adds nothing
+  uint32_t tmem;
+};
+
+template <int D>
+constexpr size_t chunk_smem() {
+  return 1024 + (kKeyBufs + kRowBufs) * (size_t)Cfg<D>::kTileBytes + sizeof(ChunkShared);
+}
+
+struct ChunkParams {
+  ChunkDims c;
+  const int32_t* bt;
   const float* lse;
   const float* w_in;
   float* w_out;
-  const uint16_t* k;
-  const int32_t* bt;
-  const int32_t* seq_lens;
+  ChunkJoin* joins;
+  float* partials;
   uint32_t* err;
-  int B, Hq, Hkv, max_pages, num_phys, num_tokens;
-  float scale, decay;
+  int Hq, num_phys;
+  float scale_log2, decay;
 };
 
-template <int D, int P, bool Decode>
-__global__ void __launch_bounds__(256) weights_kernel(const Params p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  pdl_launch_dependents();
-  pdl_wait_predecessor();
-  const int seg = blockIdx.y, b = seg / p.Hkv, hk = seg % p.Hkv, g = p.Hq / p.Hkv;
-  const int T = clamp_seq_len(p.seq_lens[b], p.max_pages, P, p.err);
-  const NewRows nr = new_rows(Decode ? nullptr : p.q_offsets, b, T, p.num_tokens, p.err);
-  const size_t wbase = (size_t)seg * p.max_pages * P;
-  for (long long s = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); s < T;
-       s += (long long)gridDim.x * 8) {
-    const int page = (int)(s / P);
-    bool listed = true;
-    if (Decode && p.lists) {
-      const int N = ceil_div(T, P);
-      int len = p.lens[seg];
-      if (len < 0 || len > N) {
-        report(p.err, ASP_DEVERR_LEN_RANGE);
-        len = len < 0 ? 0 : N;
-      }
-      bool mine = false;
-      for (int i = lane; i < len; i += 32) {
-        const int e = p.lists[(size_t)seg * p.max_pages + i];
-        if (e < 0 || e >= N) report(p.err, ASP_DEVERR_LIST_RANGE);
-        mine |= e == page;
-      }
-      listed = __any_sync(kFull, mine);
+// Weight of slot s before the call: the chunk's own tokens had none.
+__device__ __forceinline__ float weight_before(const float* w_in, float decay, size_t at, int s,
+                                               int first_new) {
+  return w_in && s < first_new ? decay * w_in[at] : 0.f;
+}
+
+template <int D, int P>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_weights_kernel(const __grid_constant__ CUtensorMap tmQ,
+                         const __grid_constant__ CUtensorMap tmK, const ChunkParams p) {
+  using C = Cfg<D>;
+  constexpr int kPages = kTileKeys / P;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* keys = smem;
+  uint8_t* rows = smem + kKeyBufs * C::kTileBytes;
+  ChunkShared& sh = *reinterpret_cast<ChunkShared*>(rows + kRowBufs * C::kTileBytes);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kKeyBufs; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_empty[i], 1);
     }
-    float acc = 0.f;
-    if (listed) {
-      const int phys = p.bt[(size_t)b * p.max_pages + page];
-      if (phys < 0 || phys >= p.num_phys) {
-        report(p.err, ASP_DEVERR_PAGE_RANGE);
-      } else {
-        float k[E];
-        const __nv_bfloat16* kr = reinterpret_cast<const __nv_bfloat16*>(p.k) +
-                                  (((size_t)phys * p.Hkv + hk) * P + s % P) * D + lane * E;
+    for (int i = 0; i < kRowBufs; ++i) {
+      mbar_init(&sh.r_full[i], 1);
+      mbar_init(&sh.r_empty[i], 1);
+    }
+    for (int i = 0; i < kSumBufs; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_empty[i], 128);
+    }
+    mbar_init(&sh.drain, 1);
+    mbar_fence_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(&sh.tmem, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();  // the tensor memory is taken: the next kernel cannot take it first
+  pdl_wait_predecessor();
+  const uint32_t tmem = sh.tmem;
+  chunk_plan<KeyCut>(p.c, &sh.start, sh.scratch, p.err);
+  ChunkWalk<KeyCut> walk(p.c, sh.start);
+  const int g = p.c.g, tile_tokens = kTileRows / g;
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------ loader
+    if (lane == 0) {
+      prefetch_tensormap(&tmQ);
+      prefetch_tensormap(&tmK);
+    }
+    uint32_t kt = 0, rt = 0;  // key tiles, row tiles loaded so far
+    bool ok = true;
+    for (; ok && walk.more(); walk.next()) {
+      if (walk.r.n == 0) continue;
+      const uint32_t kb = kt % kKeyBufs;
+      ok = __all_sync(kFull, mbar_wait(&sh.k_empty[kb], ((kt / kKeyBufs) & 1) ^ 1));
+      if (!ok) break;
+      const int page = walk.item * kPages + lane;
+      const bool have = lane < kPages && page < ceil_div(walk.r.T, P);
+      const int phys = have ? p.bt[(size_t)walk.b * p.c.max_pages + page] : 0;
+      const bool good = have && phys >= 0 && phys < p.num_phys;
+      if (have && !good) report(p.err, ASP_DEVERR_PAGE_RANGE);
+      const uint32_t mask = __ballot_sync(kFull, good);
+      if (lane == 0) {
+        sh.page_mask[kt % kMaskRing] = mask;
+        const uint32_t bytes = __popc(mask) * (P * 128 * C::kHalves);
+        if (bytes) mbar_arrive_expect_tx(&sh.k_full[kb], bytes);
+        else mbar_arrive(&sh.k_full[kb]);
+      }
+      __syncwarp();
+      if (good) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) k[i] = __bfloat162float(kr[i]);
-        for (int i = max(0, (int)(s - (T - nr.n))); i < nr.n; ++i) {
-          for (int j = 0; j < g; ++j) {
-            const size_t r = (size_t)(nr.row0 + i) * p.Hq + hk * g + j;
-            float x = 0.f;
+        for (int hf = 0; hf < C::kHalves; ++hf)
+          tma_load_2d(keys + kb * C::kTileBytes + hf * 16384 + lane * P * 128, &tmK, hf * 64,
+                      (phys * p.c.Hkv + walk.h) * P, &sh.k_full[kb]);
+      }
+      ++kt;
+      const int tile0 = KeyCut::first_tile(walk.r, g, walk.item) + walk.u0;
+      for (int j = 0; j < walk.u1 - walk.u0; ++j, ++rt) {
+        const uint32_t rb = rt % kRowBufs;
+        const int tok0 = (tile0 + j) * tile_tokens;
+        // the rows' lse while the buffer drains
+        float nl[4];
+        bool none = false;
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-              x += k[e] * (Decode ? p.q_f32[r * D + lane * E + e]
-                                  : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.q)[r * D + lane * E + e]));
+        for (int i = 0; i < 4; ++i) {
+          const int r = lane * 4 + i, tok = tok0 + r / g;
+          const float l = tok < walk.r.n
+                              ? p.lse[(size_t)(walk.r.row0 + tok) * p.Hq + walk.h * g + r % g]
+                              : -INFINITY;
+          nl[i] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+          none |= l == -INFINITY;
+        }
+        ok = __all_sync(kFull, mbar_wait(&sh.r_empty[rb], ((rt / kRowBufs) & 1) ^ 1));
+        if (!ok) break;
+        *reinterpret_cast<float4*>(&sh.lse[rt % kLseRing][lane * 4]) =
+            make_float4(nl[0], nl[1], nl[2], nl[3]);
+        none = __any_sync(kFull, none);
+        if (lane == 0) {
+          sh.row_flag[rt % kLseRing] = none;
+          mbar_arrive_expect_tx(&sh.r_full[rb], C::kTileBytes);
+          for (int hf = 0; hf < C::kHalves; ++hf)
+            tma_load_3d(rows + rb * C::kTileBytes + hf * 16384, &tmQ, hf * 64, walk.h * g,
+                        walk.r.row0 + tok0, &sh.r_full[rb]);
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) {
+      report(p.err, ASP_DEVERR_TIMEOUT);
+      for (uint32_t t = kt > kKeyBufs ? kt - kKeyBufs : 0; t < kt; ++t)  // copies in flight end
+        mbar_wait(&sh.k_full[t % kKeyBufs], (t / kKeyBufs) & 1);
+      for (uint32_t t = rt > kRowBufs ? rt - kRowBufs : 0; t < rt; ++t)
+        mbar_wait(&sh.r_full[t % kRowBufs], (t / kRowBufs) & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      constexpr uint32_t kDesc = mma_desc(kTileKeys, kTileRows, false);
+      const uint32_t k0 = smem_u32(keys), r0 = smem_u32(rows);
+      uint32_t kt = 0, rt = 0;
+      bool ok = true;
+      for (; ok && walk.more(); walk.next()) {
+        if (walk.r.n == 0) continue;
+        const uint32_t kb = kt % kKeyBufs;
+        ok = mbar_wait(&sh.k_full[kb], (kt / kKeyBufs) & 1);
+        for (int j = 0; ok && j < walk.u1 - walk.u0; ++j, ++rt) {
+          const uint32_t rb = rt % kRowBufs, sb = rt % kSumBufs;
+          ok = mbar_wait(&sh.s_empty[sb], ((rt / kSumBufs) & 1) ^ 1) &&
+               mbar_wait(&sh.r_full[rb], (rt / kRowBufs) & 1);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
-            const float lse = p.lse[r];
-            if (lse != -INFINITY) acc += expf(x * p.scale - lse);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
+            mma_ss(tmem + sb * 128, smem_desc(k0 + kb * C::kTileBytes + off, 16),
+                   smem_desc(r0 + rb * C::kTileBytes + off, 16), kDesc, k > 0);
+          }
+          mma_commit(&sh.s_full[sb]);
+          mma_commit(&sh.r_empty[rb]);
+        }
+        mma_commit(&sh.k_empty[kb]);
+        ++kt;
+      }
+      if (!ok) report(p.err, ASP_DEVERR_TIMEOUT);
+      mma_commit(&sh.drain);  // no arrival is still on its way when the CTA ends
+      mbar_wait(&sh.drain, 0);
+    }
+    __syncwarp();
+  } else if (warp < kLoadWarp) {
+    // ------------------------------------------------------------ sums
+    const int wg = warp >> 2, row = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const float c = p.scale_log2;
+    uint32_t kt = 0, rt = 0, pieces = 0;
+    bool ok = true;
+    if (tid == 0) p.joins[blockIdx.x].pieces = 0;
+    for (; walk.more(); walk.next(), ++pieces) {
+      const int slot = walk.item * kTileKeys + row;
+      float sum = 0.f;
+      if (walk.r.n > 0) {
+        const int first_new = walk.r.T - walk.r.n;
+        const int tile0 = KeyCut::first_tile(walk.r, g, walk.item) + walk.u0;
+        const int steps = walk.u1 - walk.u0;
+        for (int j = 0; ok && j < steps; ++j, ++rt) {
+          if ((rt & 1) != (uint32_t)wg) continue;
+          const uint32_t sb = rt % kSumBufs;
+          ok = __all_sync(kFull, mbar_wait(&sh.s_full[sb], (rt / kSumBufs) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t s[4][32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(tmem + lanes + sb * 128 + 32 * i, s[i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_wait_ld(s[i]);
+          tc_fence_before();
+          mbar_arrive(&sh.s_empty[sb]);
+          const float* nl = sh.lse[rt % kLseRing];
+          // rows from `lo` on see this key
+          const int lo = (slot - first_new - (tile0 + j) * tile_tokens) * g;
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+          if (__any_sync(kFull, lo > 0) || sh.row_flag[rt % kLseRing]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float l = nl[32 * i + e];
+                const float x = ex2(fmaf(__uint_as_float(s[i][e]), c, l));
+                part[i] += 32 * i + e >= lo && l != -INFINITY ? x : 0.f;
+              }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                part[i] += ex2(fmaf(__uint_as_float(s[i][e]), c, nl[32 * i + e]));
+          }
+          sum += (part[0] + part[1]) + (part[2] + part[3]);
+        }
+        if (!((sh.page_mask[kt % kMaskRing] >> (row / P)) & 1)) sum = 0.f;
+        ++kt;
+      }
+      // the two warpgroups' halves: the second hands its own over
+      float* acc = sh.acc[pieces & 1];
+      if (wg == 1) acc[row] = sum;
+      named_bar_sync(1, 256);
+      if (wg == 0) {
+        sum += acc[row];
+        if (walk.whole()) {
+          if (slot < walk.r.T) {
+            const size_t at =
+                ((size_t)walk.b * p.c.Hkv + walk.h) * p.c.max_pages * P + slot;
+            p.w_out[at] =
+                weight_before(p.w_in, p.decay, at, slot, walk.r.T - walk.r.n) + sum;
+          }
+        } else {
+          p.partials[(size_t)(2 * blockIdx.x + (walk.u0 == 0 ? 1 : 0)) * kTileKeys + row] = sum;
+          if (tid == 0 && walk.u0 == 0) {
+            const int end = chunk_share_of(sh.start.total, gridDim.x, walk.at + walk.units - 1);
+            p.joins[blockIdx.x] =
+                ChunkJoin{walk.b, walk.h, walk.item, end - (int)blockIdx.x + 1};
           }
         }
       }
     }
-    if (lane == 0) {
-      const float before = p.w_in && s < T - nr.n ? p.decay * p.w_in[wbase + s] : 0.f;
-      p.w_out[wbase + s] = before + acc;
+    if (!ok && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_free(tmem, kTmemCols);
+}
+
+// Adds up the pieces of the item that CTA blockIdx.x began, in CTA order.
+__global__ void __launch_bounds__(kTileKeys) weights_join_kernel(const ChunkParams p) {
+  pdl_launch_dependents();
+  pdl_wait_predecessor();
+  const ChunkJoin jn = p.joins[blockIdx.x];
+  if (jn.pieces < 2) return;
+  const ChunkRequest r = chunk_request(p.c, jn.b, nullptr);
+  const int row = threadIdx.x, slot = jn.item * kTileKeys + row;
+  if (slot >= r.T) return;
+  float sum = p.partials[(size_t)(2 * blockIdx.x + 1) * kTileKeys + row];
+  for (int k = 1; k < jn.pieces; ++k)
+    sum += p.partials[(size_t)(2 * (blockIdx.x + k)) * kTileKeys + row];
+  const size_t at = ((size_t)jn.b * p.c.Hkv + jn.h) * p.c.max_pages * p.c.P + slot;
+  p.w_out[at] = weight_before(p.w_in, p.decay, at, slot, r.T - r.n) + sum;
+}
+
+template <int D, int P>
+cudaError_t launch_chunk_t(const WeightArgs& a, cudaStream_t stream) {
+  const asp_paged_kv& kv = *a.kv;
+  const int g = kv.num_q_heads / kv.num_kv_heads;
+  const unsigned long long cache_rows =
+      (unsigned long long)kv.num_phys_pages * kv.num_kv_heads * P;
+  CUtensorMap tq, tk;
+  // a call without rows reads none: its map only has to be valid
+  const int n = a.num_tokens > 0 ? a.num_tokens : 1;
+  const void* q = a.num_tokens > 0 ? (const void*)a.q : (const void*)kv.k_cache;
+  cudaError_t e =
+      encode_bf16_3d_swizzled(&tq, q, D, kv.num_q_heads, n, 64, g, kTileRows / g);
+  if (e != cudaSuccess) return e;
+  if ((e = encode_bf16_2d_swizzled(&tk, kv.k_cache, D, cache_rows, 64, P)) != cudaSuccess) return e;
+  ChunkParams p{{a.q_offsets, kv.seq_lens, kv.batch, kv.num_kv_heads, g, kv.max_pages, P,
+                 a.num_tokens},
+                kv.block_table, a.lse, a.w_in, a.w_out, a.joins, a.partials, a.err, kv.num_q_heads,
+                kv.num_phys_pages, a.sm_scale * kLog2e, a.decay};
+  constexpr size_t smem = chunk_smem<D>();
+  if ((e = set_max_dynamic_smem((const void*)chunk_weights_kernel<D, P>, (int)smem)) != cudaSuccess)
+    return e;
+  if ((e = set_max_dynamic_smem((const void*)weights_join_kernel, 0)) != cudaSuccess) return e;
+  e = launch_pdl(chunk_weights_kernel<D, P>, dim3(a.num_sms), dim3(kThreads), smem, stream, tq, tk,
+                 p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(weights_join_kernel, dim3(a.num_sms), dim3(kTileKeys), 0, stream, p);
+}
+
+// =============================================================== decode form
+constexpr int kDecThreads = 224;  // summing warpgroup; loader, issuer, query warp
+constexpr int kDecLoad = 4, kDecMma = 5, kDecQuery = 6;
+constexpr int kQueryRows = 24;    // 8 heads x (high, middle, low)
+constexpr int kQueryCols = 32;    // the products' width, a multiple of 16: the last 8 columns
+                                  // come from whatever lies behind the rows and are not read
+constexpr int kMetaRing = 16;     // key tiles whose pages are kept: more than are in flight
+constexpr int kDecCols = kQueryCols * kSumBufs;
+
+template <int D>
+struct DecCfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTileBytes = kHalves * 128 * 128;
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kQueryBytes = kHalves * kQueryRows * 128;
+};
+
+struct DecShared {
+  int page[kMetaRing][kTileKeys / 16];  // logical page of each listed page of the tile
+  float lse[2][kMaxGroup];              // -lse * log2(e) of the segment's heads
+  uint64_t full[6], empty[6], q_full[2], q_empty[2], l_empty[2];
+  uint64_t s_full[kSumBufs], s_empty[kSumBufs], drain;
+  int warp_sum[kDecThreads / 32];
+  int seg, tile;
+  uint32_t tmem;
+};
+constexpr int kNoPage = -1, kNotMapped = 1 << 30;
+
+template <int D>
+constexpr size_t decode_smem() {
+  using C = DecCfg<D>;
+  return 1024 + C::kStages * (size_t)C::kTileBytes + 2 * (size_t)C::kQueryBytes + sizeof(DecShared);
+}
+
+struct DecodeParams {
+  const float* q;
+  const int32_t* lists;  // null: every page
+  const int32_t* lens;
+  const float* lse;
+  const float* w_in;
+  float* w_out;
+  const int32_t* bt;
+  const int32_t* seq_lens;
+  uint32_t* err;
+  int B, Hq, Hkv, g, max_pages, num_phys;
+  float scale_log2, decay;
+};
+
+// Pages a segment's tiles run over.
+template <int P>
+__device__ __forceinline__ int listed_pages(const DecodeParams& p, int seg, int T, uint32_t* err) {
+  const int n = ceil_div(T, P);
+  if (!p.lens) return n;
+  const int len = p.lens[seg];
+  if (len < 0 || len > n) {
+    report(err, ASP_DEVERR_LEN_RANGE);
+    return len < 0 ? 0 : n;
+  }
+  return len;
+}
+
+// A CTA's tiles: segment by segment, each role walks them for itself.
+template <int P>
+struct DecodeWalk {
+  static constexpr int kPages = kTileKeys / P;
+  const DecodeParams& p;
+  int left, seg, tile, T, pages, tiles;
+  __device__ __forceinline__ DecodeWalk(const DecodeParams& prm, int count, int s, int t)
+      : p(prm), left(count), seg(s), tile(t) {
+    if (left > 0) load();
+  }
+  __device__ __forceinline__ void load() {
+    T = clamp_seq_len(p.seq_lens[seg / p.Hkv], p.max_pages, P, nullptr);
+    pages = listed_pages<P>(p, seg, T, nullptr);
+    tiles = ceil_div(pages, kPages);
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  // Tiles of the current segment that are this CTA's.
+  __device__ __forceinline__ int run() const { return min(left, tiles - tile); }
+  __device__ __forceinline__ void next_segment() {
+    left -= run();
+    tile = 0;
+    if (left <= 0) return;
+    do {  // the share ends in a later segment that has tiles
+      if (++seg >= p.B * p.Hkv) {
+        left = 0;
+        return;
+      }
+      load();
+    } while (tiles == 0);
+  }
+};
+
+template <int D, int P>
+__global__ void __launch_bounds__(kDecThreads, 2)
+    decode_weights_kernel(const __grid_constant__ CUtensorMap tmK, const DecodeParams p) {
+  using C = DecCfg<D>;
+  constexpr int kPages = kTileKeys / P;      // listed pages of a tile
+  constexpr int kBatch = 32 / kPages;        // tiles whose pages a warp looks up at once
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* queries = smem;  // before the ring: the products read 1 KiB past the rows
+  uint8_t* ring = smem + 2 * C::kQueryBytes;
+  DecShared& sh = *reinterpret_cast<DecShared*>(ring + C::kStages * C::kTileBytes);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.l_empty[i], 128);
+    }
+    for (int i = 0; i < kSumBufs; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_empty[i], 128);
+    }
+    mbar_init(&sh.drain, 1);
+    mbar_fence_init();
+  }
+  if (warp == kDecMma) tmem_alloc(&sh.tmem, kDecCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();  // the tensor memory is taken: the next kernel cannot take it first
+  pdl_wait_predecessor();
+  const uint32_t tmem = sh.tmem;
+
+  // ---- plan: tiles of all segments, an equal share for this CTA
+  const int S = p.B * p.Hkv;
+  const int per = ceil_div(S, kDecThreads), s0 = min(S, tid * per), s1 = min(S, s0 + per);
+  uint32_t* err0 = blockIdx.x == 0 ? p.err : nullptr;
+  int mine = 0;
+  for (int s = s0; s < s1; ++s) {
+    const int T = clamp_seq_len(p.seq_lens[s / p.Hkv], p.max_pages, P, err0);
+    mine += ceil_div(listed_pages<P>(p, s, T, err0), kPages);
+  }
+  int x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sh.warp_sum[warp] = x;
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int w = 0; w < kDecThreads / 32; ++w) {
+    if (w < warp) before += sh.warp_sum[w];
+    total += sh.warp_sum[w];
+  }
+  before += x - mine;
+  const EvenSplit split(total, gridDim.x);
+  const int first = split.begin(blockIdx.x), count = split.end(blockIdx.x) - first;
+  if (count > 0 && first >= before && first < before + mine) {
+    int at = before;
+    for (int s = s0; s < s1; ++s) {
+      const int T = clamp_seq_len(p.seq_lens[s / p.Hkv], p.max_pages, P, nullptr);
+      const int n = ceil_div(listed_pages<P>(p, s, T, nullptr), kPages);
+      if (first < at + n) {
+        sh.seg = s;
+        sh.tile = first - at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  DecodeWalk<P> walk(p, count, sh.seg, sh.tile);
+
+  if (warp == kDecLoad) {
+    // ------------------------------------------------------------ loader
+    if (lane == 0) prefetch_tensormap(&tmK);
+    const uint64_t policy = l2_evict_first_policy();
+    uint32_t kt = 0;
+    bool ok = true;
+    for (; ok && walk.more(); walk.next_segment()) {
+      const int b = walk.seg / p.Hkv, h = walk.seg % p.Hkv, N = ceil_div(walk.T, P);
+      const int32_t* list = p.lists ? p.lists + (size_t)walk.seg * p.max_pages : nullptr;
+      const int32_t* bt = p.bt + (size_t)b * p.max_pages;
+      const int run = walk.run(), end = min(walk.pages, (walk.tile + run) * kPages);
+      // lane i looks up the list entries at + i, two batches ahead; their physical
+      // pages, one batch ahead
+      auto entry = [&](int i) {
+        if (i >= end) return kNoPage;
+        if (!list) return i;
+        const int e = list[i];
+        if (e >= 0 && e < N) return e;
+        report(p.err, ASP_DEVERR_LIST_RANGE);
+        return kNoPage;
+      };
+      auto physical = [&](int e) { return e == kNoPage ? -1 : bt[e]; };
+      int at = walk.tile * kPages;
+      int e_now = entry(at + lane), e_next = entry(at + 32 + lane);
+      int ph_now = physical(e_now);
+      for (int j = 0; j < run; ++j, ++kt) {
+        if (j > 0 && j % kBatch == 0) {
+          at += 32;
+          e_now = e_next;
+          ph_now = physical(e_now);
+          e_next = entry(at + 32 + lane);
+        }
+        const int src = (j % kBatch) * kPages + (lane < kPages ? lane : 0);
+        const int e = __shfl_sync(kFull, e_now, src), phys = __shfl_sync(kFull, ph_now, src);
+        const bool have = lane < kPages && e != kNoPage;
+        const bool good = have && phys >= 0 && phys < p.num_phys;
+        if (have && !good) report(p.err, ASP_DEVERR_PAGE_RANGE);
+        const uint32_t bytes = __popc(__ballot_sync(kFull, good)) * (P * 128 * C::kHalves);
+        const uint32_t st = kt % C::kStages;
+        ok = __all_sync(kFull, mbar_wait(&sh.empty[st], ((kt / C::kStages) & 1) ^ 1));
+        if (!ok) break;
+        if (lane < kPages) sh.page[kt % kMetaRing][lane] = have && !good ? e | kNotMapped : e;
+        __syncwarp();
+        if (lane == 0) {
+          if (bytes) mbar_arrive_expect_tx(&sh.full[st], bytes);
+          else mbar_arrive(&sh.full[st]);
+        }
+        __syncwarp();
+        if (good) {
+#pragma unroll
+          for (int hf = 0; hf < C::kHalves; ++hf)
+            tma_load_2d_hint(ring + st * C::kTileBytes + hf * 16384 + lane * P * 128, &tmK, hf * 64,
+                             (phys * p.Hkv + h) * P, &sh.full[st], policy);
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      report(p.err, ASP_DEVERR_TIMEOUT);
+      for (uint32_t t = kt > C::kStages ? kt - C::kStages : 0; t < kt; ++t)  // copies in flight end
+        mbar_wait(&sh.full[t % C::kStages], (t / C::kStages) & 1);
+    }
+  } else if (warp == kDecQuery) {
+    // ------------------------------------------------------------ queries
+    // rows j, 8 + j, 16 + j: head j's query in three bf16 terms; rows of no head are 0
+    uint32_t seg = 0;
+    bool ok = true;
+    for (; ok && walk.more(); walk.next_segment(), ++seg) {
+      const int b = walk.seg / p.Hkv, h = walk.seg % p.Hkv, buf = seg & 1;
+      const size_t q_row = (size_t)b * p.Hq + h * p.g;
+      const uint32_t parity = ((seg >> 1) & 1) ^ 1;
+      ok = __all_sync(kFull, mbar_wait(&sh.q_empty[buf], parity) &&
+                                 mbar_wait(&sh.l_empty[buf], parity));
+      if (!ok) break;
+      if (lane < kMaxGroup) {
+        const float l = lane < p.g ? p.lse[q_row + lane] : -INFINITY;
+        sh.lse[buf][lane] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+      }
+      uint8_t* tile = queries + buf * C::kQueryBytes;
+      for (int i = lane; i < kMaxGroup * D / 8; i += 32) {  // 8 channels of one head
+        const int j = i / (D / 8), ch = i % (D / 8);
+        float f[8] = {};
+        if (j < p.g) {
+          const float4* src = reinterpret_cast<const float4*>(p.q + (q_row + j) * D + ch * 8);
+          const float4 a = src[0], bb = src[1];
+          f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+          f[4] = bb.x, f[5] = bb.y, f[6] = bb.z, f[7] = bb.w;
+        }
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          const int r = part * 8 + j;
+          uint32_t y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            y[k] = pack_bf16(f[2 * k], f[2 * k + 1]);
+            const float2 back = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&y[k]));
+            f[2 * k] -= back.x;
+            f[2 * k + 1] -= back.y;
+          }
+          *reinterpret_cast<uint4*>(tile + (ch / 8) * (kQueryRows * 128) + r * 128 +
+                                    (((ch % 8) ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full[buf]);
+    }
+    if (!ok && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
+  } else if (warp == kDecMma) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      constexpr uint32_t kDesc = mma_desc(kTileKeys, kQueryCols, false);
+      const uint32_t r0 = smem_u32(ring), q0 = smem_u32(queries);
+      uint32_t kt = 0, seg = 0;
+      bool ok = true;
+      for (; ok && walk.more(); walk.next_segment(), ++seg) {
+        const int buf = seg & 1, run = walk.run();
+        ok = mbar_wait(&sh.q_full[buf], (seg >> 1) & 1);
+        for (int j = 0; ok && j < run; ++j, ++kt) {
+          const uint32_t st = kt % C::kStages, sb = kt % kSumBufs;
+          ok = mbar_wait(&sh.s_empty[sb], ((kt / kSumBufs) & 1) ^ 1) &&
+               mbar_wait(&sh.full[st], (kt / C::kStages) & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tmem + sb * kQueryCols,
+                   smem_desc(r0 + st * C::kTileBytes + (k / 4) * 16384 + (k % 4) * 32, 16),
+                   smem_desc(q0 + buf * C::kQueryBytes + (k / 4) * (kQueryRows * 128) + (k % 4) * 32,
+                             16),
+                   kDesc, k > 0);
+          mma_commit(&sh.s_full[sb]);
+          mma_commit(&sh.empty[st]);
+        }
+        mma_commit(&sh.q_empty[buf]);
+      }
+      if (!ok) report(p.err, ASP_DEVERR_TIMEOUT);
+      mma_commit(&sh.drain);  // no arrival is still on its way when the CTA ends
+      mbar_wait(&sh.drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ sums
+    const uint32_t lanes = (uint32_t)warp << 21;
+    const float c = p.scale_log2;
+    uint32_t kt = 0, seg = 0;
+    bool ok = true;
+    for (; ok && walk.more(); walk.next_segment(), ++seg) {
+      const int buf = seg & 1, run = walk.run();
+      const size_t base = (size_t)walk.seg * p.max_pages * P;
+      float nl[kMaxGroup];
+      for (int j = 0; j < run; ++j, ++kt) {
+        const uint32_t sb = kt % kSumBufs;
+        ok = __all_sync(kFull, mbar_wait(&sh.s_full[sb], (kt / kSumBufs) & 1));
+        if (!ok) break;
+        const int e = sh.page[kt % kMetaRing][tid / P];
+        const int slot = (e & ~kNotMapped) * P + tid % P;
+        const bool mine = e != kNoPage && slot < walk.T;
+        // lists: the weight carried over is there already
+        float before = 0.f;
+        if (mine)
+          before = p.lists ? p.w_out[base + slot]
+                           : weight_before(p.w_in, p.decay, base + slot, slot, walk.T - 1);
+        if (j == 0) {
+#pragma unroll
+          for (int i = 0; i < kMaxGroup; ++i) nl[i] = sh.lse[buf][i];
+        }
+        tc_fence_after();
+        uint32_t s[32];
+        tmem_ld32(tmem + lanes + sb * kQueryCols, s);
+        tmem_wait_ld(s);
+        tc_fence_before();
+        mbar_arrive(&sh.s_empty[sb]);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kMaxGroup; ++i) {
+          const float dot = __uint_as_float(s[i]) +
+                            (__uint_as_float(s[8 + i]) + __uint_as_float(s[16 + i]));
+          if (nl[i] != -INFINITY) sum += ex2(fmaf(dot, c, nl[i]));
+        }
+        if (mine) p.w_out[base + slot] = before + (e & kNotMapped ? 0.f : sum);
+      }
+      if (ok) mbar_arrive(&sh.l_empty[buf]);
+    }
+    if (!ok && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
+  }
+  __syncthreads();
+  if (warp == kDecMma) tmem_free(tmem, kDecCols);
+}
+
+// w_out = decay * w_in over every slot of every segment (0 for the decoded
+// token), before the listed pages' weights are added.
+__global__ void __launch_bounds__(256) carry_weights_kernel(const DecodeParams p, int P) {
+  pdl_launch_dependents();
+  pdl_wait_predecessor();
+  const int seg = blockIdx.y, b = seg / p.Hkv;
+  const int T = clamp_seq_len(p.seq_lens[b], p.max_pages, P, nullptr);
+  const size_t base = (size_t)seg * p.max_pages * P;
+  for (int s = 4 * (blockIdx.x * 256 + threadIdx.x); s < T; s += 4 * 256 * gridDim.x) {
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.w_in) w = *reinterpret_cast<const float4*>(p.w_in + base + s);
+    const float y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (s + i < T) p.w_out[base + s + i] = s + i < T - 1 ? p.decay * y[i] : 0.f;
   }
 }
 
 template <int D, int P>
-cudaError_t launch_t(const WeightArgs& a, bool decode, cudaStream_t stream) {
+cudaError_t launch_decode_t(const WeightArgs& a, cudaStream_t stream) {
   const asp_paged_kv& kv = *a.kv;
-  Params p{a.q, a.q_offsets, a.q_f32, a.lists, a.lens, a.lse, a.w_in, a.w_out, kv.k_cache,
-           kv.block_table, kv.seq_lens, a.err, kv.batch, kv.num_q_heads, kv.num_kv_heads,
-           kv.max_pages, kv.num_phys_pages, a.num_tokens, a.sm_scale, a.decay};
-  const long long blocks = ((long long)kv.max_pages * P + 7) / 8;
-  const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536), kv.batch * kv.num_kv_heads);
-  auto kernel = decode ? weights_kernel<D, P, true> : weights_kernel<D, P, false>;
-  cudaError_t e = set_max_dynamic_smem((const void*)kernel, 0);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, grid, dim3(256), 0, stream, p);
-}
-
-cudaError_t launch(const WeightArgs& a, bool decode, cudaStream_t stream) {
-  const int d = a.kv->head_dim, P = a.kv->page_size;
-  if (d == 128 && P == 16) return launch_t<128, 16>(a, decode, stream);
-  if (d == 128 && P == 32) return launch_t<128, 32>(a, decode, stream);
-  if (d == 128 && P == 64) return launch_t<128, 64>(a, decode, stream);
-  if (d == 64 && P == 16) return launch_t<64, 16>(a, decode, stream);
-  if (d == 64 && P == 32) return launch_t<64, 32>(a, decode, stream);
-  if (d == 64 && P == 64) return launch_t<64, 64>(a, decode, stream);
-  return cudaErrorInvalidValue;
+  const unsigned long long cache_rows =
+      (unsigned long long)kv.num_phys_pages * kv.num_kv_heads * P;
+  DecodeParams p{a.q_f32, a.lists, a.lens, a.lse, a.w_in, a.w_out, kv.block_table, kv.seq_lens,
+                 a.err, kv.batch, kv.num_q_heads, kv.num_kv_heads,
+                 kv.num_q_heads / kv.num_kv_heads, kv.max_pages, kv.num_phys_pages,
+                 a.sm_scale * kLog2e, a.decay};
+  cudaError_t e;
+  if (a.lists) {
+    if ((e = set_max_dynamic_smem((const void*)carry_weights_kernel, 0)) != cudaSuccess) return e;
+    const int blocks = ceil_div(kv.max_pages * P, 1024);  // < 2^26 slots
+    const dim3 grid(min(blocks, 1024), kv.batch * kv.num_kv_heads);
+    if ((e = launch_pdl(carry_weights_kernel, grid, dim3(256), 0, stream, p, P)) != cudaSuccess)
+      return e;
+  }
+  CUtensorMap tk;
+  if ((e = encode_bf16_2d_swizzled(&tk, kv.k_cache, D, cache_rows, 64, P)) != cudaSuccess) return e;
+  constexpr size_t smem = decode_smem<D>();
+  if ((e = set_max_dynamic_smem((const void*)decode_weights_kernel<D, P>, (int)smem)) != cudaSuccess)
+    return e;
+  return launch_pdl(decode_weights_kernel<D, P>, dim3(2 * a.num_sms), dim3(kDecThreads), smem, stream,
+                    tk, p);
 }
 
 }  // namespace
 
 cudaError_t launch_chunk_weights(const WeightArgs& a, cudaStream_t stream) {
-  return launch(a, false, stream);
+  const int d = a.kv->head_dim, P = a.kv->page_size;
+  if (d == 128 && P == 16) return launch_chunk_t<128, 16>(a, stream);
+  if (d == 128 && P == 32) return launch_chunk_t<128, 32>(a, stream);
+  if (d == 128 && P == 64) return launch_chunk_t<128, 64>(a, stream);
+  if (d == 64 && P == 16) return launch_chunk_t<64, 16>(a, stream);
+  if (d == 64 && P == 32) return launch_chunk_t<64, 32>(a, stream);
+  if (d == 64 && P == 64) return launch_chunk_t<64, 64>(a, stream);
+  return cudaErrorInvalidValue;
 }
+
 cudaError_t launch_decode_weights(const WeightArgs& a, cudaStream_t stream) {
-  return launch(a, true, stream);
+  const int d = a.kv->head_dim, P = a.kv->page_size;
+  if (d == 128 && P == 16) return launch_decode_t<128, 16>(a, stream);
+  if (d == 128 && P == 32) return launch_decode_t<128, 32>(a, stream);
+  if (d == 128 && P == 64) return launch_decode_t<128, 64>(a, stream);
+  if (d == 64 && P == 16) return launch_decode_t<64, 16>(a, stream);
+  if (d == 64 && P == 32) return launch_decode_t<64, 32>(a, stream);
+  if (d == 64 && P == 64) return launch_decode_t<64, 64>(a, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace asp
