@@ -368,7 +368,7 @@ asp_status asp_weight_evict(const asp_paged_kv* kv, const float* weights, int32_
   WsLayout lay;
   if ((st = check_ws(kv, ws, ws_bytes, &lay)) != ASP_OK) return st;
   EvictArgs a{kv, weights, keep, recent, dst_table, w_out, kept, new_lens,
-              static_cast<uint32_t*>(ws)};
+              static_cast<uint32_t*>(ws), current_device_sm_count()};
   return from_cuda(launch_evict(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -479,6 +479,7 @@ struct EvictArgs {
   int32_t* kept;
   int32_t* new_lens;
   uint32_t* err;
+  int num_sms;
 };
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 

@@ -2,16 +2,19 @@
 // the newest tokens and the heaviest of the others stay, in their order.
 //
 // select: one CTA per segment finds the weight of rank keep - recent by four
-// 8-bit radix passes over the order-preserving integer image of the weights,
-// then walks the slots once more, ranks what stays with a block-wide prefix
-// sum and writes kept slots and weights.
+// 8-bit radix passes over the order-preserving integer image of the weights.
+// Weights share few exponents, so most of a warp falls into one bin: every lane
+// counts in a column of its own, [bin][lane], and no two lanes of a warp meet.
+// One more walk ranks what stays (the slots above that weight, and of its equals
+// the lowest) with a block-wide prefix sum and writes kept slots and weights.
 //
-// move: old slot kept[i] >= i, so moving rows in ascending order never
-// overwrites one that is still to be read. Rows are split by channels, not by
-// slots: a CTA owns 32 bytes of every K (or V) row of its segment and walks
-// the slots in tiles, a tile's loads all before its stores, so that the order
-// holds inside the CTA and no CTA waits for another, in place too. The K CTAs
-// have each page's channels in registers and write its summary.
+// move: bound by HBM (every kept K and V row read and written once). A warp takes
+// 16 rows a step, 8 bytes a lane; a page's channel minima and maxima are in the
+// same registers, so the summaries cost no second read. Old slot kept[i] >= i, so
+// in place rows move in ascending tiles, a tile's loads all before its stores: a
+// CTA owns some channels (64 to 256 bytes) of every K or V row of a segment and
+// walks its slots alone, so that the order needs no word between CTAs. Into other
+// pages there is no order to keep, and the slots are split over CTAs too.
 #include "asp_internal.cuh"
 
 namespace asp {
@@ -43,37 +46,43 @@ __device__ __forceinline__ uint32_t ordered(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Inclusive prefix sum over the CTA's threads; `total` gets the whole sum.
-__device__ __forceinline__ int block_scan(int x, int* warp_sums, int& total) {
+constexpr int kPerThread = 4;                       // slots of a thread in one step
+constexpr int kStep = kSelThreads * kPerThread;
+
+// Exclusive prefix sum over the CTA's threads; `total` gets the whole sum.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, uint32_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t y = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kFull, x, o);
-    if (lane >= o) x += y;
+    const uint32_t z = __shfl_up_sync(kFull, y, o);
+    if (lane >= o) y += z;
   }
-  __syncthreads();  // the sums of the call before are read
-  if (lane == 31) warp_sums[warp] = x;
+  if (lane == 31) warp_sums[warp] = y;
   __syncthreads();
-  int before = 0;
-  total = 0;
-  for (int w = 0; w < kSelThreads / 32; ++w) {
-    const int y = warp_sums[w];
-    if (w < warp) before += y;
-    total += y;
+  const uint32_t w = lane < kSelThreads / 32 ? warp_sums[lane] : 0;
+  uint32_t z = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(kFull, z, o);
+    if (lane >= o) z += u;
   }
-  return before + x;
+  total = __shfl_sync(kFull, z, 31);
+  return __shfl_sync(kFull, z - w, warp) + y - x;
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params p, int P) {
-  __shared__ int hist[256];
-  __shared__ int warp_sums[32];
+  __shared__ int hist[256 * 32];           // [bin][lane]
+  __shared__ int bins[256];
+  __shared__ uint32_t warp_sums[2][kSelThreads / 32];
   __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
-  const int tid = threadIdx.x, seg = blockIdx.x, b = seg / p.Hkv;
+  __shared__ int s_need, s_in_bin;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int seg = blockIdx.x, b = seg / p.Hkv;
   pdl_launch_dependents();
   pdl_wait_predecessor();
   const int T = clamp_seq_len(p.seq_lens[b], p.max_pages, P, tid == 0 ? p.err : nullptr);
-  const float* w = p.weights + (size_t)seg * p.max_pages * P;
+  const float* w = p.weights + (size_t)seg * p.max_pages * P;  // 16-byte aligned: P % 16 == 0
   float* wo = p.w_out + (size_t)seg * p.max_pages * P;
   int32_t* kept = p.kept + (size_t)seg * p.keep;
   if (seg % p.Hkv == 0 && tid == 0) p.new_lens[b] = min(T, p.keep);
@@ -84,55 +93,127 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
     }
     return;
   }
+  // four slots of this thread from i on; past `end` they are 0 and not used
+  auto load4 = [&](int i, int end) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i + 3 < end) {
+      x = *reinterpret_cast<const float4*>(w + i);
+    } else {
+      if (i < end) x.x = w[i];
+      if (i + 1 < end) x.y = w[i + 1];
+      if (i + 2 < end) x.z = w[i + 2];
+    }
+    return x;
+  };
   const int m = T - p.recent, need0 = p.keep - p.recent;  // need0 of the first m slots stay
   uint32_t prefix = 0;
   int need = need0;
-  for (int shift = 24; need0 > 0 && shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < m; i += kSelThreads) {
-      const uint32_t u = ordered(w[i]);
-      if (shift == 24 || (u >> (shift + 8)) == prefix) atomicAdd(&hist[(u >> shift) & 255], 1);
+  if (need0 > 0) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      for (int i = tid; i < 256 * 32; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
+      for (int i0 = 0; i0 < m; i0 += kStep) {
+        const int i = i0 + tid * kPerThread;
+        const float4 x = load4(i, m);
+        const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t u = ordered(y[k]);
+          if (i + k < m && (shift == 24 || (u >> (shift + 8)) == prefix))
+            atomicAdd(&hist[((u >> shift) & 255) * 32 + lane], 1);
+        }
+      }
+      __syncthreads();
+      // bin sums: a warp adds up eight bins, a lane a column
+#pragma unroll
+      for (int k = 0; k < 256 / (kSelThreads / 32); ++k) {
+        const int bin = warp * (256 / (kSelThreads / 32)) + k;
+        const int n = __reduce_add_sync(kFull, hist[bin * 32 + lane]);
+        if (lane == 0) bins[bin] = n;
+      }
+      __syncthreads();
+      if (warp == 0) {  // the bin of rank `need` from the top; lane i holds bins 8 i .. 8 i + 7
+        int n[8], mine = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mine += n[k] = bins[lane * 8 + k];
+        int above = mine;  // inclusive sum from this lane's bins to the top
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int z = __shfl_down_sync(kFull, above, o);
+          if (lane + o < 32) above += z;
+        }
+        if (above >= need && above - mine < need) {
+          int left = need - (above - mine), k = 7;
+          while (n[k] < left) left -= n[k--];
+          s_prefix = prefix << 8 | (uint32_t)(lane * 8 + k);
+          s_need = left;
+          s_in_bin = n[k];
+        }
+      }
+      __syncthreads();
+      prefix = s_prefix;
+      need = s_need;
+      if (s_in_bin == need && shift > 0) {
+        // the whole bin stays: nothing below its lower edge does, whatever the lower digits
+        prefix <<= shift;
+        need = 0;
+        break;
+      }
     }
-    __syncthreads();
-    if (tid == 0) {
-      int left = need, d = 255;
-      while (hist[d] < left) left -= hist[d--];
-      s_prefix = prefix << 8 | d;
-      s_need = left;
-    }
-    __syncthreads();
-    prefix = s_prefix;
-    need = s_need;
   }
-  // prefix: the smallest weight that stays; need: how many of that weight do
-  int out = 0, ties = 0;
-  for (int i0 = 0; i0 < T; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    const float x = i < T ? w[i] : 0.f;
-    const uint32_t u = ordered(x);
-    const bool in = i < m && need0 > 0;
-    int total;
-    const int tie = block_scan(in && u == prefix, warp_sums, total);
-    const bool stays = i < T && (i >= m || (in && (u > prefix || (u == prefix && ties + tie <= need))));
-    ties += total;
-    const int at = out + block_scan(stays, warp_sums, total) - 1;
-    out += total;
-    if (stays) {  // at <= i: in place, later tiles are still whole
-      kept[at] = i;
-      wo[at] = x;
+  // Slots with a larger image than `prefix` stay, and the first `need` that equal it; where a
+  // whole bin stays (need 0 after it), equals of its lower edge stay too.
+  const bool all_equal = need0 > 0 && need == 0;
+  if (all_equal) need = 0x7fffffff;
+  int above_before = 0, equal_before = 0;
+  int par = 0;
+  for (int i0 = 0; i0 < T; i0 += kStep, par ^= 1) {
+    const int i = i0 + tid * kPerThread;
+    const float4 x = load4(i, T);
+    const float y[4] = {x.x, x.y, x.z, x.w};
+    bool over[4], same[4];
+    uint32_t cnt = 0;  // above in the low half, equal in the high half: at most 4096 each
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t u = ordered(y[k]);
+      const bool in = i + k < m && need0 > 0;
+      over[k] = (i + k >= m && i + k < T) || (in && u > prefix);
+      same[k] = in && u == prefix;
+      cnt += (over[k] ? 1u : 0u) + (same[k] ? 0x10000u : 0u);
     }
+    uint32_t total;
+    const uint32_t pre = block_scan(cnt, warp_sums[par], total);
+    int above = above_before + (int)(pre & 0xffff), equal = equal_before + (int)(pre >> 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (over[k] || (same[k] && equal < need)) {
+        const int at = above + min(equal, need);  // at <= slot: in place, later steps are whole
+        kept[at] = i + k;
+        wo[at] = y[k];
+      }
+      above += over[k];
+      equal += same[k];
+    }
+    above_before += (int)(total & 0xffff);
+    equal_before += (int)(total >> 16);
   }
 }
 
-template <int D, int P>
-__global__ void __launch_bounds__(256) evict_move_kernel(const Params p) {
-  constexpr int kU = 4;               // rows of one lane pair in a tile
-  constexpr int kTile = 8 * 16 * kU;  // rows of a tile: a warp owns 64 in a row
+constexpr int kMoveThreads = 256;
+constexpr int kGroup = 16;  // rows of a warp's lane group in one step
+
+// Lanes: kLanes of them, 8 bytes each, hold a row's slice.
+template <int D, int P, int kLanes>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const Params p, int in_order) {
+  constexpr int kGroups = 32 / kLanes;                 // groups of 16 rows a warp
+  constexpr int kWarpRows = kGroup * kGroups;
+  constexpr int kTile = kMoveThreads / 32 * kWarpRows;
+  constexpr int kIdx = (kWarpRows + 31) / 32;          // rows whose places a lane looks up
+  __shared__ uint2 s_mn[P > kGroup ? kMoveThreads : 1], s_mx[P > kGroup ? kMoveThreads : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int seg = blockIdx.x, b = seg / p.Hkv, h = seg % p.Hkv;
-  const bool is_k = blockIdx.z == 0;
-  const int c0 = blockIdx.y * 16 + (lane & 1) * 8;  // first of this lane's 8 channels
+  const bool is_k = (blockIdx.y & 1) == 0;
+  const int c0 = (blockIdx.y >> 1) * (kLanes * 4) + (lane % kLanes) * 4;  // this lane's 4 channels
   pdl_launch_dependents();
   pdl_wait_predecessor();
   const int T = clamp_seq_len(p.seq_lens[b], p.max_pages, P, nullptr);
@@ -140,73 +221,105 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const Params p) {
   const int32_t* kept = p.kept + (size_t)seg * p.keep;
   const int32_t* from = p.src_table + (size_t)b * p.max_pages;
   const int32_t* to = p.dst_table + (size_t)b * p.max_pages;
-  uint16_t* cache = is_k ? p.k : p.v;
-  for (int t0 = 0; t0 < n; t0 += kTile) {
-    uint4 x[kU];
-    bool ok[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int i = t0 + warp * 16 * kU + u * 16 + (lane >> 1);
-      ok[u] = false;
-      if (i >= n) continue;
-      const int s = kept[i];
-      const int phys = from[s / P];
-      if (phys < 0 || phys >= p.num_phys) {
-        report(p.err, ASP_DEVERR_PAGE_RANGE);
-        continue;
-      }
-      ok[u] = true;
-      x[u] = *reinterpret_cast<const uint4*>(cache + (((size_t)phys * p.Hkv + h) * P + s % P) * D + c0);
+  uint16_t* cache = (is_k ? p.k : p.v) + c0;
+  const int tiles = ceil_div(n, kTile);
+  const int t0 = (int)((long long)tiles * blockIdx.z / gridDim.z);
+  const int t1 = (int)((long long)tiles * (blockIdx.z + 1) / gridDim.z);
+
+  // cache row of slot s under a table, -1 where the table has none
+  auto row_of = [&](const int32_t* table, int s) {
+    const int phys = table[s / P];
+    if (phys < 0 || phys >= p.num_phys) {
+      report(p.err, ASP_DEVERR_PAGE_RANGE);
+      return -1;
     }
-    __syncthreads();  // every row of the tile is read before one is written
+    return (phys * p.Hkv + h) * P + s % P;
+  };
+  int src[kIdx], dst[kIdx];
+  auto places = [&](int t) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int i = t0 + warp * 16 * kU + u * 16 + (lane >> 1);
-      if (i >= n || !ok[u]) continue;
-      const int phys = to[i / P];
-      if (phys < 0 || phys >= p.num_phys) {
-        report(p.err, ASP_DEVERR_PAGE_RANGE);
-        continue;
+    for (int q = 0; q < kIdx; ++q) {
+      const int i = t * kTile + warp * kWarpRows + q * 32 + lane;
+      src[q] = dst[q] = -1;
+      if (q * 32 + lane < kWarpRows && i < n) {
+        src[q] = row_of(from, kept[i]);
+        dst[q] = row_of(to, i);
       }
-      *reinterpret_cast<uint4*>(cache + (((size_t)phys * p.Hkv + h) * P + i % P) * D + c0) = x[u];
     }
+  };
+  if (t0 < t1) places(t0);
+  for (int t = t0; t < t1; ++t) {
+    uint2 x[kGroup];
+    int to_row[kGroup];
+    uint32_t have = 0;
+#pragma unroll
+    for (int u = 0; u < kGroup; ++u) {
+      const int r = lane / kLanes * kGroup + u;  // the warp's row, held by lane r % 32
+      int s, d;
+      if constexpr (kIdx == 1) {
+        s = __shfl_sync(kFull, src[0], r);
+        d = __shfl_sync(kFull, dst[0], r);
+      } else {
+        const int s0 = __shfl_sync(kFull, src[0], r & 31), s1 = __shfl_sync(kFull, src[1], r & 31);
+        const int d0 = __shfl_sync(kFull, dst[0], r & 31), d1 = __shfl_sync(kFull, dst[1], r & 31);
+        s = r < 32 ? s0 : s1;
+        d = r < 32 ? d0 : d1;
+      }
+      to_row[u] = s >= 0 ? d : -1;
+      if (s >= 0) {
+        have |= 1u << u;
+        x[u] = __ldcg(reinterpret_cast<const uint2*>(cache + (size_t)s * D));
+      }
+    }
+    if (t + 1 < t1) places(t + 1);
+    if (in_order) __syncthreads();  // every row of the tile is read before one is written
+#pragma unroll
+    for (int u = 0; u < kGroup; ++u)
+      if (to_row[u] >= 0) *reinterpret_cast<uint2*>(cache + (size_t)to_row[u] * D) = x[u];
     if (!is_k) continue;
-    // summaries: rows 16 u .. 16 u + 15 of the warp lie in the lanes; a page is P / 16 of them
+    uint2 mn = make_uint2(0x7f807f80u, 0x7f807f80u), mx = make_uint2(0xff80ff80u, 0xff80ff80u);
 #pragma unroll
-    for (int u0 = 0; u0 < kU; u0 += P / 16) {
-      uint32_t mn[4], mx[4];
-      bool any = false;
+    for (int u = 0; u < kGroup; ++u)
+      if (have >> u & 1) {
+        mn = vmin(mn, x[u]);
+        mx = vmax(mx, x[u]);
+      }
+    const int first = t * kTile + warp * kWarpRows + lane / kLanes * kGroup;  // the group's slot
+    if constexpr (P > kGroup) {
+      // a page is P / 16 groups in a row: neighbouring lane groups, then warps
+      s_mn[tid] = mn;
+      s_mx[tid] = mx;
+      __syncthreads();
+      if (first % P == 0) {
 #pragma unroll
-      for (int u = u0; u < u0 + P / 16; ++u) {
-        if (!ok[u]) continue;
-        const uint32_t y[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mn[c] = any ? vmin(mn[c], y[c]) : y[c];
-          mx[c] = any ? vmax(mx[c], y[c]) : y[c];
+        for (int k = 1; k < P / kGroup; ++k) {
+          mn = vmin(mn, s_mn[tid + k * kLanes]);
+          mx = vmax(mx, s_mx[tid + k * kLanes]);
         }
-        any = true;
       }
-#pragma unroll
-      for (int o = 2; o < 32; o <<= 1) {
-        const bool oa = __shfl_xor_sync(kFull, (int)any, o) != 0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t a = __shfl_xor_sync(kFull, any ? mn[c] : 0u, o);
-          const uint32_t z = __shfl_xor_sync(kFull, any ? mx[c] : 0u, o);
-          mn[c] = any && oa ? vmin(mn[c], a) : any ? mn[c] : a;
-          mx[c] = any && oa ? vmax(mx[c], z) : any ? mx[c] : z;
-        }
-        any |= oa;
-      }
-      const int page = (t0 + warp * 16 * kU + u0 * 16) / P;
-      if (lane < 2 && any && page * P < n) {
-        uint16_t* s = p.summ + ((size_t)seg * p.max_pages + page) * 2 * D + c0;
-        *reinterpret_cast<uint4*>(s) = make_uint4(mn[0], mn[1], mn[2], mn[3]);
-        *reinterpret_cast<uint4*>(s + D) = make_uint4(mx[0], mx[1], mx[2], mx[3]);
-      }
+      __syncthreads();
+    }
+    if (first % P == 0 && first < n) {
+      uint16_t* s = p.summ + ((size_t)seg * p.max_pages + first / P) * 2 * D + c0;
+      *reinterpret_cast<uint2*>(s) = mn;
+      *reinterpret_cast<uint2*>(s + D) = mx;
     }
   }
+}
+
+template <int D, int P, int kLanes>
+cudaError_t launch_move(const Params& p, const asp_paged_kv& kv, int sms, cudaStream_t stream) {
+  auto kernel = evict_move_kernel<D, P, kLanes>;
+  const int slices = D / (kLanes * 4) * 2, segments = kv.batch * kv.num_kv_heads;
+  const bool in_order = p.src_table == p.dst_table;
+  // Into other pages: enough CTAs to fill the GPU (three an SM fit) twice over.
+  const int tile = kMoveThreads / 32 * kGroup * (32 / kLanes);
+  const int splits =
+      in_order ? 1 : max(1, min(ceil_div(p.keep, tile), ceil_div(6 * sms, slices * segments)));
+  cudaError_t e = set_max_dynamic_smem((const void*)kernel, 0);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(segments, slices, splits), dim3(kMoveThreads), 0, stream, p,
+                    (int)in_order);
 }
 
 template <int D, int P>
@@ -218,10 +331,13 @@ cudaError_t launch_t(const EvictArgs& a, cudaStream_t stream) {
   const int segments = kv.batch * kv.num_kv_heads;
   cudaError_t e = set_max_dynamic_smem((const void*)evict_select_kernel, 0);
   if (e != cudaSuccess) return e;
-  if ((e = set_max_dynamic_smem((const void*)evict_move_kernel<D, P>, 0)) != cudaSuccess) return e;
   e = launch_pdl(evict_select_kernel, dim3(segments), dim3(kSelThreads), 0, stream, p, P);
   if (e != cudaSuccess) return e;
-  return launch_pdl(evict_move_kernel<D, P>, dim3(segments, D / 16, 2), dim3(256), 0, stream, p);
+  // Whole rows where the segments alone fill the GPU; in place with fewer of them,
+  // slices of 64 bytes make up for it.
+  const bool few = p.src_table == p.dst_table && segments < a.num_sms;
+  if (few) return launch_move<D, P, 8>(p, kv, a.num_sms, stream);
+  return launch_move<D, P, D / 4>(p, kv, a.num_sms, stream);
 }
 
 }  // namespace
