@@ -5,11 +5,15 @@
 //   y = x * rsqrt(mean(x^2) + eps) * weight;  (a, b) -> (a cos - b sin, b cos + a sin)
 //
 // One work item is one page of one request: the new tokens that fall into it.
-// Its CTA computes each token's cosines and sines once, in shared memory, for
-// all heads; a warp takes a head and walks the item's tokens, so a key head's
-// channel minima and maxima stay in registers until the page is done and the
-// summary is written once, without atomics. d / 4 lanes hold a row, 8 bytes
-// each; the two halves of a rotated pair meet through one shuffle.
+// Its CTA computes each token's cosines and sines once, in shared memory, for all
+// heads, while a loader thread streams the tokens' rows (contiguous in the packed
+// array) through a ring of shared-memory stages, so that what is in flight does
+// not cost registers: with the loads in registers the kernel took 110 us for 16k
+// tokens of 48 heads, and 173 where smaller register budgets made them spill.
+// Warps take rows; a row is d / 8 lanes wide, and a lane holds the two halves of
+// four rotated pairs, so a pair never crosses lanes. A warp keeps the same key
+// heads for all tokens, their channel minima and maxima in registers until the
+// page is done: the summary is written once, without atomics.
 //
 // The angle: a frequency becomes a 64-bit fixed-point fraction of a turn, whose
 // product with the integer position wraps exactly modulo one turn, so that
@@ -21,7 +25,8 @@ namespace asp {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kThreads = (kWarps + 1) * 32;  // and a loader
+constexpr int kMaxStages = 16;
 constexpr unsigned kFull = 0xffffffffu;
 
 struct Params {
@@ -40,7 +45,7 @@ struct Params {
   const int32_t* seq_lens;
   uint32_t* err;
   int B, Hq, Hkv, max_pages, num_phys, num_tokens;
-  int rot, interleaved;
+  int rot, nq, nk, stages;  // nq, nk: query and KV heads of a CTA
   float eps;
 };
 
@@ -57,14 +62,77 @@ __device__ __forceinline__ float2 unpack(uint32_t x) {
   return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&x));
 }
 
+__device__ __forceinline__ void unpack4(uint2 v, float* f) {
+  const float2 lo = unpack(v.x), hi = unpack(v.y);
+  f[0] = lo.x, f[1] = lo.y, f[2] = hi.x, f[3] = hi.y;
+}
+__device__ __forceinline__ uint2 pack4(const float* f) {
+  return make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+}
+__device__ __forceinline__ uint2 load4(const uint16_t* p) {
+  return __ldg(reinterpret_cast<const uint2*>(p));
+}
+
+// A lane's eight channels of a row are two times four. Halves rotated against each
+// other: channels a + i and b + i are pair i; interleaved: eight in a row. Lanes
+// past the rotated channels hold eight plain ones.
+// x normed, weighted and rotated in place; kLanes lanes of a row.
+template <int kLanes>
+__device__ __forceinline__ void norm_rotate(float (&x)[8], const uint2 (&wb)[2], bool norm,
+                                            float inv_d, float eps, bool turns, bool interleaved,
+                                            const float2 (&cs)[4]) {
+  if (norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+    const float r = rsqrtf(fmaf(ss, inv_d, eps));
+    float w[8];
+    unpack4(wb[0], w);
+    unpack4(wb[1], w + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
+  }
+  if (turns) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // pairs (i, 4 + i), or (2i, 2i + 1) of the eight
+      const int ia = interleaved ? 2 * i : i, ib = interleaved ? 2 * i + 1 : 4 + i;
+      const float a = x[ia], b = x[ib];
+      x[ia] = a * cs[i].x - b * cs[i].y;
+      x[ib] = b * cs[i].x + a * cs[i].y;
+    }
+  }
+}
+
+// Shared memory of a CTA: the ring, then these.
 template <int D, int P>
+struct Shared {
+  float2 turn[P * (D / 2)];             // (cos, sin) of [token of the page][pair]
+  unsigned long long turns_of[D / 2];   // 2^64 * inv_freq / (2 pi), modulo 2^64
+  uint64_t full[kMaxStages], empty[kMaxStages];
+};
+
+template <int D, int P, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) norm_rotate_kernel(const Params p) {
-  constexpr int kLanes = D / 4;          // lanes of one row
-  constexpr int kRows = 32 / kLanes;     // rows a warp takes at once
-  constexpr int kUnroll = 4;
-  __shared__ float2 turn[P * (D / 2)];   // (cos, sin) of [token of the page][pair]
+  constexpr int kLanes = D / 8;        // lanes of one row
+  constexpr int kRows = 32 / kLanes;   // rows a warp takes at once
+  extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int sub = lane / kLanes, l = lane % kLanes, c0 = 4 * l;
+  const int sub = lane / kLanes, l = lane % kLanes;
+  // this CTA's heads: a share of the query heads and of the KV heads
+  const int q0 = blockIdx.y * p.nq, nq = max(0, min(p.nq, p.Hq - q0));
+  const int k0 = blockIdx.y * p.nk, nk = max(0, min(p.nk, p.Hkv - k0));
+  const int stage_bytes = (p.nq + 2 * p.nk) * D * 2;
+  Shared<D, P>& sh = *reinterpret_cast<Shared<D, P>*>(smem + p.stages * stage_bytes);
+  if (tid == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], kWarps);
+    }
+    mbar_fence_init();
+  }
   pdl_launch_dependents();
   pdl_wait_predecessor();
 
@@ -72,6 +140,12 @@ __global__ void __launch_bounds__(kThreads) norm_rotate_kernel(const Params p) {
     for (int x = tid; x < p.B; x += kThreads)
       new_rows(p.q_offsets, x, clamp_seq_len(p.seq_lens[x], p.max_pages, P, p.err), p.num_tokens,
                p.err);
+  }
+  const int half = p.rot / 2;
+  if (tid < half) {
+    double t = (double)p.inv_freq[tid] * 0.15915494309189533577;  // 1 / (2 pi)
+    t -= floor(t);
+    sh.turns_of[tid] = (unsigned long long)(t * 18446744073709551616.0);
   }
 
   // the item's request: the last whose first item is not past it
@@ -95,139 +169,166 @@ __global__ void __launch_bounds__(kThreads) norm_rotate_kernel(const Params p) {
   const int lo = max(first, page * P), hi = min(T, (page + 1) * P);
   if (lo >= hi || page_of_b < 0) return;
   const int row0 = nr.row0 + (lo - first), cnt = hi - lo;  // packed rows of the item
+  const int Hall = p.Hq + 2 * p.Hkv;
+  __syncthreads();  // barriers and turns_of are set
 
-  const int half = p.rot / 2;
-  for (int i = tid; i < cnt * half; i += kThreads) {
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ loader
+    if (lane != 0) return;
+    const uint32_t bytes = (uint32_t)(nq + 2 * nk) * D * 2;
+    if (bytes == 0) return;
+    int t = 0;
+    bool ok = true;
+    for (; t < cnt; ++t) {
+      const int st = t % p.stages;
+      ok = mbar_wait(&sh.empty[st], ((t / p.stages) & 1) ^ 1);
+      if (!ok) break;
+      const uint16_t* row = p.qkv + (size_t)(row0 + t) * Hall * D;
+      uint8_t* dst = smem + st * stage_bytes;
+      mbar_arrive_expect_tx(&sh.full[st], bytes);
+      if (nq > 0) bulk_g2s(dst, row + q0 * D, nq * D * 2, &sh.full[st]);
+      if (nk > 0) {
+        dst += p.nq * D * 2;
+        bulk_g2s(dst, row + (p.Hq + k0) * D, nk * D * 2, &sh.full[st]);
+        bulk_g2s(dst + p.nk * D * 2, row + (p.Hq + p.Hkv + k0) * D, nk * D * 2, &sh.full[st]);
+      }
+    }
+    // the CTA's memory stays until its copies have ended
+    if (!ok) report(p.err, ASP_DEVERR_TIMEOUT);
+    for (int i = max(0, t - p.stages); i < t; ++i)
+      mbar_wait(&sh.full[i % p.stages], (i / p.stages) & 1);
+    return;
+  }
+
+  for (int i = tid; i < cnt * half; i += kWarps * 32) {
     const int t = i / half, f = i % half;
     const int pos = p.positions ? p.positions[row0 + t] : lo + t;
-    double turns = (double)p.inv_freq[f] * 0.15915494309189533577;  // 1 / (2 pi)
-    turns -= floor(turns);
-    const unsigned long long fixed = (unsigned long long)(turns * 18446744073709551616.0);
-    const unsigned long long phase = fixed * (unsigned long long)(long long)pos;
+    const unsigned long long phase = sh.turns_of[f] * (unsigned long long)(long long)pos;
     float s, c;
     sincospif((float)(int)(phase >> 32) * 4.656612873077393e-10f, &s, &c);  // 2 * 2^-32 half turns
-    turn[t * (D / 2) + f] = make_float2(c, s);
+    sh.turn[t * (D / 2) + f] = make_float2(c, s);
   }
   const int phys = p.bt[(size_t)b * p.max_pages + page];
   const bool mapped = phys >= 0 && phys < p.num_phys;
   if (!mapped && tid == 0) report(p.err, ASP_DEVERR_PAGE_RANGE);
-  __syncthreads();
+  named_bar_sync(1, kWarps * 32);
 
-  const int Hall = p.Hq + 2 * p.Hkv;
+  // the lane's channels, and its weights
+  const bool turns = 8 * l < p.rot, split = turns && !kInterleaved;
+  const int ca = split ? 4 * l : 8 * l, cb = split ? half + 4 * l : 8 * l + 4;
   const float inv_d = 1.0f / D;
-  for (int h = blockIdx.y * kWarps + warp; h < p.Hq + p.Hkv; h += gridDim.y * kWarps) {
-    const bool key = h >= p.Hq;
-    if (key && !mapped) continue;
-    const uint16_t* wsrc = key ? p.k_weight : p.q_weight;
-    float w[4] = {1.f, 1.f, 1.f, 1.f};
-    if (wsrc) {
-      const uint2 wb = *reinterpret_cast<const uint2*>(wsrc + c0);
-      const float2 w0 = unpack(wb.x), w1 = unpack(wb.y);
-      w[0] = w0.x, w[1] = w0.y, w[2] = w1.x, w[3] = w1.y;
+  uint2 wq[2] = {}, wk[2] = {};
+  if (p.q_weight) {
+    wq[0] = load4(p.q_weight + ca);
+    wq[1] = load4(p.q_weight + cb);
+  }
+  if (p.k_weight) {
+    wk[0] = load4(p.k_weight + ca);
+    wk[1] = load4(p.k_weight + cb);
+  }
+  // rows of this warp: query rows (warp + 8 i) * kRows + sub, one group of key heads,
+  // and, from the other end, groups of value heads
+  const int kh = warp * kRows + sub;
+  const bool k_mine = warp * kRows < nk, k_row = kh < nk;
+  const size_t k_block = mapped ? ((size_t)phys * p.Hkv + k0) * P : 0;
+  // folding starts from values that any key replaces
+  uint2 mn[2] = {make_uint2(0x7f807f80u, 0x7f807f80u), make_uint2(0x7f807f80u, 0x7f807f80u)};
+  uint2 mx[2] = {make_uint2(0xff80ff80u, 0xff80ff80u), make_uint2(0xff80ff80u, 0xff80ff80u)};
+  bool ok = true;
+  for (int t = 0; t < cnt; ++t) {
+    const int st = t % p.stages;
+    if (nq + nk > 0) ok = __all_sync(kFull, mbar_wait(&sh.full[st], (t / p.stages) & 1));
+    if (!ok) break;
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(smem + st * stage_bytes);
+    const uint16_t* k = q + p.nq * D;
+    const uint16_t* v = k + p.nk * D;
+    float2 cs[4];
+    if (turns) {
+      const float4* src = reinterpret_cast<const float4*>(sh.turn + t * (D / 2) + 4 * l);
+      const float4 x = src[0], y = src[1];
+      cs[0] = make_float2(x.x, x.y), cs[1] = make_float2(x.z, x.w);
+      cs[2] = make_float2(y.x, y.y), cs[3] = make_float2(y.z, y.w);
     }
-    const size_t head_block = key ? ((size_t)phys * p.Hkv + (h - p.Hq)) * P : 0;
-    uint2 mn = make_uint2(0, 0), mx = mn;
-    bool any = false;
-    for (int t0 = 0; t0 < cnt; t0 += kRows * kUnroll) {
-      uint2 x[kUnroll], vv[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int t = t0 + u * kRows + sub;
-        x[u] = vv[u] = make_uint2(0, 0);
-        if (t < cnt) {
-          const uint16_t* row = p.qkv + ((size_t)(row0 + t) * Hall + h) * D + c0;
-          x[u] = __ldg(reinterpret_cast<const uint2*>(row));
-          if (key) vv[u] = __ldg(reinterpret_cast<const uint2*>(row + (size_t)p.Hkv * D));
-        }
+    auto row_at = [&](const uint16_t* base, int r, float (&x)[8]) {
+      unpack4(*reinterpret_cast<const uint2*>(base + r * D + ca), x);
+      unpack4(*reinterpret_cast<const uint2*>(base + r * D + cb), x + 4);
+    };
+#pragma unroll 2
+    for (int g = warp; g * kRows < nq; g += kWarps) {
+      const int r = g * kRows + sub;
+      float x[8];
+      row_at(q, min(r, nq - 1), x);
+      norm_rotate<kLanes>(x, wq, p.q_weight != nullptr, inv_d, p.eps, turns, kInterleaved, cs);
+      if (r >= nq) continue;
+      const size_t o = ((size_t)(row0 + t) * p.Hq + q0 + r) * D;
+      if (p.q_out) {
+        *reinterpret_cast<uint2*>(p.q_out + o + ca) = pack4(x);
+        *reinterpret_cast<uint2*>(p.q_out + o + cb) = pack4(x + 4);
       }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int t = t0 + u * kRows + sub;
-        const float2 x0 = unpack(x[u].x), x1 = unpack(x[u].y);
-        float y[4] = {x0.x, x0.y, x1.x, x1.y};
-        if (wsrc) {
-          float ss = y[0] * y[0] + y[1] * y[1] + y[2] * y[2] + y[3] * y[3];
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-          const float r = rsqrtf(ss * inv_d + p.eps);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = y[i] * r * w[i];
-        }
-        if (p.rot > 0) {
-          if (p.interleaved) {
-            if (c0 < p.rot && t < cnt) {
-              const float2* cs = turn + t * (D / 2) + c0 / 2;
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float a = y[2 * i], bb = y[2 * i + 1];
-                y[2 * i] = a * cs[i].x - bb * cs[i].y;
-                y[2 * i + 1] = bb * cs[i].x + a * cs[i].y;
-              }
-            }
-          } else {
-            const int hl = p.rot / 8;  // lanes of one half of the rotated channels
-            const int peer = l < hl ? l + hl : l < 2 * hl ? l - hl : l;
-            float z[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) z[i] = __shfl_sync(kFull, y[i], peer + sub * kLanes);
-            if (c0 < p.rot && t < cnt) {
-              const float2* cs = turn + t * (D / 2) + (l < hl ? c0 : c0 - half);
-              const float sign = l < hl ? -1.f : 1.f;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) y[i] = y[i] * cs[i].x + sign * z[i] * cs[i].y;
-            }
-          }
-        }
-        if (t >= cnt) continue;
-        const uint2 yb = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
-        if (!key) {
-          const size_t o = ((size_t)(row0 + t) * p.Hq + h) * D + c0;
-          if (p.q_out) *reinterpret_cast<uint2*>(p.q_out + o) = yb;
-          if (p.q_out_f32)
-            *reinterpret_cast<float4*>(p.q_out_f32 + o) = make_float4(y[0], y[1], y[2], y[3]);
-        } else {
-          const size_t o = (head_block + (lo + t) % P) * D + c0;
-          *reinterpret_cast<uint2*>(p.k + o) = yb;
-          *reinterpret_cast<uint2*>(p.v + o) = vv[u];
-          mn = any ? vmin(mn, yb) : yb;
-          mx = any ? vmax(mx, yb) : yb;
-          any = true;
-        }
+      if (p.q_out_f32) {
+        *reinterpret_cast<float4*>(p.q_out_f32 + o + ca) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(p.q_out_f32 + o + cb) = make_float4(x[4], x[5], x[6], x[7]);
       }
     }
-    if (!key) continue;
-    if (kRows == 2) {  // the two half-warps took alternate rows
-      const uint2 on = make_uint2(__shfl_xor_sync(kFull, mn.x, 16), __shfl_xor_sync(kFull, mn.y, 16));
-      const uint2 ox = make_uint2(__shfl_xor_sync(kFull, mx.x, 16), __shfl_xor_sync(kFull, mx.y, 16));
-      const bool oa = __shfl_xor_sync(kFull, (int)any, 16) != 0;
-      mn = any && oa ? vmin(mn, on) : any ? mn : on;
-      mx = any && oa ? vmax(mx, ox) : any ? mx : ox;
+    if (mapped && k_mine) {
+      float x[8];
+      row_at(k, min(kh, nk - 1), x);
+      norm_rotate<kLanes>(x, wk, p.k_weight != nullptr, inv_d, p.eps, turns, kInterleaved, cs);
+      if (k_row) {
+        uint16_t* dst = p.k + (k_block + (size_t)kh * P + (lo + t) % P) * D;
+        const uint2 ya = pack4(x), yb = pack4(x + 4);
+        *reinterpret_cast<uint2*>(dst + ca) = ya;
+        *reinterpret_cast<uint2*>(dst + cb) = yb;
+        mn[0] = vmin(mn[0], ya), mn[1] = vmin(mn[1], yb);
+        mx[0] = vmax(mx[0], ya), mx[1] = vmax(mx[1], yb);
+      }
     }
-    if (sub != 0) continue;
-    uint16_t* s = p.summ + (((size_t)b * p.Hkv + (h - p.Hq)) * p.max_pages + page) * 2 * D + c0;
-    uint2* smin = reinterpret_cast<uint2*>(s);
-    uint2* smax = reinterpret_cast<uint2*>(s + D);
-    const bool fresh = lo == page * P;
-    *smin = fresh ? mn : vmin(*smin, mn);
-    *smax = fresh ? mx : vmax(*smax, mx);
+    if (mapped) {
+      const int vh = (kWarps - 1 - warp) * kRows + sub;  // nk <= 8: one group at most
+      if (vh < nk)
+        *reinterpret_cast<uint4*>(p.v + (k_block + (size_t)vh * P + (lo + t) % P) * D + 8 * l) =
+            *reinterpret_cast<const uint4*>(v + vh * D + 8 * l);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.empty[st]);
+  }
+  if (!ok) {
+    if (lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
+    return;
+  }
+  if (!mapped || !k_row) return;
+  uint16_t* s = p.summ + (((size_t)b * p.Hkv + k0 + kh) * p.max_pages + page) * 2 * D;
+  const bool fresh = lo == page * P;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint2* smin = reinterpret_cast<uint2*>(s + (i ? cb : ca));
+    uint2* smax = reinterpret_cast<uint2*>(s + D + (i ? cb : ca));
+    *smin = fresh ? mn[i] : vmin(*smin, mn[i]);
+    *smax = fresh ? mx[i] : vmax(*smax, mx[i]);
   }
 }
 
 template <int D, int P>
 cudaError_t launch_t(const NormRotateArgs& a, cudaStream_t stream) {
   const asp_paged_kv& kv = *a.kv;
+  const int items = a.q_offsets ? a.num_tokens / P + 2 * kv.batch : kv.batch;
+  // Few items: split their heads over several CTAs (each computes the angles
+  // again) until there are about four CTAs an SM, but not below a step of query rows for every warp.
+  const int split = max(1, min(4 * a.num_sms / items, kv.num_q_heads * D / (kWarps * 256)));
+  const int nq = ceil_div(kv.num_q_heads, split), nk = ceil_div(kv.num_kv_heads, split);
+  const int stage_bytes = (nq + 2 * nk) * D * 2;
+  // as many stages as an item has tokens, in a third of an SM's shared memory at most
+  constexpr int kBudget = 72 * 1024;
+  const int stages = max(2, min(min(kMaxStages, P), kBudget / stage_bytes));
   Params p{a.qkv, a.q_offsets, a.positions, a.q_weight, a.k_weight, a.inv_freq, a.q_out,
            a.q_out_f32, kv.k_cache, kv.v_cache, kv.summaries, kv.block_table, kv.seq_lens, a.err,
            kv.batch, kv.num_q_heads, kv.num_kv_heads, kv.max_pages, kv.num_phys_pages,
-           a.num_tokens, a.rotary_dim, a.interleaved, a.eps};
-  const int items = a.q_offsets ? a.num_tokens / P + 2 * kv.batch : kv.batch;
-  const int heads = kv.num_q_heads + kv.num_kv_heads;
-  // Few items: split their heads over several CTAs (each computes the angles
-  // again) until there are about four CTAs an SM.
-  const int split = min(ceil_div(heads, kWarps), max(1, 4 * a.num_sms / items));
-  cudaError_t e = set_max_dynamic_smem((const void*)norm_rotate_kernel<D, P>, 0);
+           a.num_tokens, a.rotary_dim, nq, nk, stages, a.eps};
+  auto kernel = a.interleaved ? norm_rotate_kernel<D, P, true> : norm_rotate_kernel<D, P, false>;
+  const int smem = stages * stage_bytes + (int)sizeof(Shared<D, P>);
+  cudaError_t e = set_max_dynamic_smem((const void*)kernel, kBudget + (int)sizeof(Shared<D, P>));
   if (e != cudaSuccess) return e;
-  return launch_pdl(norm_rotate_kernel<D, P>, dim3(items, split), dim3(kThreads), 0, stream, p);
+  return launch_pdl(kernel, dim3(items, split), dim3(kThreads), smem, stream, p);
 }
 
 }  // namespace
