@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 128);
+      mbar_init(&sh.p_full[i], 4);  // the tile's warps
       mbar_init(&sh.o_full[i], 1);
     }
     mbar_fence_init();
@@ -201,64 +201,76 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (lane == 0) {
-      constexpr uint32_t kDescS = mma_desc(128, kTileKeys, false);
-      constexpr uint32_t kDescO = mma_desc(128, D, true);
-      const uint32_t q0 = smem_u32(q_tiles), r0 = smem_u32(ring);
-      uint32_t tile = 0, piece = 0, np[2] = {0, 0};
-      bool ok = true;
-      auto product_s = [&](int t, uint32_t st) {
+    constexpr uint32_t kDescS = mma_desc(128, kTileKeys, false);
+    constexpr uint32_t kDescO = mma_desc(128, D, true);
+    const uint32_t q0 = uniform(smem_u32(q_tiles)), r0 = uniform(smem_u32(ring));
+    const uint32_t tm = uniform(tmem);
+    uint32_t tile = 0, piece = 0, np[2] = {0, 0};
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(kFull, mbar_wait(bar, parity)) != 0;
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) mma_commit(bar);
+    };
+    auto product_s = [&](int t, uint32_t st) {
+      const uint64_t a = smem_desc(q0 + t * C::kTileBytes, 16);
+      const uint64_t b = smem_desc(r0 + st * C::kTileBytes, 16);
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-          mma_ss(tmem + t * 128, smem_desc(q0 + t * C::kTileBytes + off, 16),
-                 smem_desc(r0 + st * C::kTileBytes + off, 16), kDescS, k > 0);
+          const uint32_t off = ((k / 4) * 16384 + (k % 4) * 32) >> 4;
+          mma_ss(tm + t * 128, a + off, b + off, kDescS, k > 0);
         }
         mma_commit(&sh.s_full[t]);
-      };
-      auto product_o = [&](int t, uint32_t st, bool add) {
+      }
+    };
+    auto product_o = [&](int t, uint32_t st, bool add) {
+      const uint64_t b = smem_desc(r0 + st * C::kTileBytes, 16384);
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kTileKeys / 16; ++k)
-          mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8,
-                 smem_desc(r0 + st * C::kTileBytes + k * 2048, 16384), kDescO, add || k > 0);
-      };
-      for (; ok && walk.more(); walk.next(), ++piece) {
-        const Piece pc(walk, tile_tokens);
-        const int n = max(pc.n[0], pc.n[1]);
-        uint32_t st = tile % C::kStages;
-        ok = mbar_wait(&sh.q_full, piece & 1) &&
-             mbar_wait(&sh.full[st], (tile / C::kStages) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        for (int t = 0; t < 2; ++t)
-          if (pc.n[t] > 0) product_s(t, st);
-        mma_commit(&sh.empty[st]);
-        if (n == 1) mma_commit(&sh.q_empty);
-        for (int j = 0; j < n; ++j, tile += 2) {
-          const uint32_t sv = (tile + 1) % C::kStages, sk = (tile + 2) % C::kStages;
-          ok = mbar_wait(&sh.full[sv], ((tile + 1) / C::kStages) & 1);
-          if (ok && j + 1 < n) ok = mbar_wait(&sh.full[sk], ((tile + 2) / C::kStages) & 1);
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (j >= pc.n[t]) continue;
-            ok = mbar_wait(&sh.p_full[t], np[t] & 1);
-            ++np[t];
-            if (!ok) break;
-            tc_fence_after();
-            product_o(t, sv, j > 0);
-            if (j + 1 < pc.n[t]) product_s(t, sk);
-            else mma_commit(&sh.o_full[t]);
-          }
-          if (!ok) break;
-          mma_commit(&sh.empty[sv]);
-          if (j + 1 < n) mma_commit(&sh.empty[sk]);
-          if (j + 2 == n) mma_commit(&sh.q_empty);
-        }
+          mma_ts(tm + 256 + t * 128, tm + t * 128 + k * 8, b + (k * 2048 >> 4), kDescO,
+                 add || k > 0);
       }
-      if (!ok) fail();
-      mma_commit(&sh.drain);  // no arrival is still on its way when the CTA ends
-      mbar_wait(&sh.drain, 0);
+    };
+    for (; ok && uniform(walk.more()); walk.next(), ++piece) {
+      const Piece pc(walk, tile_tokens);
+      const int nt[2] = {uniform(pc.n[0]), uniform(pc.n[1])};
+      const int n = max(nt[0], nt[1]);
+      uint32_t st = tile % C::kStages;
+      ok = wait(&sh.q_full, piece & 1) && wait(&sh.full[st], (tile / C::kStages) & 1);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (nt[t] > 0) product_s(t, st);
+      commit(&sh.empty[st]);
+      if (n == 1) commit(&sh.q_empty);
+      for (int j = 0; j < n; ++j, tile += 2) {
+        const uint32_t sv = (tile + 1) % C::kStages, sk = (tile + 2) % C::kStages;
+        ok = wait(&sh.full[sv], ((tile + 1) / C::kStages) & 1);
+        if (ok && j + 1 < n) ok = wait(&sh.full[sk], ((tile + 2) / C::kStages) & 1);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || j >= nt[t]) continue;
+          ok = wait(&sh.p_full[t], np[t] & 1);
+          ++np[t];
+          if (!ok) continue;
+          tc_fence_after();
+          product_o(t, sv, j > 0);
+          if (j + 1 < nt[t]) product_s(t, sk);
+          else commit(&sh.o_full[t]);
+        }
+        if (!ok) break;
+        commit(&sh.empty[sv]);
+        if (j + 1 < n) commit(&sh.empty[sk]);
+        if (j + 2 == n) commit(&sh.q_empty);
+      }
     }
-    __syncwarp();
+    if (!ok && lane == 0) fail();
+    commit(&sh.drain);  // no arrival is still on its way when the CTA ends
+    mbar_wait(&sh.drain, 0);
   } else {
     // ------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -318,9 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float mx[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          mx[i] = __uint_as_float(s[i][0]);
+          mx[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
 #pragma unroll
-          for (int e = 1; e < 32; ++e) mx[i] = fmaxf(mx[i], __uint_as_float(s[i][e]));
+          for (int e = 2; e < 32; e += 2)
+            mx[i] = max3(mx[i], __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         if (j == 0) {
@@ -344,25 +357,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float mc = m == -INFINITY ? 0.f : m * c;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // 16 exponentials at a time; the ones before are summed and packed while they run
+        auto exponentials = [&](int q) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            uint32_t* x = &s[q / 2][(q & 1) * 16 + e];
+            const float2 y =
+                fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, mc2);
+            x[0] = __float_as_uint(ex2(y.x));
+            x[1] = __float_as_uint(ex2(y.y));
+          }
+        };
+        exponentials(0);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           uint32_t pk[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int k = 2 * e;
-            const float a = ex2(fmaf(__uint_as_float(s[2 * i + k / 32][k % 32]), c, -mc));
-            const float b = ex2(fmaf(__uint_as_float(s[2 * i + k / 32][k % 32 + 1]), c, -mc));
-            sum[2 * (e & 1)] += a;
-            sum[2 * (e & 1) + 1] += b;
-            pk[e] = pack_bf16(a, b);
+          for (int q = 0; q < 4; ++q) {
+            if (4 * i + q < 7) exponentials(4 * i + q + 1);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const uint32_t* x = &s[(4 * i + q) / 2][(q & 1) * 16 + e];
+              const float2 y = make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+              sum[(e / 2) & 1] = add2(sum[(e / 2) & 1], y);
+              pk[q * 8 + e / 2] = pack_bf16(y.x, y.y);
+            }
           }
           tmem_st32(s_at + 32 * i, pk);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&sh.p_full[t]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[t]);
       }
       if (!ok) break;
       units_seen += max(pc.n[0], pc.n[1]);
