@@ -488,10 +488,11 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 // fill out of bounds (decode.cu). box_inner * 2 must be 128.
 cudaError_t encode_bf16_2d_swizzled(CUtensorMap* map, const void* base, unsigned long long inner,
                                     unsigned long long rows, unsigned box_inner, unsigned box_rows);
-// The same over a dense [outer, mid, inner] tensor.
-cudaError_t encode_bf16_3d_swizzled(CUtensorMap* map, const void* base, unsigned long long inner,
-                                    unsigned long long mid, unsigned long long outer,
-                                    unsigned box_inner, unsigned box_mid, unsigned box_outer);
+// The same in three dimensions, innermost first; strides in bytes of the outer two.
+cudaError_t encode_bf16_3d_swizzled(CUtensorMap* map, const void* base,
+                                    const unsigned long long (&dims)[3],
+                                    const unsigned long long (&strides)[2],
+                                    const unsigned (&box)[3]);
 
 // Per-device helpers (abi.cu).
 int current_device_sm_count();

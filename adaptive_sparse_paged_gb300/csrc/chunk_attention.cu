@@ -23,6 +23,8 @@
 #include "chunk_plan.cuh"
 #include "tc.cuh"
 
+#include <type_traits>
+
 namespace asp {
 namespace {
 
@@ -49,7 +51,7 @@ struct Cfg {
 struct Shared {
   uint64_t q_full, q_empty, drain;
   uint64_t full[8], empty[8];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_full[2];
   ChunkStart start;
   long long scratch[kThreads / 32];
   uint32_t page_mask[kPageMasks];
@@ -97,7 +99,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_tiles = smem;                         // [2][halves][128 rows x 128 B]
-  uint8_t* ring = smem + 2 * C::kTileBytes;        // [stages][halves][128 keys x 128 B]
+  // K: [stages][halves][128 keys x 128 B], V: [stages][pages][halves][P keys x 128 B]
+  uint8_t* ring = smem + 2 * C::kTileBytes;
   Shared& sh = *reinterpret_cast<Shared*>(ring + C::kStages * C::kTileBytes);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -111,7 +114,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);  // the tile's warps
+      mbar_init(&sh.p_half[i], 4);  // the tile's warps
+      mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.o_full[i], 1);
     }
     mbar_fence_init();
@@ -181,11 +185,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             else mbar_arrive(&sh.full[st]);
           }
           __syncwarp();
-          if (good) {
-            uint8_t* dst = ring + st * C::kTileBytes + lane * P * 128;
+          uint8_t* dst = ring + st * C::kTileBytes;
+          if (good && kv == 0) {
 #pragma unroll
             for (int hf = 0; hf < C::kHalves; ++hf)
-              tma_load_2d(dst + hf * 16384, kv == 0 ? &tmK : &tmV, hf * 64, y, &sh.full[st]);
+              tma_load_2d(dst + hf * 16384 + lane * P * 128, &tmK, hf * 64, y, &sh.full[st]);
+          } else if (good) {
+            tma_load_3d(dst + lane * C::kHalves * P * 128, &tmV, 0, y, 0, &sh.full[st]);
           }
         }
         if (!ok) break;
@@ -225,13 +231,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(&sh.s_full[t]);
       }
     };
-    auto product_o = [&](int t, uint32_t st, bool add) {
-      const uint64_t b = smem_desc(r0 + st * C::kTileBytes, 16384);
+    // keys 64 hf .. 64 hf + 63 of the tile
+    auto product_o = [&](int t, uint32_t st, int hf, bool add) {
+      const uint64_t b = smem_desc(r0 + st * C::kTileBytes, P * 128);
       if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kTileKeys / 16; ++k)
-          mma_ts(tm + 256 + t * 128, tm + t * 128 + k * 8, b + (k * 2048 >> 4), kDescO,
-                 add || k > 0);
+        for (int i = 0; i < kTileKeys / 32; ++i) {
+          const int k = hf * (kTileKeys / 32) + i;
+          const uint32_t off = k * 16 / P * (C::kHalves * P * 128) + k * 16 % P * 128;
+          mma_ts(tm + 256 + t * 128, tm + t * 128 + k * 8, b + (off >> 4), kDescO, add || i > 0);
+        }
       }
     };
     for (; ok && uniform(walk.more()); walk.next(), ++piece) {
@@ -250,15 +259,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < n; ++j, tile += 2) {
         const uint32_t sv = (tile + 1) % C::kStages, sk = (tile + 2) % C::kStages;
         ok = wait(&sh.full[sv], ((tile + 1) / C::kStages) & 1);
-        if (ok && j + 1 < n) ok = wait(&sh.full[sk], ((tile + 2) / C::kStages) & 1);
+        bool k_there = false;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!ok || j >= nt[t]) continue;
-          ok = wait(&sh.p_full[t], np[t] & 1);
-          ++np[t];
+          ok = wait(&sh.p_half[t], np[t] & 1);
           if (!ok) continue;
           tc_fence_after();
-          product_o(t, sv, j > 0);
+          product_o(t, sv, 0, j > 0);
+          ok = wait(&sh.p_full[t], np[t] & 1);
+          ++np[t];
+          if (ok && j + 1 < n && !k_there)
+            k_there = ok = wait(&sh.full[sk], ((tile + 2) / C::kStages) & 1);
+          if (!ok) continue;
+          tc_fence_after();
+          product_o(t, sv, 1, true);
           if (j + 1 < nt[t]) product_s(t, sk);
           else commit(&sh.o_full[t]);
         }
@@ -318,10 +333,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(kFull, mbar_wait(&sh.full[tv % C::kStages], (tv / C::kStages) & 1));
             if (!ok) break;
             if (key0 + row >= walk.r.T || !((pages >> (row / P)) & 1)) {
-              uint8_t* v = ring + (tv % C::kStages) * C::kTileBytes + row * 128;
+              uint8_t* v = ring + (tv % C::kStages) * C::kTileBytes +
+                           row / P * (C::kHalves * P * 128) + row % P * 128;
 #pragma unroll
               for (int e = 0; e < 8 * C::kHalves; ++e)
-                *reinterpret_cast<uint4*>(v + (e / 8) * 16384 + (e % 8) * 16) =
+                *reinterpret_cast<uint4*>(v + (e / 8) * (P * 128) + (e % 8) * 16) =
                     make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
@@ -386,12 +402,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           tmem_st32(s_at + 32 * i, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(i == 0 ? &sh.p_half[t] : &sh.p_full[t]);
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[t]);
       }
       if (!ok) break;
       units_seen += max(pc.n[0], pc.n[1]);
@@ -450,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (tid == 0 && walk.u0 == 0) {
-          const int end = chunk_share_of(sh.start.total, gridDim.x, walk.at + walk.units - 1);
+          const int end = sh.start.shares.taker(walk.at + walk.units - 1, blockIdx.x);
           p.joins[blockIdx.x] = ChunkJoin{walk.b, walk.h, walk.item, end - (int)blockIdx.x + 1};
         }
       }
@@ -462,53 +478,73 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_free(tmem, kTmemCols);
 }
 
-// Joins the pieces of the item that CTA blockIdx.x began: rows 32 blockIdx.y to
-// + 31, a warp each. out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
+// Joins the pieces of the item that CTA blockIdx.x began, a warp a row:
+// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i. A lane holds one piece's
+// maximum and sum; the pieces' O rows are added in order, eight loads in flight.
 template <int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const Params p) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, kInFlight = 8;
+  using V = typename std::conditional<E == 4, float4, float2>::type;
   pdl_launch_dependents();
   pdl_wait_predecessor();
   const ChunkJoin jn = p.joins[blockIdx.x];
   if (jn.pieces < 2) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = p.c.g, tpi = kChunkRows / g;
+  const int g = p.c.g, row = blockIdx.y * 8 + warp;
   const ChunkRequest r = chunk_request(p.c, jn.b, nullptr);
+  const int tok = jn.item * (kChunkRows / g) + row / g;
+  if (tok >= r.n) return;
   const size_t slot_floats = chunk_slot_floats(D);
-  for (int i = 0; i < 4; ++i) {
-    const int row = blockIdx.y * 32 + i * 8 + warp;
-    const int tok = jn.item * tpi + row / g;
-    if (tok >= r.n) return;
-    const float* first = p.partials + (size_t)(2 * blockIdx.x + 1) * slot_floats;
-    const float* rest = p.partials + (size_t)(2 * blockIdx.x) * slot_floats;
-    auto part = [&](int k) { return k == 0 ? first : rest + (size_t)(2 * k) * slot_floats; };
-    float M = -INFINITY;
-    for (int k = lane; k < jn.pieces; k += 32) M = fmaxf(M, part(k)[row]);
+  const float* first = p.partials + (size_t)(2 * blockIdx.x + 1) * slot_floats;
+  const float* rest = p.partials + (size_t)(2 * blockIdx.x) * slot_floats;
+  auto part = [&](int k) { return k == 0 ? first : rest + (size_t)(2 * k) * slot_floats; };
+  float M = -INFINITY;
+  for (int k = lane; k < jn.pieces; k += 32) M = fmaxf(M, part(k)[row]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-    const float ref = M == -INFINITY ? 0.f : M;
-    float acc[E], L = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int k = 0; k < jn.pieces; ++k) {
-      const float* q = part(k);
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+  const float ref = M == -INFINITY ? 0.f : M;
+  float acc[E] = {}, L = 0.f;
+  for (int k0 = 0; k0 < jn.pieces; k0 += 32) {
+    float w = 0.f, wl = 0.f;  // a piece none of whose keys count for this row adds nothing
+    if (k0 + lane < jn.pieces) {
+      const float* q = part(k0 + lane);
       const float mk = q[row];
-      if (mk == -INFINITY) continue;  // no key of that piece counts for this row
-      const float w = ex2(mk - ref);
-      L += w * q[kChunkRows + row];
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        acc[e] += w * q[2 * kChunkRows + (size_t)row * D + lane * E + e];
+      if (mk != -INFINITY) {
+        w = ex2(mk - ref);
+        wl = w * q[kChunkRows + row];
+      }
     }
-    const float inv = L > 0.f ? 1.0f / L : L;
-    const size_t at = (size_t)(r.row0 + tok) * p.Hq + jn.h * g + row % g;
+    const uint32_t some = __ballot_sync(kFull, w != 0.f);  // true for NaN too
+    const int n = min(32, jn.pieces - k0);
+    for (int k = 0; k < n; k += kInFlight) {
+      float o[kInFlight][E];
 #pragma unroll
-    for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<uint32_t*>(p.out + at * D + lane * E + e) =
-          pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0)
-      p.lse[at] = L == 0.f ? -INFINITY : M * 0.69314718055994530942f + logf(L);
+      for (int u = 0; u < kInFlight; ++u) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[u][e] = 0.f;
+        if (k + u < n && (some >> (k + u) & 1))
+          *reinterpret_cast<V*>(o[u]) = *reinterpret_cast<const V*>(
+              part(k0 + k + u) + 2 * kChunkRows + (size_t)row * D + lane * E);
+      }
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        const float wk = __shfl_sync(kFull, w, (k + u) & 31);
+        if (k + u >= n) continue;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, o[u][e], acc[e]);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) wl += __shfl_xor_sync(kFull, wl, o);
+    L += wl;
   }
+  const float inv = L > 0.f ? 1.0f / L : L;
+  const size_t at = (size_t)(r.row0 + tok) * p.Hq + jn.h * g + row % g;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(p.out + at * D + lane * E + e) =
+        pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0) p.lse[at] = L == 0.f ? -INFINITY : M * 0.69314718055994530942f + logf(L);
 }
 
 template <int D, int P>
@@ -518,11 +554,17 @@ cudaError_t launch_t(const ChunkAttentionArgs& a, cudaStream_t stream) {
   const int g = kv.num_q_heads / kv.num_kv_heads;
   const unsigned long long rows = (unsigned long long)kv.num_phys_pages * kv.num_kv_heads * P;
   CUtensorMap tq, tk, tv;
-  cudaError_t e = encode_bf16_3d_swizzled(&tq, a.q, D, kv.num_q_heads, a.num_tokens, 64, g, 128 / g);
+  cudaError_t e = encode_bf16_3d_swizzled(
+      &tq, a.q, {D, (unsigned long long)kv.num_q_heads, (unsigned long long)a.num_tokens},
+      {2 * D, 2ull * D * kv.num_q_heads}, {64, (unsigned)g, (unsigned)(kTileRows / g)});
   if (e != cudaSuccess) return e;
   if ((e = encode_bf16_2d_swizzled(&tk, kv.k_cache, D, rows, 64, P)) != cudaSuccess) return e;
-  if ((e = encode_bf16_2d_swizzled(&tv, kv.v_cache, D, rows, 64, P)) != cudaSuccess) return e;
-  Params p{{a.q_offsets, kv.seq_lens, kv.batch, kv.num_kv_heads, g, kv.max_pages, P, a.num_tokens},
+  // a V page in one box: [half][P rows][64 channels]
+  if ((e = encode_bf16_3d_swizzled(&tv, kv.v_cache, {64, rows, D / 64}, {2 * D, 128},
+                                   {64, (unsigned)P, (unsigned)(D / 64)})) != cudaSuccess)
+    return e;
+  Params p{{a.q_offsets, kv.seq_lens, kv.batch, kv.num_kv_heads, g, kv.max_pages, P, a.num_tokens,
+            chunk_inverse(a.num_sms)},
            kv.block_table, a.out, a.lse, a.joins, a.partials, a.err, kv.num_q_heads,
            kv.num_phys_pages, a.sm_scale, a.sm_scale * 1.4426950408889634f};
   if ((e = set_max_dynamic_smem((const void*)chunk_attention_kernel<D, P>, (int)C::kSmem)) !=
@@ -532,7 +574,10 @@ cudaError_t launch_t(const ChunkAttentionArgs& a, cudaStream_t stream) {
   e = launch_pdl(chunk_attention_kernel<D, P>, dim3(a.num_sms), dim3(kThreads), C::kSmem, stream, tq,
                  tk, tv, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(chunk_join_kernel<D>, dim3(a.num_sms, kChunkRows / 32), dim3(256), 0, stream, p);
+  // an item has no more rows than the call
+  const long long item_rows = min((long long)a.num_tokens * g, (long long)kChunkRows);
+  return launch_pdl(chunk_join_kernel<D>, dim3(a.num_sms, (unsigned)((item_rows + 7) / 8)), dim3(256),
+                    0, stream, p);
 }
 
 }  // namespace

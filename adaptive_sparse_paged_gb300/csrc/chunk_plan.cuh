@@ -22,6 +22,7 @@ struct ChunkDims {
   const int32_t* q_offsets;
   const int32_t* seq_lens;
   int B, Hkv, g, max_pages, P, num_tokens;
+  unsigned long long inv_ctas;  // chunk_inverse of the grid
 };
 
 // One request: its tokens, and its rows.
@@ -94,21 +95,34 @@ struct KeyCut {
   }
 };
 
+// Even shares of `total` units over G CTAs: the first r = total % G take q + 1, the
+// others q = total / G. The division is a product with 2^64 / G rounded up, which is
+// exact for totals under 2^63 / G (a 64-bit division is a called routine, whose code
+// alone takes microseconds to fetch at a kernel's start).
+struct ChunkShares {
+  long long q;
+  int r;
+  __device__ __forceinline__ ChunkShares() {}
+  __device__ __forceinline__ ChunkShares(long long total, int G, unsigned long long inv) {
+    q = (long long)__umul64hi((unsigned long long)total, inv);
+    r = (int)(total - q * G);
+  }
+  __device__ __forceinline__ long long begin(int c) const { return c * q + min(c, r); }
+  // The CTA that takes `unit`, which CTA c or a later one does.
+  __device__ __forceinline__ int taker(long long unit, int c) const {
+    while (begin(c + 1) <= unit) ++c;
+    return c;
+  }
+};
+// 2^64 / G rounded up (G > 1: the devices of this library have 152 SMs).
+inline unsigned long long chunk_inverse(int G) { return ~0ull / (unsigned)G + 1; }
+
 // Where a CTA's share begins: unit `u` of item (b, h, item); and the share.
 struct ChunkStart {
   int b, h, item, u;
-  long long first, count, total;
+  long long first, count;
+  ChunkShares shares;
 };
-
-// Even shares of `total` units over G CTAs: the first total % G take one more.
-__device__ __forceinline__ long long chunk_share_begin(long long total, int G, int c) {
-  const long long q = total / G, r = total % G;
-  return c * q + (c < r ? c : r);
-}
-__device__ __forceinline__ int chunk_share_of(long long total, int G, long long unit) {
-  const long long q = total / G, r = total % G, big = r * (q + 1);
-  return (int)(unit < big ? unit / (q + 1) : r + (unit - big) / q);
-}
 
 // Fills *start (shared memory) for this CTA; every thread of the block calls it.
 // scratch: one long long for each warp.
@@ -137,8 +151,8 @@ __device__ __forceinline__ void chunk_plan(const ChunkDims& c, ChunkStart* start
     total += scratch[w];
   }
   before += x - mine;
-  const long long first = chunk_share_begin(total, gridDim.x, blockIdx.x);
-  const long long count = chunk_share_begin(total, gridDim.x, blockIdx.x + 1) - first;
+  const ChunkShares shares(total, gridDim.x, c.inv_ctas);
+  const long long first = shares.begin(blockIdx.x), count = shares.begin(blockIdx.x + 1) - first;
   if (count > 0 && first >= before && first < before + mine) {
     long long at = before;
     for (int b = b0; b < b1; ++b) {
@@ -149,15 +163,15 @@ __device__ __forceinline__ void chunk_plan(const ChunkDims& c, ChunkStart* start
         at += c.Hkv * head;
         continue;
       }
-      const long long in_b = first - at;
-      const int h = (int)(in_b / head);
-      const long long in_h = in_b - h * head;
+      int h = 0;
+      long long in_h = first - at;
+      for (; in_h >= head; in_h -= head) ++h;  // fewer than Hkv <= 8 steps
       int lo = 0, hi = items - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (Cut::before(r, c.g, mid) <= in_h) lo = mid; else hi = mid - 1;
       }
-      *start = ChunkStart{b, h, lo, (int)(in_h - Cut::before(r, c.g, lo)), first, count, total};
+      *start = ChunkStart{b, h, lo, (int)(in_h - Cut::before(r, c.g, lo)), first, count, shares};
       break;
     }
   }

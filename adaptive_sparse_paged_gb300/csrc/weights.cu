@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           p.partials[(size_t)(2 * blockIdx.x + (walk.u0 == 0 ? 1 : 0)) * kTileKeys + row] = sum;
           if (tid == 0 && walk.u0 == 0) {
-            const int end = chunk_share_of(sh.start.total, gridDim.x, walk.at + walk.units - 1);
+            const int end = sh.start.shares.taker(walk.at + walk.units - 1, blockIdx.x);
             p.joins[blockIdx.x] =
                 ChunkJoin{walk.b, walk.h, walk.item, end - (int)blockIdx.x + 1};
           }
@@ -332,11 +332,13 @@ cudaError_t launch_chunk_t(const WeightArgs& a, cudaStream_t stream) {
   const int n = a.num_tokens > 0 ? a.num_tokens : 1;
   const void* q = a.num_tokens > 0 ? (const void*)a.q : (const void*)kv.k_cache;
   cudaError_t e =
-      encode_bf16_3d_swizzled(&tq, q, D, kv.num_q_heads, n, 64, g, kTileRows / g);
+      encode_bf16_3d_swizzled(&tq, q, {D, (unsigned long long)kv.num_q_heads, (unsigned long long)n},
+                              {2 * D, 2ull * D * kv.num_q_heads},
+                              {64, (unsigned)g, (unsigned)(kTileRows / g)});
   if (e != cudaSuccess) return e;
   if ((e = encode_bf16_2d_swizzled(&tk, kv.k_cache, D, cache_rows, 64, P)) != cudaSuccess) return e;
   ChunkParams p{{a.q_offsets, kv.seq_lens, kv.batch, kv.num_kv_heads, g, kv.max_pages, P,
-                 a.num_tokens},
+                 a.num_tokens, chunk_inverse(a.num_sms)},
                 kv.block_table, a.lse, a.w_in, a.w_out, a.joins, a.partials, a.err, kv.num_q_heads,
                 kv.num_phys_pages, a.sm_scale * kLog2e, a.decay};
   constexpr size_t smem = chunk_smem<D>();
