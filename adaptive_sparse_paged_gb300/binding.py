@@ -10,6 +10,7 @@ any function fails loudly (build it with adaptive_sparse_paged_gb300.build).
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -80,6 +81,8 @@ _lock = threading.Lock()
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Loads libasp.so once (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -135,11 +138,25 @@ def _check(status: int, where: str) -> None:
 
 
 def _stream_ptr(device: torch.device, stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """Makes `device` the current one; entering a device that already is costs more than a check."""
+    if torch.cuda.current_device() == device.index:
+        return _HERE
+    return torch.cuda.device(device)
 
 
 def _need(t: torch.Tensor, name: str, dtype, device, shape=None):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -207,14 +224,14 @@ def asp_abi_version() -> int:
 
 def asp_workspace_size(kv: PagedKV) -> int:
     out = ctypes.c_size_t(0)
-    with torch.cuda.device(kv.device):
+    with _on(kv.device):
         _check(load_library().asp_workspace_size(kv.ref, ctypes.byref(out)), "asp_workspace_size")
     return int(out.value)
 
 
 def asp_workspace_init(ws: torch.Tensor, stream=None) -> None:
     _need(ws, "ws", torch.uint8, ws.device)
-    with torch.cuda.device(ws.device):
+    with _on(ws.device):
         _check(load_library().asp_workspace_init(ws.data_ptr(), ws.numel(),
                                                  _stream_ptr(ws.device, stream)),
                "asp_workspace_init")
@@ -229,7 +246,7 @@ def asp_page_summarize(kv: PagedKV, mode: int, k_new, v_new, ws: torch.Tensor, s
     else:
         kp = vp = None
     _need(ws, "ws", torch.uint8, kv.device)
-    with torch.cuda.device(kv.device):
+    with _on(kv.device):
         _check(load_library().asp_page_summarize(kv.ref, int(mode), kp, vp, ws.data_ptr(),
                                                  ws.numel(), _stream_ptr(kv.device, stream)),
                "asp_page_summarize")
@@ -242,7 +259,7 @@ def asp_coverage_select(kv: PagedKV, q: torch.Tensor, gamma: float, budget: int,
     _need(lists, "lists", torch.int32, kv.device, (kv.batch, kv.num_kv_heads, kv.max_pages))
     _need(lens, "lens", torch.int32, kv.device, (kv.batch, kv.num_kv_heads))
     _need(ws, "ws", torch.uint8, kv.device)
-    with torch.cuda.device(kv.device):
+    with _on(kv.device):
         _check(load_library().asp_coverage_select(
             kv.ref, q.data_ptr(), ctypes.c_float(gamma), int(budget), lists.data_ptr(),
             lens.data_ptr(), ws.data_ptr(), ws.numel(), _stream_ptr(kv.device, stream)),
@@ -260,7 +277,7 @@ def asp_coverage_select_append(kv: PagedKV, k_new: torch.Tensor, v_new: torch.Te
     _need(lists, "lists", torch.int32, kv.device, (kv.batch, kv.num_kv_heads, kv.max_pages))
     _need(lens, "lens", torch.int32, kv.device, (kv.batch, kv.num_kv_heads))
     _need(ws, "ws", torch.uint8, kv.device)
-    with torch.cuda.device(kv.device):
+    with _on(kv.device):
         _check(load_library().asp_coverage_select_append(
             kv.ref, k_new.data_ptr(), v_new.data_ptr(), q.data_ptr(), ctypes.c_float(gamma),
             int(budget), lists.data_ptr(), lens.data_ptr(), ws.data_ptr(), ws.numel(),
@@ -270,7 +287,7 @@ def asp_coverage_select_append(kv: PagedKV, k_new: torch.Tensor, v_new: torch.Te
 def asp_select_plan(kv: PagedKV, gamma: float, budget: int = 0, append: bool = False):
     """(kernels one selection call launches, cluster CTAs per segment or 0)."""
     k, c = ctypes.c_int32(0), ctypes.c_int32(0)
-    with torch.cuda.device(kv.device):
+    with _on(kv.device):
         _check(load_library().asp_select_plan(kv.ref, ctypes.c_float(gamma), int(budget),
                                               int(bool(append)), ctypes.byref(k),
                                               ctypes.byref(c)), "asp_select_plan")
@@ -284,7 +301,7 @@ def asp_page_scores(kv: PagedKV, q: torch.Tensor, scores: torch.Tensor, ws: torc
     _need(scores, "scores", torch.float32, kv.device,
           (kv.batch, kv.num_kv_heads, kv.max_pages))
     _need(ws, "ws", torch.uint8, kv.device)
-    with torch.cuda.device(kv.device):
+    with _on(kv.device):
         _check(load_library().asp_page_scores(kv.ref, q.data_ptr(), scores.data_ptr(),
                                               ws.data_ptr(), ws.numel(),
                                               _stream_ptr(kv.device, stream)),
@@ -300,7 +317,7 @@ def asp_sparse_decode(kv: PagedKV, q: torch.Tensor, lists: torch.Tensor, lens: t
     _need(out, "out", torch.float32, kv.device, (kv.batch, kv.num_q_heads, kv.head_dim))
     _need(lse, "lse", torch.float32, kv.device, (kv.batch, kv.num_q_heads))
     _need(ws, "ws", torch.uint8, kv.device)
-    with torch.cuda.device(kv.device):
+    with _on(kv.device):
         _check(load_library().asp_sparse_decode(
             kv.ref, q.data_ptr(), lists.data_ptr(), lens.data_ptr(), ctypes.c_float(sm_scale),
             out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(),
@@ -323,7 +340,7 @@ def asp_coverage_select_noalloc(kv: PagedKV, q: torch.Tensor, gamma: float, budg
     if dev_error is not None:
         _need(dev_error, "dev_error", torch.int32, kv.device, (1,))
         err_ptr = dev_error.data_ptr()
-    with torch.cuda.device(kv.device):
+    with _on(kv.device):
         _check(load_library().asp_coverage_select_noalloc(
             kv.ref, q.data_ptr(), ctypes.c_float(gamma), int(budget), lists.data_ptr(),
             lens.data_ptr(), err_ptr, _stream_ptr(kv.device, stream)),
@@ -383,7 +400,7 @@ def asp_norm_rotate_append(kv: PagedKV, qkv: torch.Tensor, q_offsets, positions,
         return None if t is None else t.data_ptr()
 
     half = q_out.dtype == torch.bfloat16
-    with torch.cuda.device(kv.device):
+    with _on(kv.device):
         _check(load_library().asp_norm_rotate_append(
             kv.ref, _rows_ptr(qkv), ptr(q_offsets), n, ptr(positions), ptr(q_weight),
             ptr(k_weight), ctypes.c_float(eps), ptr(inv_freq),
@@ -407,7 +424,7 @@ def asp_chunk_attention(kv: PagedKV, q: torch.Tensor, q_offsets: torch.Tensor, s
     _need(out, "out", torch.bfloat16, kv.device, (n, kv.num_q_heads, kv.head_dim))
     _need(lse, "lse", torch.float32, kv.device, (n, kv.num_q_heads))
     _need(ws, "ws", torch.uint8, kv.device)
-    with torch.cuda.device(kv.device):
+    with _on(kv.device):
         _check(load_library().asp_chunk_attention(
             kv.ref, _rows_ptr(q), q_offsets.data_ptr(), n, ctypes.c_float(sm_scale),
             _rows_ptr(out), _rows_ptr(lse), ws.data_ptr(), ws.numel(),
@@ -423,7 +440,7 @@ def asp_chunk_weights(kv: PagedKV, q: torch.Tensor, q_offsets: torch.Tensor, lse
     _need(lse, "lse", torch.float32, kv.device, (n, kv.num_q_heads))
     w_ptr = _need_weights(kv, w_in, w_out)
     _need(ws, "ws", torch.uint8, kv.device)
-    with torch.cuda.device(kv.device):
+    with _on(kv.device):
         _check(load_library().asp_chunk_weights(
             kv.ref, _rows_ptr(q), q_offsets.data_ptr(), n, _rows_ptr(lse),
             ctypes.c_float(sm_scale), ctypes.c_float(decay), w_ptr, w_out.data_ptr(),
@@ -443,7 +460,7 @@ def asp_decode_weights(kv: PagedKV, q: torch.Tensor, lists, lens, lse: torch.Ten
     _need(lse, "lse", torch.float32, kv.device, (kv.batch, kv.num_q_heads))
     w_ptr = _need_weights(kv, w_in, w_out)
     _need(ws, "ws", torch.uint8, kv.device)
-    with torch.cuda.device(kv.device):
+    with _on(kv.device):
         _check(load_library().asp_decode_weights(
             kv.ref, q.data_ptr(), lists_ptr, lens_ptr, lse.data_ptr(), ctypes.c_float(sm_scale),
             ctypes.c_float(decay), w_ptr, w_out.data_ptr(), ws.data_ptr(), ws.numel(),
@@ -460,7 +477,7 @@ def asp_weight_evict(kv: PagedKV, weights: torch.Tensor, keep: int, recent: int,
     _need(kept, "kept", torch.int32, kv.device, (kv.batch, kv.num_kv_heads, int(keep)))
     _need(new_lens, "new_lens", torch.int32, kv.device, (kv.batch,))
     _need(ws, "ws", torch.uint8, kv.device)
-    with torch.cuda.device(kv.device):
+    with _on(kv.device):
         _check(load_library().asp_weight_evict(
             kv.ref, weights.data_ptr(), int(keep), int(recent), dst_table.data_ptr(),
             w_out.data_ptr(), kept.data_ptr(), new_lens.data_ptr(), ws.data_ptr(), ws.numel(),
@@ -472,7 +489,7 @@ def asp_selftest_wait_timeout(ws: torch.Tensor, stream=None) -> None:
     and sets ASP_DEVERR_TIMEOUT in `ws`'s error word (read it with
     asp_get_device_error)."""
     _need(ws, "ws", torch.uint8, ws.device)
-    with torch.cuda.device(ws.device):
+    with _on(ws.device):
         _check(load_library().asp_selftest_wait_timeout(ws.data_ptr(), ws.numel(),
                                                         _stream_ptr(ws.device, stream)),
                "asp_selftest_wait_timeout")
@@ -481,7 +498,7 @@ def asp_selftest_wait_timeout(ws: torch.Tensor, stream=None) -> None:
 def asp_get_device_error(ws: torch.Tensor, stream=None) -> int:
     """Synchronises the stream and returns (and clears) the device error mask."""
     code = ctypes.c_uint32(0)
-    with torch.cuda.device(ws.device):
+    with _on(ws.device):
         st = load_library().asp_get_device_error(ws.data_ptr(), ctypes.byref(code),
                                                  _stream_ptr(ws.device, stream))
     if st not in (ASP_OK, ASP_EDEVICE):
