@@ -166,10 +166,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int n_pages = ceil_div(walk.r.T, P);
       const int32_t* bt = p.bt + (size_t)walk.b * p.c.max_pages;
-      for (int j = 0; j < n; ++j) {
+      // the tile's physical pages, read one tile ahead
+      auto look_up = [&](int j) {
         const int page = (walk.u0 + j) * kPages + lane;
-        const bool have = lane < kPages && page < n_pages;
-        const int phys = have ? bt[page] : 0;
+        return lane < kPages && page < n_pages ? bt[page] : 0;
+      };
+      int next = look_up(0);
+      for (int j = 0; j < n; ++j) {
+        const bool have = lane < kPages && (walk.u0 + j) * kPages + lane < n_pages;
+        const int phys = next;
+        next = look_up(j + 1);
         const bool good = have && phys >= 0 && phys < p.num_phys;
         if (have && !good) report(p.err, ASP_DEVERR_PAGE_RANGE);
         const uint32_t mask = __ballot_sync(kFull, good);

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kSumBufs; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.s_empty[i], 128);
+      mbar_init(&sh.s_empty[i], 4);  // a warpgroup's warps
     }
     mbar_init(&sh.drain, 1);
     mbar_fence_init();
@@ -152,21 +152,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++kt;
       const int tile0 = KeyCut::first_tile(walk.r, g, walk.item) + walk.u0;
-      for (int j = 0; j < walk.u1 - walk.u0; ++j, ++rt) {
+      const int steps = walk.u1 - walk.u0;
+      // the rows' lse, four a lane, read one step ahead
+      float next[4];
+      auto fetch = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = lane * 4 + i, tok = (tile0 + j) * tile_tokens + r / g;
+          next[i] = tok < walk.r.n
+                        ? p.lse[(size_t)(walk.r.row0 + tok) * p.Hq + walk.h * g + r % g]
+                        : -INFINITY;
+        }
+      };
+      fetch(0);
+      for (int j = 0; j < steps; ++j, ++rt) {
         const uint32_t rb = rt % kRowBufs;
         const int tok0 = (tile0 + j) * tile_tokens;
-        // the rows' lse while the buffer drains
         float nl[4];
         bool none = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = lane * 4 + i, tok = tok0 + r / g;
-          const float l = tok < walk.r.n
-                              ? p.lse[(size_t)(walk.r.row0 + tok) * p.Hq + walk.h * g + r % g]
-                              : -INFINITY;
-          nl[i] = l == -INFINITY ? -INFINITY : -l * kLog2e;
-          none |= l == -INFINITY;
+          nl[i] = next[i] == -INFINITY ? -INFINITY : -next[i] * kLog2e;
+          none |= next[i] == -INFINITY;
         }
+        if (j + 1 < steps) fetch(j + 1);
         ok = __all_sync(kFull, mbar_wait(&sh.r_empty[rb], ((rt / kRowBufs) & 1) ^ 1));
         if (!ok) break;
         *reinterpret_cast<float4*>(&sh.lse[rt % kLseRing][lane * 4]) =
@@ -191,38 +200,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      constexpr uint32_t kDesc = mma_desc(kTileKeys, kTileRows, false);
-      const uint32_t k0 = smem_u32(keys), r0 = smem_u32(rows);
-      uint32_t kt = 0, rt = 0;
-      bool ok = true;
-      for (; ok && walk.more(); walk.next()) {
-        if (walk.r.n == 0) continue;
-        const uint32_t kb = kt % kKeyBufs;
-        ok = mbar_wait(&sh.k_full[kb], (kt / kKeyBufs) & 1);
-        for (int j = 0; ok && j < walk.u1 - walk.u0; ++j, ++rt) {
-          const uint32_t rb = rt % kRowBufs, sb = rt % kSumBufs;
-          ok = mbar_wait(&sh.s_empty[sb], ((rt / kSumBufs) & 1) ^ 1) &&
-               mbar_wait(&sh.r_full[rb], (rt / kRowBufs) & 1);
-          if (!ok) break;
-          tc_fence_after();
+    constexpr uint32_t kDesc = mma_desc(kTileKeys, kTileRows, false);
+    const uint32_t k0 = uniform(smem_u32(keys)), r0 = uniform(smem_u32(rows));
+    const uint32_t tm = uniform(tmem);
+    uint32_t kt = 0, rt = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(kFull, mbar_wait(bar, parity)) != 0;
+    };
+    for (; ok && uniform(walk.more()); walk.next()) {
+      if (uniform(walk.r.n) == 0) continue;
+      const uint32_t kb = kt % kKeyBufs;
+      const int steps = uniform(walk.u1 - walk.u0);
+      ok = wait(&sh.k_full[kb], (kt / kKeyBufs) & 1);
+      for (int j = 0; ok && j < steps; ++j, ++rt) {
+        const uint32_t rb = rt % kRowBufs, sb = rt % kSumBufs;
+        ok = wait(&sh.s_empty[sb], ((rt / kSumBufs) & 1) ^ 1) &&
+             wait(&sh.r_full[rb], (rt / kRowBufs) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t a = smem_desc(k0 + kb * C::kTileBytes, 16);
+        const uint64_t b = smem_desc(r0 + rb * C::kTileBytes, 16);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-            mma_ss(tmem + sb * 128, smem_desc(k0 + kb * C::kTileBytes + off, 16),
-                   smem_desc(r0 + rb * C::kTileBytes + off, 16), kDesc, k > 0);
+            const uint32_t off = ((k / 4) * 16384 + (k % 4) * 32) >> 4;
+            mma_ss(tm + sb * 128, a + off, b + off, kDesc, k > 0);
           }
           mma_commit(&sh.s_full[sb]);
           mma_commit(&sh.r_empty[rb]);
         }
-        mma_commit(&sh.k_empty[kb]);
-        ++kt;
       }
-      if (!ok) report(p.err, ASP_DEVERR_TIMEOUT);
-      mma_commit(&sh.drain);  // no arrival is still on its way when the CTA ends
-      mbar_wait(&sh.drain, 0);
+      if (elect_one()) mma_commit(&sh.k_empty[kb]);
+      ++kt;
     }
-    __syncwarp();
+    if (!ok && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
+    if (elect_one()) mma_commit(&sh.drain);  // no arrival is still on its way when the CTA ends
+    mbar_wait(&sh.drain, 0);
   } else if (warp < kLoadWarp) {
     // ------------------------------------------------------------ sums
     const int wg = warp >> 2, row = tid & 127;
@@ -250,7 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) tmem_wait_ld(s[i]);
           tc_fence_before();
-          mbar_arrive(&sh.s_empty[sb]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.s_empty[sb]);
           const float* nl = sh.lse[rt % kLseRing];
           // rows from `lo` on see this key
           const int lo = (slot - first_new - (tile0 + j) * tile_tokens) * g;
@@ -265,11 +280,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 part[i] += 32 * i + e >= lo && l != -INFINITY ? x : 0.f;
               }
           } else {
+            const float2 c2 = make_float2(c, c);
+            float2 two[4] = {};
+            // 16 exponentials at a time; the ones before are summed while they run
+            auto exponentials = [&](int q) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+              for (int e = 0; e < 16; e += 4) {
+                const float4 l = *reinterpret_cast<const float4*>(nl + 16 * q + e);
+                uint32_t* x = &s[q / 2][(q & 1) * 16 + e];
+                const float2 y0 = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                                       c2, make_float2(l.x, l.y));
+                const float2 y1 = fma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                                       c2, make_float2(l.z, l.w));
+                x[0] = __float_as_uint(ex2(y0.x));
+                x[1] = __float_as_uint(ex2(y0.y));
+                x[2] = __float_as_uint(ex2(y1.x));
+                x[3] = __float_as_uint(ex2(y1.y));
+              }
+            };
+            exponentials(0);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                part[i] += ex2(fmaf(__uint_as_float(s[i][e]), c, nl[32 * i + e]));
+            for (int q = 0; q < 8; ++q) {
+              if (q < 7) exponentials(q + 1);
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                const uint32_t* x = &s[q / 2][(q & 1) * 16 + e];
+                two[(e / 2) & 3] = add2(two[(e / 2) & 3], make_float2(__uint_as_float(x[0]),
+                                                                      __uint_as_float(x[1])));
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) part[i] = two[i].x + two[i].y;
           }
           sum += (part[0] + part[1]) + (part[2] + part[3]);
         }
@@ -633,37 +674,39 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     if (!ok && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
   } else if (warp == kDecMma) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      constexpr uint32_t kDesc = mma_desc(kTileKeys, kQueryCols, false);
-      const uint32_t r0 = smem_u32(ring), q0 = smem_u32(queries);
-      uint32_t kt = 0, seg = 0;
-      bool ok = true;
-      for (; ok && walk.more(); walk.next_segment(), ++seg) {
-        const int buf = seg & 1, run = walk.run();
-        ok = mbar_wait(&sh.q_full[buf], (seg >> 1) & 1);
-        for (int j = 0; ok && j < run; ++j, ++kt) {
-          const uint32_t st = kt % C::kStages, sb = kt % kSumBufs;
-          ok = mbar_wait(&sh.s_empty[sb], ((kt / kSumBufs) & 1) ^ 1) &&
-               mbar_wait(&sh.full[st], (kt / C::kStages) & 1);
-          if (!ok) break;
-          tc_fence_after();
+    constexpr uint32_t kDesc = mma_desc(kTileKeys, kQueryCols, false);
+    const uint32_t r0 = uniform(smem_u32(ring)), q0 = uniform(smem_u32(queries));
+    const uint32_t tm = uniform(tmem);
+    uint32_t kt = 0, seg = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(kFull, mbar_wait(bar, parity)) != 0;
+    };
+    for (; ok && uniform(walk.more()); walk.next_segment(), ++seg) {
+      const int buf = seg & 1, run = uniform(walk.run());
+      ok = wait(&sh.q_full[buf], (seg >> 1) & 1);
+      for (int j = 0; ok && j < run; ++j, ++kt) {
+        const uint32_t st = kt % C::kStages, sb = kt % kSumBufs;
+        ok = wait(&sh.s_empty[sb], ((kt / kSumBufs) & 1) ^ 1) &&
+             wait(&sh.full[st], (kt / C::kStages) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t a = smem_desc(r0 + st * C::kTileBytes, 16);
+        const uint64_t b = smem_desc(q0 + buf * C::kQueryBytes, 16);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ss(tmem + sb * kQueryCols,
-                   smem_desc(r0 + st * C::kTileBytes + (k / 4) * 16384 + (k % 4) * 32, 16),
-                   smem_desc(q0 + buf * C::kQueryBytes + (k / 4) * (kQueryRows * 128) + (k % 4) * 32,
-                             16),
-                   kDesc, k > 0);
+            mma_ss(tm + sb * kQueryCols, a + (((k / 4) * 16384 + (k % 4) * 32) >> 4),
+                   b + (((k / 4) * (kQueryRows * 128) + (k % 4) * 32) >> 4), kDesc, k > 0);
           mma_commit(&sh.s_full[sb]);
           mma_commit(&sh.empty[st]);
         }
-        mma_commit(&sh.q_empty[buf]);
       }
-      if (!ok) report(p.err, ASP_DEVERR_TIMEOUT);
-      mma_commit(&sh.drain);  // no arrival is still on its way when the CTA ends
-      mbar_wait(&sh.drain, 0);
+      if (elect_one()) mma_commit(&sh.q_empty[buf]);
     }
-    __syncwarp();
+    if (!ok && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
+    if (elect_one()) mma_commit(&sh.drain);  // no arrival is still on its way when the CTA ends
+    mbar_wait(&sh.drain, 0);
   } else {
     // ------------------------------------------------------------ sums
     const uint32_t lanes = (uint32_t)warp << 21;
