@@ -23,19 +23,17 @@
 #include "chunk_plan.cuh"
 #include "tc.cuh"
 
-#include <type_traits>
-
 namespace asp {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-// Two softmax warpgroups; loader, issuer and two idle warps that make up the
-// third. 384 threads start with 168 registers; a row of 128 logits wants more,
+// Two softmax warpgroups; loader, issuer, the warp that hands out pieces and an idle
+// one make up the third. 384 threads start with 168 registers; a row of 128 logits wants more,
 // so the third warpgroup gives up 96 a thread and the others take 48:
 // 128 * 72 + 256 * 216 = 384 * 168.
 constexpr int kThreads = 384;
 constexpr int kRegsSoftmax = 216, kRegsRest = 72;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kTaskWarp = 10;
 constexpr float kMoveLog2 = 8.0f;     // the maximum moves when it grows by more than 2^8
 constexpr int kPageMasks = 8;         // units whose page masks are kept at once
 constexpr uint32_t kTmemCols = 512;   // S of two tiles (128 each), O of two tiles (128 each)
@@ -45,36 +43,20 @@ struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kTileBytes = kHalves * 128 * 128;  // 128 rows x d bf16, swizzled halves
   static constexpr int kStages = D == 128 ? 5 : 8;
-  static constexpr size_t kSmem = 1024 + (2 + kStages) * (size_t)kTileBytes + 512;
+  static constexpr size_t kSmem = 1024 + (2 + kStages) * (size_t)kTileBytes + 1024;
 };
 
 struct Shared {
   uint64_t q_full, q_empty, drain;
   uint64_t full[8], empty[8];
   uint64_t s_full[2], p_half[2], p_full[2], o_full[2];
+  ChunkTasks tasks;
   ChunkStart start;
   long long scratch[kThreads / 32];
   uint32_t page_mask[kPageMasks];
   uint32_t tmem;
-  int failed;
 };
-static_assert(sizeof(Shared) <= 512, "the tail of the dynamic shared memory");
-
-// The current piece's tokens of the chunk, [tok0, last), and the units that its
-// two tiles of rows need.
-struct Piece {
-  int tok0, last, n[2];
-  __device__ __forceinline__ Piece(const ChunkWalk<RowCut>& w, int tile_tokens) {
-    tok0 = w.item * 2 * tile_tokens;
-    last = min(w.r.n, tok0 + 2 * tile_tokens);
-    for (int t = 0; t < 2; ++t) {
-      const int end = min(last, tok0 + (t + 1) * tile_tokens);
-      n[t] = end > tok0 + t * tile_tokens
-                 ? max(0, min(w.u1, RowCut::units_to(w.r, end - 1)) - w.u0)
-                 : 0;
-    }
-  }
-};
+static_assert(sizeof(Shared) <= 1024, "the tail of the dynamic shared memory");
 
 struct Params {
   ChunkDims c;
@@ -118,8 +100,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.o_full[i], 1);
     }
+    chunk_tasks_init(sh.tasks, 10);  // loader, issuer, eight softmax warps
     mbar_fence_init();
-    sh.failed = 0;
+  }
+  if (tid == kLoadWarp * 32) {
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
   }
   if (warp == kMmaWarp) tmem_alloc(&sh.tmem, kTmemCols);
   tc_fence_before();
@@ -130,56 +117,65 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait_predecessor();
   const uint32_t tmem = sh.tmem;
   chunk_plan<RowCut>(p.c, &sh.start, sh.scratch, p.err);
-  ChunkWalk<RowCut> walk(p.c, sh.start);
   const int g = p.c.g, tile_tokens = kTileRows / g;
-  auto fail = [&] {
-    report(p.err, ASP_DEVERR_TIMEOUT);
-    *(volatile int*)&sh.failed = 1;
-  };
+  ChunkReader reader(sh.tasks);
+  ChunkTask task;  // x: units of its two tiles of rows, its first token, its end
 
   if (warp > kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (tid == kTaskWarp * 32) {
+      // ---------------------------------------------------------- pieces
+      const bool ok = chunk_hand_out<RowCut>(
+          sh.tasks, p.c, sh.start, p.joins + blockIdx.x,
+          [&](const ChunkWalk<RowCut>& w, ChunkTask& t) {
+            t.x[2] = w.item * 2 * tile_tokens;
+            t.x[3] = min(w.r.n, t.x[2] + 2 * tile_tokens);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int end = min(t.x[3], t.x[2] + (i + 1) * tile_tokens);
+              t.x[i] = end > t.x[2] + i * tile_tokens
+                           ? max(0, min(w.u1, RowCut::units_to(w.r, end - 1)) - w.u0)
+                           : 0;
+            }
+          });
+      if (!ok) report(p.err, ASP_DEVERR_TIMEOUT);
+    }
+    __syncwarp();
   } else if (warp == kLoadWarp) {
     // ------------------------------------------------------------ loader
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (lane == 0) {
-      prefetch_tensormap(&tmQ);
-      prefetch_tensormap(&tmK);
-      prefetch_tensormap(&tmV);
-    }
     uint32_t tile = 0;   // K and V tiles loaded so far
     uint32_t piece = 0;
     bool ok = true;
     uint32_t masks = 0;
-    for (; ok && walk.more(); walk.next(), ++piece) {
-      const Piece pc(walk, tile_tokens);
-      const int n = max(pc.n[0], pc.n[1]);
-      const bool two = pc.last - pc.tok0 > tile_tokens;
+    for (; ok && reader.next(task); ++piece) {
+      const int n = max(task.x[0], task.x[1]);
+      const bool two = task.x[3] - task.x[2] > tile_tokens;
       ok = __all_sync(kFull, mbar_wait(&sh.q_empty, (piece & 1) ^ 1));
       if (!ok) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(&sh.q_full, (two ? 2 : 1) * C::kTileBytes);
         for (int t = 0; t < (two ? 2 : 1); ++t)
           for (int hf = 0; hf < C::kHalves; ++hf)
-            tma_load_3d(q_tiles + t * C::kTileBytes + hf * 16384, &tmQ, hf * 64, walk.h * g,
-                        walk.r.row0 + pc.tok0 + t * tile_tokens, &sh.q_full);
+            tma_load_3d(q_tiles + t * C::kTileBytes + hf * 16384, &tmQ, hf * 64, task.h * g,
+                        task.row0 + task.x[2] + t * tile_tokens, &sh.q_full);
       }
-      const int n_pages = ceil_div(walk.r.T, P);
-      const int32_t* bt = p.bt + (size_t)walk.b * p.c.max_pages;
+      const int n_pages = ceil_div(task.T, P);
+      const int32_t* bt = p.bt + (size_t)task.b * p.c.max_pages;
       // the tile's physical pages, read one tile ahead
       auto look_up = [&](int j) {
-        const int page = (walk.u0 + j) * kPages + lane;
+        const int page = (task.u0 + j) * kPages + lane;
         return lane < kPages && page < n_pages ? bt[page] : 0;
       };
       int next = look_up(0);
       for (int j = 0; j < n; ++j) {
-        const bool have = lane < kPages && (walk.u0 + j) * kPages + lane < n_pages;
+        const bool have = lane < kPages && (task.u0 + j) * kPages + lane < n_pages;
         const int phys = next;
         next = look_up(j + 1);
         const bool good = have && phys >= 0 && phys < p.num_phys;
         if (have && !good) report(p.err, ASP_DEVERR_PAGE_RANGE);
         const uint32_t mask = __ballot_sync(kFull, good);
-        const int y = (phys * p.c.Hkv + walk.h) * P;
+        const int y = (phys * p.c.Hkv + task.h) * P;
         for (int kv = 0; kv < 2; ++kv, ++tile) {
           const int st = tile % C::kStages;
           ok = __all_sync(kFull, mbar_wait(&sh.empty[st], ((tile / C::kStages) & 1) ^ 1));
@@ -204,8 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++masks;
       }
     }
-    if (!ok && lane == 0) {
-      fail();
+    if (!(ok && reader.ok) && lane == 0) {
+      report(p.err, ASP_DEVERR_TIMEOUT);
       // copies in flight end before the CTA does
       for (uint32_t t = tile > C::kStages ? tile - C::kStages : 0; t < tile; ++t)
         mbar_wait(&sh.full[t % C::kStages], (t / C::kStages) & 1);
@@ -249,9 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    for (; ok && uniform(walk.more()); walk.next(), ++piece) {
-      const Piece pc(walk, tile_tokens);
-      const int nt[2] = {uniform(pc.n[0]), uniform(pc.n[1])};
+    for (; ok && uniform(reader.next(task)); ++piece) {
+      const int nt[2] = {uniform(task.x[0]), uniform(task.x[1])};
       const int n = max(nt[0], nt[1]);
       uint32_t st = tile % C::kStages;
       ok = wait(&sh.q_full, piece & 1) && wait(&sh.full[st], (tile / C::kStages) & 1);
@@ -289,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j + 2 == n) commit(&sh.q_empty);
       }
     }
-    if (!ok && lane == 0) fail();
+    if (!(ok && reader.ok) && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
     commit(&sh.drain);  // no arrival is still on its way when the CTA ends
     mbar_wait(&sh.drain, 0);
   } else {
@@ -301,47 +296,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = p.scale_log2;
     uint32_t phase_s = 0, phase_o = 0, units_seen = 0;
     bool ok = true;
-    if (tid == 0) p.joins[blockIdx.x].pieces = 0;
-    for (; ok && walk.more(); walk.next()) {
-      const Piece pc(walk, tile_tokens);
-      const int n = pc.n[t];
-      const int tok = pc.tok0 + t * tile_tokens + row / g;
+    const int row_tok = row / g, row_head = row % g;
+    while (ok && reader.next(task)) {
+      const int n = t == 0 ? task.x[0] : task.x[1];
+      const int tok = task.x[2] + t * tile_tokens + row_tok;
       // rows past the item's last take any slot that keeps them off the masked path
-      const bool mine = tok < pc.last;
-      const int pos = mine ? walk.r.T - walk.r.n + tok : walk.r.T - 1;
+      const bool mine = tok < task.x[3];
+      const int pos = mine ? task.T - task.n + tok : task.T - 1;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
-        const int key0 = (walk.u0 + j) * kTileKeys;
+        const int key0 = (task.u0 + j) * kTileKeys;
         ok = __all_sync(kFull, mbar_wait(&sh.s_full[t], phase_s & 1));
         if (!ok) break;
         ++phase_s;
         tc_fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s[i]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_wait_ld(s[i]);
         const uint32_t pages = sh.page_mask[(units_seen + j) % kPageMasks];
         // keys past the request's tokens, or of a page that is not there
         const bool holes = pages != (1u << kPages) - 1;
         if (__any_sync(kFull, pos < key0 + kTileKeys - 1) || holes) {
-          const int lim = pos - key0;
+          // Masked keys become -inf in tensor memory, 32 at a time: few units need it, and
+          // a short loop costs them less than long straight code would (it is fetched anew).
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            const int lim = pos - key0 - 32 * i;  // the last key of the 32 that the row sees
+            uint32_t see = lim >= 31 ? ~0u : lim < 0 ? 0u : (2u << lim) - 1;
+            if (P == 16)
+              see &= (pages >> (2 * i) & 1 ? 0xffffu : 0u) |
+                     (pages >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
+            else
+              see &= pages >> (32 * i / P) & 1 ? ~0u : 0u;
+            if (__all_sync(kFull, see == ~0u)) continue;
+            uint32_t x[32];
+            tmem_ld32(s_at + 32 * i, x);
+            tmem_wait_ld(x);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int k = 32 * i + e;
-              if (k > lim || !((pages >> (k / P)) & 1)) s[i][e] = 0xff800000u;  // -inf
-            }
-          if (holes || key0 + kTileKeys > walk.r.T) {
+            for (int e = 0; e < 32; ++e)
+              if (!(see >> e & 1)) x[e] = 0xff800000u;  // -inf
+            tmem_st32(s_at + 32 * i, x);
+          }
+          tmem_wait_st();
+          if (holes || key0 + kTileKeys > task.T) {
             // their V rows may hold anything: zero times it has to stay zero
             const uint32_t tv = 2 * (units_seen + j) + 1;
             ok = __all_sync(kFull, mbar_wait(&sh.full[tv % C::kStages], (tv / C::kStages) & 1));
             if (!ok) break;
-            if (key0 + row >= walk.r.T || !((pages >> (row / P)) & 1)) {
+            if (key0 + row >= task.T || !((pages >> (row / P)) & 1)) {
               uint8_t* v = ring + (tv % C::kStages) * C::kTileBytes +
                            row / P * (C::kHalves * P * 128) + row % P * 128;
-#pragma unroll
+#pragma unroll 1
               for (int e = 0; e < 8 * C::kHalves; ++e)
                 *reinterpret_cast<uint4*>(v + (e / 8) * (P * 128) + (e % 8) * 16) =
                     make_uint4(0, 0, 0, 0);
@@ -349,6 +351,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
           }
         }
+        uint32_t s[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_wait_ld(s[i]);
         float mx[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -367,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = moves ? ex2((m - top) * c) : 1.0f;
             if (moves) m = top;
             l *= f;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < D / 32; ++i) {
               uint32_t o[32];
               tmem_ld32(o_at + 32 * i, o);
@@ -416,141 +423,171 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       if (!ok) break;
-      units_seen += max(pc.n[0], pc.n[1]);
+      units_seen += max(task.x[0], task.x[1]);
       // ---- the piece's end: the whole item goes out, a part of it into the workspace
-      const bool whole = walk.whole();
       if (n > 0) {
         ok = __all_sync(kFull, mbar_wait(&sh.o_full[t], phase_o & 1));
         if (!ok) break;
         ++phase_o;
         tc_fence_after();
       }
-      const int head = walk.h * g + row % g;
-      if (whole) {
-        const size_t at = (size_t)(walk.r.row0 + tok) * p.Hq + head;
+      const size_t at = (size_t)(task.row0 + tok) * p.Hq + task.h * g + row_head;
+      if (task.whole) {
         const float inv = l > 0.f ? 1.0f / l : l;  // a NaN sum stays NaN, an empty row gives 0
+        // Four lanes exchange 16-byte pieces so that a row's 64 bytes leave together: a
+        // thread's own row, 16 bytes a store, would touch a cache line for every lane.
+        const int base = lane & ~3, q = lane & 3;
+        uint16_t* dst[4];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          if (n == 0) break;
-          uint32_t o[32];
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t there = __shfl_sync(
+              kFull, mine ? reinterpret_cast<uint64_t>(p.out + at * D) : 0ull, base + k);
+          dst[k] = reinterpret_cast<uint16_t*>(there);
+        }
+#pragma unroll 1
+        for (int i = 0; i < D / 32 && n > 0; ++i) {
+          uint32_t o[32], y[4][4];  // y[piece][word]
           tmem_ld32(o_at + 32 * i, o);
           tmem_wait_ld(o);
-          if (mine) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + 32 * i);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t y[4];
+          for (int e = 0; e < 16; ++e)
+            y[e / 4][e % 4] = pack_bf16(__uint_as_float(o[2 * e]) * inv,
+                                        __uint_as_float(o[2 * e + 1]) * inv);
+          // 4 x 4 transpose: lane q then holds piece q of rows base .. base + 3
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                y[k] = pack_bf16(__uint_as_float(o[8 * e + 2 * k]) * inv,
-                                 __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-              dst[e] = make_uint4(y[0], y[1], y[2], y[3]);
+          for (int w = 0; w < 4; ++w) {
+#pragma unroll
+            for (int step = 1; step < 4; step <<= 1) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (k & step) continue;
+                const bool up = q & step;
+                const uint32_t give = up ? y[k][w] : y[k | step][w];
+                const uint32_t got = __shfl_xor_sync(kFull, give, step);
+                if (up) y[k][w] = got; else y[k | step][w] = got;
+              }
             }
           }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (dst[k])
+              *reinterpret_cast<uint4*>(dst[k] + 32 * i + 8 * q) =
+                  make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
         }
         if (mine) p.lse[at] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
       } else {
-        const int slot = 2 * blockIdx.x + (walk.u0 == 0 ? 1 : 0);
-        float* part = p.partials + (size_t)slot * chunk_slot_floats(D);
+        // [m | l | O as D / 4 columns of four, each kChunkRows rows]
+        const int slot = 2 * blockIdx.x + (task.u0 == 0 ? 1 : 0);
         const int r = t * 128 + row;
-        if (mine) {
-          part[r] = m * c;
-          part[kChunkRows + r] = l;
-        }
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          if (n == 0) break;
+        float* part = p.partials + (size_t)slot * chunk_slot_floats(D);
+        part[r] = mine ? m * c : -INFINITY;
+        part[kChunkRows + r] = l;
+        float4* dst = reinterpret_cast<float4*>(part + 2 * kChunkRows) + r;
+#pragma unroll 1
+        for (int i = 0; i < D / 32 && n > 0; ++i) {
           uint32_t o[32];
           tmem_ld32(o_at + 32 * i, o);
           tmem_wait_ld(o);
-          if (mine) {
-            float4* dst = reinterpret_cast<float4*>(part + 2 * kChunkRows + (size_t)r * D + 32 * i);
+          if (!mine) continue;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                   __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-          }
-        }
-        if (tid == 0 && walk.u0 == 0) {
-          const int end = sh.start.shares.taker(walk.at + walk.units - 1, blockIdx.x);
-          p.joins[blockIdx.x] = ChunkJoin{walk.b, walk.h, walk.item, end - (int)blockIdx.x + 1};
+          for (int e = 0; e < 8; ++e)
+            dst[(8 * i + e) * kChunkRows] =
+                make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                            __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
         }
       }
       tc_fence_before();  // the next piece's first product writes O after the next P arrives
     }
-    if (!ok && lane == 0) fail();
+    if (!(ok && reader.ok) && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
   }
   __syncthreads();
   if (warp == kMmaWarp) tmem_free(tmem, kTmemCols);
 }
 
-// Joins the pieces of the item that CTA blockIdx.x began, a warp a row:
-// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i. A lane holds one piece's
-// maximum and sum; the pieces' O rows are added in order, eight loads in flight.
+// Joins the pieces of the item that CTA blockIdx.x began, 32 of its rows a block:
+// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i. A lane owns a row, a warp some of
+// its columns, four at a time; the pieces are added in order, eight loads in flight. The
+// rows leave through shared memory, so that they are written as rows.
 template <int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const Params p) {
-  constexpr int E = D / 32, kInFlight = 8;
-  using V = typename std::conditional<E == 4, float4, float2>::type;
+  constexpr int kInFlight = 8, kCols = D / 4 / 8;  // columns of four a warp
+  constexpr int kPitch = D + 8;                    // of a row in shared memory
+  __shared__ __align__(16) uint16_t tile[32 * kPitch];
   pdl_launch_dependents();
   pdl_wait_predecessor();
   const ChunkJoin jn = p.joins[blockIdx.x];
   if (jn.pieces < 2) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = p.c.g, row = blockIdx.y * 8 + warp;
+  const int g = p.c.g, row = blockIdx.y * 32 + lane;
   const ChunkRequest r = chunk_request(p.c, jn.b, nullptr);
-  const int tok = jn.item * (kChunkRows / g) + row / g;
-  if (tok >= r.n) return;
+  const int tok0 = jn.item * (kChunkRows / g);
   const size_t slot_floats = chunk_slot_floats(D);
-  const float* first = p.partials + (size_t)(2 * blockIdx.x + 1) * slot_floats;
-  const float* rest = p.partials + (size_t)(2 * blockIdx.x) * slot_floats;
+  const float* first = p.partials + (size_t)(2 * blockIdx.x + 1) * slot_floats + row;
+  const float* rest = p.partials + (size_t)(2 * blockIdx.x) * slot_floats + row;
   auto part = [&](int k) { return k == 0 ? first : rest + (size_t)(2 * k) * slot_floats; };
   float M = -INFINITY;
-  for (int k = lane; k < jn.pieces; k += 32) M = fmaxf(M, part(k)[row]);
+  for (int k = 0; k < jn.pieces; k += kInFlight) {
+    float m[kInFlight];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    for (int u = 0; u < kInFlight; ++u) m[u] = k + u < jn.pieces ? *part(k + u) : -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) M = fmaxf(M, m[u]);
+  }
   const float ref = M == -INFINITY ? 0.f : M;
-  float acc[E] = {}, L = 0.f;
-  for (int k0 = 0; k0 < jn.pieces; k0 += 32) {
-    float w = 0.f, wl = 0.f;  // a piece none of whose keys count for this row adds nothing
-    if (k0 + lane < jn.pieces) {
-      const float* q = part(k0 + lane);
-      const float mk = q[row];
-      if (mk != -INFINITY) {
-        w = ex2(mk - ref);
-        wl = w * q[kChunkRows + row];
-      }
-    }
-    const uint32_t some = __ballot_sync(kFull, w != 0.f);  // true for NaN too
-    const int n = min(32, jn.pieces - k0);
-    for (int k = 0; k < n; k += kInFlight) {
-      float o[kInFlight][E];
+  float L = 0.f;
+  float4 acc[kCols];
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
+  for (int i = 0; i < kCols; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kStep = kInFlight / kCols;
+  for (int k = 0; k < jn.pieces; k += kStep) {
+    float w[kStep], l[kStep];
+    float4 o[kStep][kCols];
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[u][e] = 0.f;
-        if (k + u < n && (some >> (k + u) & 1))
-          *reinterpret_cast<V*>(o[u]) = *reinterpret_cast<const V*>(
-              part(k0 + k + u) + 2 * kChunkRows + (size_t)row * D + lane * E);
-      }
+    for (int u = 0; u < kStep; ++u) {
+      w[u] = -INFINITY;
+      l[u] = 0.f;
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        const float wk = __shfl_sync(kFull, w, (k + u) & 31);
-        if (k + u >= n) continue;
+      for (int i = 0; i < kCols; ++i) o[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k + u >= jn.pieces) continue;
+      const float* q = part(k + u);
+      w[u] = *q;
+      l[u] = q[kChunkRows];
+      if (w[u] == -INFINITY) continue;  // none of its keys count for this row: no O was written
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, o[u][e], acc[e]);
-      }
+      for (int i = 0; i < kCols; ++i)
+        o[u][i] = *reinterpret_cast<const float4*>(
+            q - row + 2 * kChunkRows + 4 * ((size_t)(warp * kCols + i) * kChunkRows + row));
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) wl += __shfl_xor_sync(kFull, wl, o);
-    L += wl;
+    for (int u = 0; u < kStep; ++u) {
+      const float f = ex2(w[u] - ref);  // 0 where there is nothing
+      L = fmaf(f, l[u], L);
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        acc[i].x = fmaf(f, o[u][i].x, acc[i].x);
+        acc[i].y = fmaf(f, o[u][i].y, acc[i].y);
+        acc[i].z = fmaf(f, o[u][i].z, acc[i].z);
+        acc[i].w = fmaf(f, o[u][i].w, acc[i].w);
+      }
+    }
   }
   const float inv = L > 0.f ? 1.0f / L : L;
-  const size_t at = (size_t)(r.row0 + tok) * p.Hq + jn.h * g + row % g;
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(p.out + at * D + lane * E + e) =
-        pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0) p.lse[at] = L == 0.f ? -INFINITY : M * 0.69314718055994530942f + logf(L);
+  for (int i = 0; i < kCols; ++i)
+    *reinterpret_cast<uint2*>(tile + lane * kPitch + 4 * (warp * kCols + i)) =
+        make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
+  if (warp == 0 && tok0 + row / g < r.n)
+    p.lse[(size_t)(r.row0 + tok0 + row / g) * p.Hq + jn.h * g + row % g] =
+        L == 0.f ? -INFINITY : M * 0.69314718055994530942f + logf(L);
+  __syncthreads();
+  constexpr int kPieces = D / 8;  // of 16 bytes
+  for (int i = threadIdx.x; i < 32 * kPieces; i += 256) {
+    const int rr = blockIdx.y * 32 + i / kPieces;
+    if (tok0 + rr / g >= r.n) break;
+    const size_t at = (size_t)(r.row0 + tok0 + rr / g) * p.Hq + jn.h * g + rr % g;
+    *reinterpret_cast<uint4*>(p.out + at * D + 8 * (i % kPieces)) =
+        *reinterpret_cast<const uint4*>(tile + i / kPieces * kPitch + 8 * (i % kPieces));
+  }
 }
 
 template <int D, int P>
@@ -582,7 +619,7 @@ cudaError_t launch_t(const ChunkAttentionArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // an item has no more rows than the call
   const long long item_rows = min((long long)a.num_tokens * g, (long long)kChunkRows);
-  return launch_pdl(chunk_join_kernel<D>, dim3(a.num_sms, (unsigned)((item_rows + 7) / 8)), dim3(256),
+  return launch_pdl(chunk_join_kernel<D>, dim3(a.num_sms, (unsigned)((item_rows + 31) / 32)), dim3(256),
                     0, stream, p);
 }
 

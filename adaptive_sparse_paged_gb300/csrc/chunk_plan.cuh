@@ -224,4 +224,80 @@ struct ChunkWalk {
   }
 };
 
+// ------------------------------------------------------------ handing out pieces
+// One thread of the CTA walks the share and hands its pieces to the other warps
+// through a ring in shared memory, ahead of them: the walk is long straight code that
+// runs once a piece, and in every role's way it costs more than its arithmetic (its
+// instructions come from L2, some hundred cycles a line: 8 us between two items where
+// every warp walked for itself).
+struct alignas(16) ChunkTask {
+  int b, h, item;       // b < 0: no more pieces
+  int u0;               // first unit
+  int T, n, row0;       // the request (ChunkRequest)
+  int whole;            // the piece is the whole item
+  int x[4];             // what the kernel's roles want to know of it
+};
+constexpr int kTaskRing = 4;
+struct ChunkTasks {
+  ChunkTask task[kTaskRing];
+  uint64_t full[kTaskRing], empty[kTaskRing];
+};
+
+__device__ __forceinline__ void chunk_tasks_init(ChunkTasks& r, int readers) {
+  for (int i = 0; i < kTaskRing; ++i) {
+    mbar_init(&r.full[i], 1);
+    mbar_init(&r.empty[i], readers);
+  }
+}
+
+// The handing thread: fill(walk, task) sets task.x. Returns false where a wait ran out.
+template <typename Cut, typename Fill>
+__device__ __forceinline__ bool chunk_hand_out(ChunkTasks& r, const ChunkDims& c,
+                                               const ChunkStart& start, ChunkJoin* join,
+                                               Fill fill) {
+  ChunkWalk<Cut> w(c, start);
+  ChunkJoin jn{0, 0, 0, 0};
+  for (uint32_t i = 0;; ++i) {
+    const int slot = i % kTaskRing;
+    if (!mbar_wait(&r.empty[slot], ((i / kTaskRing) & 1) ^ 1)) return false;
+    ChunkTask& t = r.task[slot];
+    if (!w.more()) {
+      t.b = -1;
+      mbar_arrive(&r.full[slot]);
+      break;
+    }
+    t.b = w.b, t.h = w.h, t.item = w.item, t.u0 = w.u0;
+    t.T = w.r.T, t.n = w.r.n, t.row0 = w.r.row0;
+    t.whole = w.whole();
+    fill(w, t);
+    mbar_arrive(&r.full[slot]);
+    if (w.u0 == 0 && !w.whole())  // the last piece: other CTAs end this item
+      jn = ChunkJoin{w.b, w.h, w.item,
+                     start.shares.taker(w.at + w.units - 1, blockIdx.x) - (int)blockIdx.x + 1};
+    w.next();
+  }
+  *join = jn;
+  return true;
+}
+
+// A warp that takes pieces, all its lanes together.
+struct ChunkReader {
+  ChunkTasks& r;
+  uint32_t i = 0;
+  bool ok = true;  // false: a wait ran out
+  __device__ __forceinline__ explicit ChunkReader(ChunkTasks& ring) : r(ring) {}
+  __device__ __forceinline__ bool next(ChunkTask& t) {
+    const int slot = i % kTaskRing;
+    ok = __all_sync(0xffffffffu, mbar_wait(&r.full[slot], (i / kTaskRing) & 1)) != 0;
+    if (!ok) return false;
+    ++i;
+    const int4* src = reinterpret_cast<const int4*>(&r.task[slot]);
+    int4* dst = reinterpret_cast<int4*>(&t);
+    dst[0] = src[0], dst[1] = src[1], dst[2] = src[2];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&r.empty[slot]);
+    return t.b >= 0;
+  }
+};
+
 }  // namespace asp
