@@ -28,8 +28,8 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ================================================================ chunk form
-constexpr int kThreads = 384;  // two summing warpgroups; loader, issuer, two idle warps
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 384;  // two summing warpgroups; loader, issuer, piece warp, an idle one
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kTaskWarp = 10;
 constexpr int kKeyBufs = 3, kRowBufs = 3, kSumBufs = 4;
 constexpr int kLseRing = 16;   // tiles of rows whose lse is kept: more than are in flight
 constexpr int kMaskRing = 16;
@@ -45,7 +45,8 @@ struct ChunkShared {
   float lse[kLseRing][kTileRows];  // -lse * log2(e); -inf: the row adds nothing
   float acc[2][kTileKeys];
   uint64_t k_full[kKeyBufs], k_empty[kKeyBufs], r_full[kRowBufs], r_empty[kRowBufs];
-  uint64_t s_full[kSumBufs], s_empty[kSumBufs], drain;
+  uint64_t s_full[kSumBufs], s_empty[kSumBufs], acc_full[2], acc_empty[2], drain;
+  ChunkTasks tasks;
   ChunkStart start;
   long long scratch[kThreads / 32];
   uint32_t page_mask[kMaskRing];
@@ -104,8 +105,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_empty[i], 4);  // a warpgroup's warps
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.acc_full[i], 4);
+      mbar_init(&sh.acc_empty[i], 4);
+    }
     mbar_init(&sh.drain, 1);
+    chunk_tasks_init(sh.tasks, 10);  // loader, issuer, eight summing warps
     mbar_fence_init();
+  }
+  if (tid == kLoadWarp * 32) {
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmK);
   }
   if (warp == kMmaWarp) tmem_alloc(&sh.tmem, kTmemCols);
   tc_fence_before();
@@ -115,25 +125,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait_predecessor();
   const uint32_t tmem = sh.tmem;
   chunk_plan<KeyCut>(p.c, &sh.start, sh.scratch, p.err);
-  ChunkWalk<KeyCut> walk(p.c, sh.start);
   const int g = p.c.g, tile_tokens = kTileRows / g;
+  ChunkReader reader(sh.tasks);
+  ChunkTask task;  // x: row tiles of the piece, the first of them
 
-  if (warp == kLoadWarp) {
-    // ------------------------------------------------------------ loader
-    if (lane == 0) {
-      prefetch_tensormap(&tmQ);
-      prefetch_tensormap(&tmK);
+  if (warp > kMmaWarp) {
+    if (tid == kTaskWarp * 32) {
+      // ---------------------------------------------------------- pieces
+      const bool ok = chunk_hand_out<KeyCut>(
+          sh.tasks, p.c, sh.start, p.joins + blockIdx.x,
+          [&](const ChunkWalk<KeyCut>& w, ChunkTask& t) {
+            t.x[0] = w.r.n > 0 ? w.u1 - w.u0 : 0;
+            t.x[1] = KeyCut::first_tile(w.r, g, w.item) + w.u0;
+          });
+      if (!ok) report(p.err, ASP_DEVERR_TIMEOUT);
     }
+    __syncwarp();
+  } else if (warp == kLoadWarp) {
+    // ------------------------------------------------------------ loader
     uint32_t kt = 0, rt = 0;  // key tiles, row tiles loaded so far
+    int row_tok[4], row_at[4];  // the lane's rows in a tile: token, and place in lse
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      row_tok[i] = (lane * 4 + i) / g;
+      row_at[i] = row_tok[i] * p.Hq + (lane * 4 + i) % g;
+    }
     bool ok = true;
-    for (; ok && walk.more(); walk.next()) {
-      if (walk.r.n == 0) continue;
+    while (ok && reader.next(task)) {
+      const int steps = task.x[0], tile0 = task.x[1];
+      if (steps == 0) continue;
       const uint32_t kb = kt % kKeyBufs;
       ok = __all_sync(kFull, mbar_wait(&sh.k_empty[kb], ((kt / kKeyBufs) & 1) ^ 1));
       if (!ok) break;
-      const int page = walk.item * kPages + lane;
-      const bool have = lane < kPages && page < ceil_div(walk.r.T, P);
-      const int phys = have ? p.bt[(size_t)walk.b * p.c.max_pages + page] : 0;
+      const int page = task.item * kPages + lane;
+      const bool have = lane < kPages && page < ceil_div(task.T, P);
+      const int phys = have ? p.bt[(size_t)task.b * p.c.max_pages + page] : 0;
       const bool good = have && phys >= 0 && phys < p.num_phys;
       if (have && !good) report(p.err, ASP_DEVERR_PAGE_RANGE);
       const uint32_t mask = __ballot_sync(kFull, good);
@@ -148,21 +174,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int hf = 0; hf < C::kHalves; ++hf)
           tma_load_2d(keys + kb * C::kTileBytes + hf * 16384 + lane * P * 128, &tmK, hf * 64,
-                      (phys * p.c.Hkv + walk.h) * P, &sh.k_full[kb]);
+                      (phys * p.c.Hkv + task.h) * P, &sh.k_full[kb]);
       }
       ++kt;
-      const int tile0 = KeyCut::first_tile(walk.r, g, walk.item) + walk.u0;
-      const int steps = walk.u1 - walk.u0;
       // the rows' lse, four a lane, read one step ahead
       float next[4];
+      const float* lse = p.lse + (size_t)task.row0 * p.Hq + task.h * g;
       auto fetch = [&](int j) {
+        const int tok0 = (tile0 + j) * tile_tokens;
+        const float* src = lse + (size_t)tok0 * p.Hq;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = lane * 4 + i, tok = (tile0 + j) * tile_tokens + r / g;
-          next[i] = tok < walk.r.n
-                        ? p.lse[(size_t)(walk.r.row0 + tok) * p.Hq + walk.h * g + r % g]
-                        : -INFINITY;
-        }
+        for (int i = 0; i < 4; ++i)
+          next[i] = tok0 + row_tok[i] < task.n ? src[row_at[i]] : -INFINITY;
       };
       fetch(0);
       for (int j = 0; j < steps; ++j, ++rt) {
@@ -185,13 +208,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           sh.row_flag[rt % kLseRing] = none;
           mbar_arrive_expect_tx(&sh.r_full[rb], C::kTileBytes);
           for (int hf = 0; hf < C::kHalves; ++hf)
-            tma_load_3d(rows + rb * C::kTileBytes + hf * 16384, &tmQ, hf * 64, walk.h * g,
-                        walk.r.row0 + tok0, &sh.r_full[rb]);
+            tma_load_3d(rows + rb * C::kTileBytes + hf * 16384, &tmQ, hf * 64, task.h * g,
+                        task.row0 + tok0, &sh.r_full[rb]);
         }
         __syncwarp();
       }
     }
-    if (!ok && lane == 0) {
+    if (!(ok && reader.ok) && lane == 0) {
       report(p.err, ASP_DEVERR_TIMEOUT);
       for (uint32_t t = kt > kKeyBufs ? kt - kKeyBufs : 0; t < kt; ++t)  // copies in flight end
         mbar_wait(&sh.k_full[t % kKeyBufs], (t / kKeyBufs) & 1);
@@ -208,10 +231,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(kFull, mbar_wait(bar, parity)) != 0;
     };
-    for (; ok && uniform(walk.more()); walk.next()) {
-      if (uniform(walk.r.n) == 0) continue;
+    while (ok && uniform(reader.next(task))) {
+      const int steps = uniform(task.x[0]);
+      if (steps == 0) continue;
       const uint32_t kb = kt % kKeyBufs;
-      const int steps = uniform(walk.u1 - walk.u0);
       ok = wait(&sh.k_full[kb], (kt / kKeyBufs) & 1);
       for (int j = 0; ok && j < steps; ++j, ++rt) {
         const uint32_t rb = rt % kRowBufs, sb = rt % kSumBufs;
@@ -234,52 +257,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) mma_commit(&sh.k_empty[kb]);
       ++kt;
     }
-    if (!ok && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
+    if (!(ok && reader.ok) && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
     if (elect_one()) mma_commit(&sh.drain);  // no arrival is still on its way when the CTA ends
     mbar_wait(&sh.drain, 0);
-  } else if (warp < kLoadWarp) {
+  } else {
     // ------------------------------------------------------------ sums
     const int wg = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const float c = p.scale_log2;
     uint32_t kt = 0, rt = 0, pieces = 0;
     bool ok = true;
-    if (tid == 0) p.joins[blockIdx.x].pieces = 0;
-    for (; walk.more(); walk.next(), ++pieces) {
-      const int slot = walk.item * kTileKeys + row;
+    for (; ok && reader.next(task); ++pieces) {
+      const int slot = task.item * kTileKeys + row, steps = task.x[0], tile0 = task.x[1];
+      const int first_new = task.T - task.n;
       float sum = 0.f;
-      if (walk.r.n > 0) {
-        const int first_new = walk.r.T - walk.r.n;
-        const int tile0 = KeyCut::first_tile(walk.r, g, walk.item) + walk.u0;
-        const int steps = walk.u1 - walk.u0;
+      if (steps > 0) {
         for (int j = 0; ok && j < steps; ++j, ++rt) {
           if ((rt & 1) != (uint32_t)wg) continue;
           const uint32_t sb = rt % kSumBufs;
           ok = __all_sync(kFull, mbar_wait(&sh.s_full[sb], (rt / kSumBufs) & 1));
           if (!ok) break;
           tc_fence_after();
-          uint32_t s[4][32];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(tmem + lanes + sb * 128 + 32 * i, s[i]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_wait_ld(s[i]);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.s_empty[sb]);
+          const uint32_t s_at = tmem + lanes + sb * 128;
           const float* nl = sh.lse[rt % kLseRing];
+          auto release = [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.s_empty[sb]);
+          };
           // rows from `lo` on see this key
           const int lo = (slot - first_new - (tile0 + j) * tile_tokens) * g;
           float part[4] = {0.f, 0.f, 0.f, 0.f};
           if (__any_sync(kFull, lo > 0) || sh.row_flag[rt % kLseRing]) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
+            // few tiles: a short loop, whose code is fetched faster than straight code
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              uint32_t x[32];
+              tmem_ld32(s_at + 32 * i, x);
+              tmem_wait_ld(x);
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 const float l = nl[32 * i + e];
-                const float x = ex2(fmaf(__uint_as_float(s[i][e]), c, l));
-                part[i] += 32 * i + e >= lo && l != -INFINITY ? x : 0.f;
+                const float y = ex2(fmaf(__uint_as_float(x[e]), c, l));
+                part[e & 3] += 32 * i + e >= lo && l != -INFINITY ? y : 0.f;
               }
+            }
+            release();
           } else {
+            uint32_t s[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_wait_ld(s[i]);
+            release();
             const float2 c2 = make_float2(c, c);
             float2 two[4] = {};
             // 16 exponentials at a time; the ones before are summed while they run
@@ -318,29 +348,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++kt;
       }
       // the two warpgroups' halves: the second hands its own over
-      float* acc = sh.acc[pieces & 1];
-      if (wg == 1) acc[row] = sum;
-      named_bar_sync(1, 256);
-      if (wg == 0) {
-        sum += acc[row];
-        if (walk.whole()) {
-          if (slot < walk.r.T) {
-            const size_t at =
-                ((size_t)walk.b * p.c.Hkv + walk.h) * p.c.max_pages * P + slot;
-            p.w_out[at] =
-                weight_before(p.w_in, p.decay, at, slot, walk.r.T - walk.r.n) + sum;
-          }
-        } else {
-          p.partials[(size_t)(2 * blockIdx.x + (walk.u0 == 0 ? 1 : 0)) * kTileKeys + row] = sum;
-          if (tid == 0 && walk.u0 == 0) {
-            const int end = sh.start.shares.taker(walk.at + walk.units - 1, blockIdx.x);
-            p.joins[blockIdx.x] =
-                ChunkJoin{walk.b, walk.h, walk.item, end - (int)blockIdx.x + 1};
-          }
+      const int buf = pieces & 1;
+      const uint32_t parity = (pieces >> 1) & 1;
+      ok = ok && __all_sync(kFull, wg == 1 ? mbar_wait(&sh.acc_empty[buf], parity ^ 1)
+                                           : mbar_wait(&sh.acc_full[buf], parity));
+      if (!ok) break;
+      if (wg == 1) {
+        sh.acc[buf][row] = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.acc_full[buf]);
+      } else {
+        sum += sh.acc[buf][row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
+        if (!task.whole) {
+          p.partials[(size_t)(2 * blockIdx.x + (task.u0 == 0 ? 1 : 0)) * kTileKeys + row] = sum;
+        } else if (slot < task.T) {
+          const size_t at = ((size_t)task.b * p.c.Hkv + task.h) * p.c.max_pages * P + slot;
+          p.w_out[at] = weight_before(p.w_in, p.decay, at, slot, first_new) + sum;
         }
       }
     }
-    if (!ok && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
+    if (!(ok && reader.ok) && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
   }
   __syncthreads();
   if (warp == kMmaWarp) tmem_free(tmem, kTmemCols);
