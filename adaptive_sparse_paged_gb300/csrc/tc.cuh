@@ -113,6 +113,11 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(desc), "r"(accumulate)
       : "memory");
 }
+// 128 rows x 32 bytes of a K-major shared-memory operand into eight columns of tensor
+// memory, where mma_ts reads it; in order with the products issued after it.
+__device__ __forceinline__ void tmem_copy(uint32_t dst, uint64_t src) {
+  asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(dst), "l"(src) : "memory");
+}
 // Arrives on `bar` once every product that this thread issued is done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(

@@ -8,9 +8,10 @@
 //
 // Chunk form (chunk_weights_kernel): a persistent CTA per SM takes an equal share
 // of the units (128 keys x 128 query rows, chunk_plan.cuh); a key tile stays in
-// shared memory while the query tiles that see it stream past. Two warpgroups
-// take the products' results in turn, four of which are in tensor memory at
-// once. An item that several CTAs share leaves its partial sums in the
+// tensor memory while the query tiles that see it stream past (from shared memory it
+// would be read again for every one of them, and with the query tile's own reads and
+// writes that is more than shared memory gives). Two warpgroups take the products'
+// results in turn, three of which are in tensor memory at once. An item that several CTAs share leaves its partial sums in the
 // workspace; a second, small kernel adds them up.
 //
 // Decode form (decode_weights_kernel): one token a request, fp32 queries, page
@@ -30,10 +31,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 // ================================================================ chunk form
 constexpr int kThreads = 384;  // two summing warpgroups; loader, issuer, piece warp, an idle one
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kTaskWarp = 10;
-constexpr int kKeyBufs = 3, kRowBufs = 3, kSumBufs = 4;
+constexpr int kKeyBufs = 3, kRowBufs = 3, kSumBufs = 3;
 constexpr int kLseRing = 16;   // tiles of rows whose lse is kept: more than are in flight
 constexpr int kMaskRing = 16;
-constexpr uint32_t kTmemCols = 128 * kSumBufs;
+constexpr uint32_t kTmemCols = 512;    // sums (128 columns each), then key tiles (64 each)
+constexpr uint32_t kKeyCol = 128 * kSumBufs;
 
 template <int D>
 struct Cfg {
@@ -45,7 +47,8 @@ struct ChunkShared {
   float lse[kLseRing][kTileRows];  // -lse * log2(e); -inf: the row adds nothing
   float acc[2][kTileKeys];
   uint64_t k_full[kKeyBufs], k_empty[kKeyBufs], r_full[kRowBufs], r_empty[kRowBufs];
-  uint64_t s_full[kSumBufs], s_empty[kSumBufs], acc_full[2], acc_empty[2], drain;
+  uint64_t s_full[kSumBufs], s_empty[kSumBufs], acc_full[2], acc_empty[2], k_done[2],
+      drain;
   ChunkTasks tasks;
   ChunkStart start;
   long long scratch[kThreads / 32];
@@ -108,6 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.acc_full[i], 4);
       mbar_init(&sh.acc_empty[i], 4);
+      mbar_init(&sh.k_done[i], 1);
     }
     mbar_init(&sh.drain, 1);
     chunk_tasks_init(sh.tasks, 10);  // loader, issuer, eight summing warps
@@ -235,26 +239,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int steps = uniform(task.x[0]);
       if (steps == 0) continue;
       const uint32_t kb = kt % kKeyBufs;
-      ok = wait(&sh.k_full[kb], (kt / kKeyBufs) & 1);
+      // the products with the keys that were in this half of the key columns are done
+      ok = wait(&sh.k_done[kt & 1], ((kt >> 1) & 1) ^ 1) &&
+           wait(&sh.k_full[kb], (kt / kKeyBufs) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t a = tm + kKeyCol + (kt & 1) * 64;
+      if (elect_one()) {
+        const uint64_t k_tile = smem_desc(k0 + kb * C::kTileBytes, 16);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tmem_copy(a + 8 * k, k_tile + (((k / 4) * 16384 + (k % 4) * 32) >> 4));
+        mma_commit(&sh.k_empty[kb]);
+      }
       for (int j = 0; ok && j < steps; ++j, ++rt) {
         const uint32_t rb = rt % kRowBufs, sb = rt % kSumBufs;
         ok = wait(&sh.s_empty[sb], ((rt / kSumBufs) & 1) ^ 1) &&
              wait(&sh.r_full[rb], (rt / kRowBufs) & 1);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t a = smem_desc(k0 + kb * C::kTileBytes, 16);
         const uint64_t b = smem_desc(r0 + rb * C::kTileBytes, 16);
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = ((k / 4) * 16384 + (k % 4) * 32) >> 4;
-            mma_ss(tm + sb * 128, a + off, b + off, kDesc, k > 0);
-          }
+          for (int k = 0; k < D / 16; ++k)
+            mma_ts(tm + sb * 128, a + 8 * k, b + (((k / 4) * 16384 + (k % 4) * 32) >> 4), kDesc,
+                   k > 0);
           mma_commit(&sh.s_full[sb]);
           mma_commit(&sh.r_empty[rb]);
         }
       }
-      if (elect_one()) mma_commit(&sh.k_empty[kb]);
+      if (elect_one()) mma_commit(&sh.k_done[kt & 1]);
       ++kt;
     }
     if (!(ok && reader.ok) && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
@@ -428,7 +442,8 @@ constexpr int kQueryRows = 24;    // 8 heads x (high, middle, low)
 constexpr int kQueryCols = 32;    // the products' width, a multiple of 16: the last 8 columns
                                   // come from whatever lies behind the rows and are not read
 constexpr int kMetaRing = 16;     // key tiles whose pages are kept: more than are in flight
-constexpr int kDecCols = kQueryCols * kSumBufs;
+constexpr int kDecBufs = 4;      // products in tensor memory at once
+constexpr int kDecCols = kQueryCols * kDecBufs;
 
 template <int D>
 struct DecCfg {
@@ -442,7 +457,7 @@ struct DecShared {
   int page[kMetaRing][kTileKeys / 16];  // logical page of each listed page of the tile
   float lse[2][kMaxGroup];              // -lse * log2(e) of the segment's heads
   uint64_t full[6], empty[6], q_full[2], q_empty[2], l_empty[2];
-  uint64_t s_full[kSumBufs], s_empty[kSumBufs], drain;
+  uint64_t s_full[kDecBufs], s_empty[kDecBufs], drain;
   int warp_sum[kDecThreads / 32];
   int seg, tile;
   uint32_t tmem;
@@ -538,7 +553,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       mbar_init(&sh.q_empty[i], 1);
       mbar_init(&sh.l_empty[i], 128);
     }
-    for (int i = 0; i < kSumBufs; ++i) {
+    for (int i = 0; i < kDecBufs; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_empty[i], 128);
     }
@@ -715,8 +730,8 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       const int buf = seg & 1, run = uniform(walk.run());
       ok = wait(&sh.q_full[buf], (seg >> 1) & 1);
       for (int j = 0; ok && j < run; ++j, ++kt) {
-        const uint32_t st = kt % C::kStages, sb = kt % kSumBufs;
-        ok = wait(&sh.s_empty[sb], ((kt / kSumBufs) & 1) ^ 1) &&
+        const uint32_t st = kt % C::kStages, sb = kt % kDecBufs;
+        ok = wait(&sh.s_empty[sb], ((kt / kDecBufs) & 1) ^ 1) &&
              wait(&sh.full[st], (kt / C::kStages) & 1);
         if (!ok) break;
         tc_fence_after();
@@ -747,8 +762,8 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       const size_t base = (size_t)walk.seg * p.max_pages * P;
       float nl[kMaxGroup];
       for (int j = 0; j < run; ++j, ++kt) {
-        const uint32_t sb = kt % kSumBufs;
-        ok = __all_sync(kFull, mbar_wait(&sh.s_full[sb], (kt / kSumBufs) & 1));
+        const uint32_t sb = kt % kDecBufs;
+        ok = __all_sync(kFull, mbar_wait(&sh.s_full[sb], (kt / kDecBufs) & 1));
         if (!ok) break;
         const int e = sh.page[kt % kMetaRing][tid / P];
         const int slot = (e & ~kNotMapped) * P + tid % P;
