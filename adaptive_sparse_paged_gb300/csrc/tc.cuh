@@ -90,6 +90,13 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t block) {
   return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(block >> 4) << 16 |
          (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
+// One step of the contraction (16 elements) without a swizzle: 8 rows of 16 bytes are a
+// block of 128 bytes, the blocks of all rows follow one another, and the second eight
+// elements lie `half` bytes behind the first.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t addr, uint32_t half) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(half >> 4) << 16 |
+         (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
 // bf16 operands, fp32 accumulators, M x N; b_mn: B is MN-major (A is K-major).
 __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_mn) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
@@ -150,6 +157,15 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   asm("{\n\t.reg .b64 a, b, d;\n\t"
       "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
       "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;

@@ -32,7 +32,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kThreads = 384;  // two summing warpgroups; loader, issuer, piece warp, an idle one
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kTaskWarp = 10;
 constexpr int kKeyBufs = 3, kRowBufs = 3, kSumBufs = 3;
-constexpr int kLseRing = 16;   // tiles of rows whose lse is kept: more than are in flight
+constexpr int kFlagRing = 16;  // tiles of rows whose flags are kept: more than are in flight
+constexpr int kLseBytes = 2 * 128 * 16;  // a tile's lse as one step of the contraction
 constexpr int kMaskRing = 16;
 constexpr uint32_t kTmemCols = 512;    // sums (128 columns each), then key tiles (64 each)
 constexpr uint32_t kKeyCol = 128 * kSumBufs;
@@ -44,7 +45,6 @@ struct Cfg {
 };
 
 struct ChunkShared {
-  float lse[kLseRing][kTileRows];  // -lse * log2(e); -inf: the row adds nothing
   float acc[2][kTileKeys];
   uint64_t k_full[kKeyBufs], k_empty[kKeyBufs], r_full[kRowBufs], r_empty[kRowBufs];
   uint64_t s_full[kSumBufs], s_empty[kSumBufs], acc_full[2], acc_empty[2], k_done[2],
@@ -53,13 +53,15 @@ struct ChunkShared {
   ChunkStart start;
   long long scratch[kThreads / 32];
   uint32_t page_mask[kMaskRing];
-  uint32_t row_flag[kLseRing];     // some row of the tile adds nothing
+  uint32_t row_none[kFlagRing];               // some row of the tile adds nothing:
+  uint32_t row_adds[kFlagRing][kTileRows / 32];  // then these are the ones that do
   uint32_t tmem;
 };
 
 template <int D>
 constexpr size_t chunk_smem() {
-  return 1024 + (kKeyBufs + kRowBufs) * (size_t)Cfg<D>::kTileBytes + sizeof(ChunkShared);
+  return 1024 + (kKeyBufs + kRowBufs) * (size_t)Cfg<D>::kTileBytes + (1 + kRowBufs) * kLseBytes +
+         sizeof(ChunkShared);
 }
 
 struct ChunkParams {
@@ -72,7 +74,7 @@ struct ChunkParams {
   float* partials;
   uint32_t* err;
   int Hq, num_phys;
-  float scale_log2, decay;
+  float scale_log2, inv_scale, decay;
 };
 
 // Weight of slot s before the call: the chunk's own tokens had none.
@@ -92,7 +94,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* keys = smem;
   uint8_t* rows = smem + kKeyBufs * C::kTileBytes;
-  ChunkShared& sh = *reinterpret_cast<ChunkShared*>(rows + kRowBufs * C::kTileBytes);
+  // One more step of the contraction subtracts the rows' lse: three ones in every key's
+  // row against the three bf16 terms of -lse / scale in every query's.
+  uint8_t* ones = rows + kRowBufs * C::kTileBytes;
+  uint8_t* lses = ones + kLseBytes;  // [kRowBufs]
+  ChunkShared& sh = *reinterpret_cast<ChunkShared*>(lses + kRowBufs * kLseBytes);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -121,6 +127,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tmQ);
     prefetch_tensormap(&tmK);
   }
+  for (int i = tid; i < (1 + kRowBufs) * kLseBytes / 16; i += kThreads)
+    reinterpret_cast<uint4*>(ones)[i] =
+        i < 128 ? make_uint4(0x3f803f80u, 0x00003f80u, 0, 0) : make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
   if (warp == kMmaWarp) tmem_alloc(&sh.tmem, kTmemCols);
   tc_fence_before();
   __syncthreads();
@@ -195,21 +205,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < steps; ++j, ++rt) {
         const uint32_t rb = rt % kRowBufs;
         const int tok0 = (tile0 + j) * tile_tokens;
-        float nl[4];
-        bool none = false;
+        uint4 terms[4];
+        uint32_t adds = 0;  // which of the lane's four rows add anything
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          nl[i] = next[i] == -INFINITY ? -INFINITY : -next[i] * kLog2e;
-          none |= next[i] == -INFINITY;
+          const float v = -next[i] * p.inv_scale;
+          const bool none = fabsf(next[i]) == INFINITY;
+          adds |= none ? 0u : 1u << i;
+          const uint32_t hm = pack_bf16(v, 0.f);
+          const float r1 = v - __uint_as_float(hm << 16);
+          const uint32_t mid = pack_bf16(0.f, r1);
+          const float r2 = r1 - __uint_as_float(mid & 0xffff0000u);
+          terms[i] = none ? make_uint4(0, 0, 0, 0)
+                          : make_uint4((hm & 0xffffu) | mid, pack_bf16(r2, 0.f), 0, 0);
         }
         if (j + 1 < steps) fetch(j + 1);
         ok = __all_sync(kFull, mbar_wait(&sh.r_empty[rb], ((rt / kRowBufs) & 1) ^ 1));
         if (!ok) break;
-        *reinterpret_cast<float4*>(&sh.lse[rt % kLseRing][lane * 4]) =
-            make_float4(nl[0], nl[1], nl[2], nl[3]);
-        none = __any_sync(kFull, none);
+        uint4* dst = reinterpret_cast<uint4*>(lses + rb * kLseBytes) + lane * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[i] = terms[i];
+        fence_proxy_async_smem();
+        const bool some_none = __any_sync(kFull, adds != 15u);
+        if (some_none) {
+          uint32_t word = adds << (lane % 8 * 4);
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) word |= __shfl_xor_sync(kFull, word, o);
+          if (lane % 8 == 0) sh.row_adds[rt % kFlagRing][lane / 8] = word;
+        }
+        __syncwarp();
         if (lane == 0) {
-          sh.row_flag[rt % kLseRing] = none;
+          sh.row_none[rt % kFlagRing] = some_none;
           mbar_arrive_expect_tx(&sh.r_full[rb], C::kTileBytes);
           for (int hf = 0; hf < C::kHalves; ++hf)
             tma_load_3d(rows + rb * C::kTileBytes + hf * 16384, &tmQ, hf * 64, task.h * g,
@@ -229,7 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ products
     constexpr uint32_t kDesc = mma_desc(kTileKeys, kTileRows, false);
     const uint32_t k0 = uniform(smem_u32(keys)), r0 = uniform(smem_u32(rows));
-    const uint32_t tm = uniform(tmem);
+    const uint32_t tm = uniform(tmem), l0 = uniform(smem_u32(lses));
+    const uint64_t one = smem_desc_plain(uniform(smem_u32(ones)), kLseBytes / 2);
     uint32_t kt = 0, rt = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -264,6 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < D / 16; ++k)
             mma_ts(tm + sb * 128, a + 8 * k, b + (((k / 4) * 16384 + (k % 4) * 32) >> 4), kDesc,
                    k > 0);
+          mma_ss(tm + sb * 128, one, smem_desc_plain(l0 + rb * kLseBytes, kLseBytes / 2), kDesc, 1);
           mma_commit(&sh.s_full[sb]);
           mma_commit(&sh.r_empty[rb]);
         }
@@ -293,7 +321,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t s_at = tmem + lanes + sb * 128;
-          const float* nl = sh.lse[rt % kLseRing];
           auto release = [&] {
             tc_fence_before();
             __syncwarp();
@@ -302,18 +329,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           // rows from `lo` on see this key
           const int lo = (slot - first_new - (tile0 + j) * tile_tokens) * g;
           float part[4] = {0.f, 0.f, 0.f, 0.f};
-          if (__any_sync(kFull, lo > 0) || sh.row_flag[rt % kLseRing]) {
+          const bool none = sh.row_none[rt % kFlagRing] != 0;
+          if (__any_sync(kFull, lo > 0) || none) {
             // few tiles: a short loop, whose code is fetched faster than straight code
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
+              const int from = lo - 32 * i;
+              uint32_t see = from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
+              if (none) see &= sh.row_adds[rt % kFlagRing][i];
               uint32_t x[32];
               tmem_ld32(s_at + 32 * i, x);
               tmem_wait_ld(x);
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
-                const float l = nl[32 * i + e];
-                const float y = ex2(fmaf(__uint_as_float(x[e]), c, l));
-                part[e & 3] += 32 * i + e >= lo && l != -INFINITY ? y : 0.f;
+                const float y = ex2(__uint_as_float(x[e]) * c);
+                part[e & 3] += see >> e & 1 ? y : 0.f;
               }
             }
             release();
@@ -329,17 +359,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // 16 exponentials at a time; the ones before are summed while they run
             auto exponentials = [&](int q) {
 #pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                const float4 l = *reinterpret_cast<const float4*>(nl + 16 * q + e);
+              for (int e = 0; e < 16; e += 2) {
                 uint32_t* x = &s[q / 2][(q & 1) * 16 + e];
-                const float2 y0 = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])),
-                                       c2, make_float2(l.x, l.y));
-                const float2 y1 = fma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])),
-                                       c2, make_float2(l.z, l.w));
-                x[0] = __float_as_uint(ex2(y0.x));
-                x[1] = __float_as_uint(ex2(y0.y));
-                x[2] = __float_as_uint(ex2(y1.x));
-                x[3] = __float_as_uint(ex2(y1.y));
+                const float2 y =
+                    mul2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2);
+                x[0] = __float_as_uint(ex2(y.x));
+                x[1] = __float_as_uint(ex2(y.y));
               }
             };
             exponentials(0);
@@ -424,7 +449,7 @@ cudaError_t launch_chunk_t(const WeightArgs& a, cudaStream_t stream) {
   ChunkParams p{{a.q_offsets, kv.seq_lens, kv.batch, kv.num_kv_heads, g, kv.max_pages, P,
                  a.num_tokens, chunk_inverse(a.num_sms)},
                 kv.block_table, a.lse, a.w_in, a.w_out, a.joins, a.partials, a.err, kv.num_q_heads,
-                kv.num_phys_pages, a.sm_scale * kLog2e, a.decay};
+                kv.num_phys_pages, a.sm_scale * kLog2e, 1.0f / a.sm_scale, a.decay};
   constexpr size_t smem = chunk_smem<D>();
   if ((e = set_max_dynamic_smem((const void*)chunk_weights_kernel<D, P>, (int)smem)) != cudaSuccess)
     return e;
