@@ -6,7 +6,7 @@
 // A cut says how many items a head of a request has and how many units an item:
 //   RowCut   item: up to 256 query rows, a row being one (token, head of the
 //            group), token-major; unit: those rows against 128 keys that they see.
-//   KeyCut   item: 128 keys; unit: those keys against 128 query rows.
+//   KeyCut   item: 256 keys; unit: those keys against 128 query rows.
 // The items in order (request, head, item) form one sequence of units, of which
 // every CTA takes an equal, contiguous share.
 #pragma once
@@ -17,6 +17,7 @@ namespace asp {
 
 constexpr int kTileKeys = 128;
 constexpr int kTileRows = 128;
+constexpr int kItemKeys = 2 * kTileKeys;
 
 struct ChunkDims {
   const int32_t* q_offsets;
@@ -69,11 +70,11 @@ struct RowCut {
 
 struct KeyCut {
   static __device__ __forceinline__ int items(const ChunkRequest& r, int) {
-    return ceil_div(r.T, kTileKeys);
+    return ceil_div(r.T, kItemKeys);
   }
   // First tile of rows that sees a key of the item.
   static __device__ __forceinline__ int first_tile(const ChunkRequest& r, int g, int item) {
-    return max(0, item * kTileKeys - (r.T - r.n)) / (kTileRows / g);
+    return max(0, item * kItemKeys - (r.T - r.n)) / (kTileRows / g);
   }
   static __device__ __forceinline__ int tiles(const ChunkRequest& r, int g) {
     return ceil_div(r.n, kTileRows / g);
@@ -85,12 +86,12 @@ struct KeyCut {
   static __device__ __forceinline__ long long before(const ChunkRequest& r, int g, int m) {
     if (r.n == 0) return m;
     const int a = r.T - r.n, nq = tiles(r, g);
-    const int full = min(m, a / kTileKeys + 1);  // items that every tile of rows sees
+    const int full = min(m, a / kItemKeys + 1);  // items that every tile of rows sees
     long long sum = (long long)full * nq;
-    const long long cut = m - full;              // the others: g tiles fewer each time
+    const long long cut = m - full;              // the others: 2 g tiles fewer each time
     if (cut > 0)
-      sum += cut * (nq - (kTileKeys * (a / kTileKeys + 1) - a) / (kTileRows / g)) -
-             g * (cut * (cut - 1) / 2);
+      sum += cut * (nq - (kItemKeys * (a / kItemKeys + 1) - a) / (kTileRows / g)) -
+             kItemKeys / kTileRows * g * (cut * (cut - 1) / 2);
     return sum;
   }
 };

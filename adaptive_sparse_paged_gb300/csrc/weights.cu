@@ -7,11 +7,14 @@
 // exchange and no atomics, and comes out in a fixed order.
 //
 // Chunk form (chunk_weights_kernel): a persistent CTA per SM takes an equal share
-// of the units (128 keys x 128 query rows, chunk_plan.cuh); a key tile stays in
+// of the units (256 keys x 128 query rows, chunk_plan.cuh); two key tiles stay in
 // tensor memory while the query tiles that see it stream past (from shared memory it
 // would be read again for every one of them, and with the query tile's own reads and
-// writes that is more than shared memory gives). Two warpgroups take the products'
-// results in turn, three of which are in tensor memory at once. An item that several CTAs share leaves its partial sums in the
+// writes that is more than shared memory gives); with one key tile instead of two the
+// query tiles' loads are what bounds the kernel (1030 cycles a tile of 128 x 128,
+// whatever the products and sums take). A warpgroup sums one key tile's rows; three
+// products are in tensor memory at once. The rows' lse is subtracted by the product
+// itself: read from shared memory for every element it cost as much as the products. An item that several CTAs share leaves its partial sums in the
 // workspace; a second, small kernel adds them up.
 //
 // Decode form (decode_weights_kernel): one token a request, fp32 queries, page
@@ -45,10 +48,8 @@ struct Cfg {
 };
 
 struct ChunkShared {
-  float acc[2][kTileKeys];
   uint64_t k_full[kKeyBufs], k_empty[kKeyBufs], r_full[kRowBufs], r_empty[kRowBufs];
-  uint64_t s_full[kSumBufs], s_empty[kSumBufs], acc_full[2], acc_empty[2], k_done[2],
-      drain;
+  uint64_t s_full[kSumBufs], s_empty[kSumBufs], k_done, drain;
   ChunkTasks tasks;
   ChunkStart start;
   long long scratch[kThreads / 32];
@@ -114,11 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_empty[i], 4);  // a warpgroup's warps
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.acc_full[i], 4);
-      mbar_init(&sh.acc_empty[i], 4);
-      mbar_init(&sh.k_done[i], 1);
-    }
+    mbar_init(&sh.k_done, 1);
     mbar_init(&sh.drain, 1);
     chunk_tasks_init(sh.tasks, 10);  // loader, issuer, eight summing warps
     mbar_fence_init();
@@ -168,29 +165,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && reader.next(task)) {
       const int steps = task.x[0], tile0 = task.x[1];
       if (steps == 0) continue;
-      const uint32_t kb = kt % kKeyBufs;
-      ok = __all_sync(kFull, mbar_wait(&sh.k_empty[kb], ((kt / kKeyBufs) & 1) ^ 1));
-      if (!ok) break;
-      const int page = task.item * kPages + lane;
-      const bool have = lane < kPages && page < ceil_div(task.T, P);
-      const int phys = have ? p.bt[(size_t)task.b * p.c.max_pages + page] : 0;
-      const bool good = have && phys >= 0 && phys < p.num_phys;
-      if (have && !good) report(p.err, ASP_DEVERR_PAGE_RANGE);
-      const uint32_t mask = __ballot_sync(kFull, good);
-      if (lane == 0) {
-        sh.page_mask[kt % kMaskRing] = mask;
-        const uint32_t bytes = __popc(mask) * (P * 128 * C::kHalves);
-        if (bytes) mbar_arrive_expect_tx(&sh.k_full[kb], bytes);
-        else mbar_arrive(&sh.k_full[kb]);
-      }
-      __syncwarp();
-      if (good) {
+      for (int t = 0; t < 2; ++t, ++kt) {
+        const uint32_t kb = kt % kKeyBufs;
+        ok = ok && __all_sync(kFull, mbar_wait(&sh.k_empty[kb], ((kt / kKeyBufs) & 1) ^ 1));
+        if (!ok) break;
+        const int page = (2 * task.item + t) * kPages + lane;
+        const bool have = lane < kPages && page < ceil_div(task.T, P);
+        const int phys = have ? p.bt[(size_t)task.b * p.c.max_pages + page] : 0;
+        const bool good = have && phys >= 0 && phys < p.num_phys;
+        if (have && !good) report(p.err, ASP_DEVERR_PAGE_RANGE);
+        const uint32_t mask = __ballot_sync(kFull, good);
+        if (lane == 0) {
+          sh.page_mask[kt % kMaskRing] = mask;
+          const uint32_t bytes = __popc(mask) * (P * 128 * C::kHalves);
+          if (bytes) mbar_arrive_expect_tx(&sh.k_full[kb], bytes);
+          else mbar_arrive(&sh.k_full[kb]);
+        }
+        __syncwarp();
+        if (good) {
 #pragma unroll
-        for (int hf = 0; hf < C::kHalves; ++hf)
-          tma_load_2d(keys + kb * C::kTileBytes + hf * 16384 + lane * P * 128, &tmK, hf * 64,
-                      (phys * p.c.Hkv + task.h) * P, &sh.k_full[kb]);
+          for (int hf = 0; hf < C::kHalves; ++hf)
+            tma_load_2d(keys + kb * C::kTileBytes + hf * 16384 + lane * P * 128, &tmK, hf * 64,
+                        (phys * p.c.Hkv + task.h) * P, &sh.k_full[kb]);
+        }
       }
-      ++kt;
+      if (!ok) break;
       // the rows' lse, four a lane, read one step ahead
       float next[4];
       const float* lse = p.lse + (size_t)task.row0 * p.Hq + task.h * g;
@@ -265,59 +264,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && uniform(reader.next(task))) {
       const int steps = uniform(task.x[0]);
       if (steps == 0) continue;
-      const uint32_t kb = kt % kKeyBufs;
-      // the products with the keys that were in this half of the key columns are done
-      ok = wait(&sh.k_done[kt & 1], ((kt >> 1) & 1) ^ 1) &&
-           wait(&sh.k_full[kb], (kt / kKeyBufs) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t a = tm + kKeyCol + (kt & 1) * 64;
-      if (elect_one()) {
-        const uint64_t k_tile = smem_desc(k0 + kb * C::kTileBytes, 16);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tmem_copy(a + 8 * k, k_tile + (((k / 4) * 16384 + (k % 4) * 32) >> 4));
-        mma_commit(&sh.k_empty[kb]);
-      }
-      for (int j = 0; ok && j < steps; ++j, ++rt) {
-        const uint32_t rb = rt % kRowBufs, sb = rt % kSumBufs;
-        ok = wait(&sh.s_empty[sb], ((rt / kSumBufs) & 1) ^ 1) &&
-             wait(&sh.r_full[rb], (rt / kRowBufs) & 1);
+      // the products with the keys before are done
+      ok = wait(&sh.k_done, ((kt >> 1) & 1) ^ 1);
+      const uint32_t a = tm + kKeyCol;
+      for (int t = 0; t < 2 && ok; ++t, ++kt) {
+        const uint32_t kb = kt % kKeyBufs;
+        ok = wait(&sh.k_full[kb], (kt / kKeyBufs) & 1);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t b = smem_desc(r0 + rb * C::kTileBytes, 16);
         if (elect_one()) {
+          const uint64_t k_tile = smem_desc(k0 + kb * C::kTileBytes, 16);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ts(tm + sb * 128, a + 8 * k, b + (((k / 4) * 16384 + (k % 4) * 32) >> 4), kDesc,
-                   k > 0);
-          mma_ss(tm + sb * 128, one, smem_desc_plain(l0 + rb * kLseBytes, kLseBytes / 2), kDesc, 1);
-          mma_commit(&sh.s_full[sb]);
-          mma_commit(&sh.r_empty[rb]);
+            tmem_copy(a + 64 * t + 8 * k, k_tile + (((k / 4) * 16384 + (k % 4) * 32) >> 4));
+          mma_commit(&sh.k_empty[kb]);
         }
       }
-      if (elect_one()) mma_commit(&sh.k_done[kt & 1]);
-      ++kt;
+      for (int j = 0; ok && j < steps; ++j, ++rt) {
+        const uint32_t rb = rt % kRowBufs;
+        ok = wait(&sh.r_full[rb], (rt / kRowBufs) & 1);
+        const uint64_t b = smem_desc(r0 + rb * C::kTileBytes, 16);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t x = 2 * rt + t, sb = x % kSumBufs;
+          ok = ok && wait(&sh.s_empty[sb], ((x / kSumBufs) & 1) ^ 1);
+          if (!ok) continue;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ts(tm + sb * 128, a + 64 * t + 8 * k,
+                     b + (((k / 4) * 16384 + (k % 4) * 32) >> 4), kDesc, k > 0);
+            mma_ss(tm + sb * 128, one, smem_desc_plain(l0 + rb * kLseBytes, kLseBytes / 2), kDesc,
+                   1);
+            mma_commit(&sh.s_full[sb]);
+            if (t == 1) mma_commit(&sh.r_empty[rb]);
+          }
+        }
+      }
+      if (elect_one()) mma_commit(&sh.k_done);
     }
     if (!(ok && reader.ok) && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
     if (elect_one()) mma_commit(&sh.drain);  // no arrival is still on its way when the CTA ends
     mbar_wait(&sh.drain, 0);
   } else {
     // ------------------------------------------------------------ sums
-    const int wg = warp >> 2, row = tid & 127;
+    const int t = warp >> 2, row = tid & 127;  // the warpgroup's key tile, the thread's key in it
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const float c = p.scale_log2;
-    uint32_t kt = 0, rt = 0, pieces = 0;
+    uint32_t kt = 0, rt = 0;
     bool ok = true;
-    for (; ok && reader.next(task); ++pieces) {
-      const int slot = task.item * kTileKeys + row, steps = task.x[0], tile0 = task.x[1];
+    while (ok && reader.next(task)) {
+      const int slot = task.item * kItemKeys + t * kTileKeys + row;
+      const int steps = task.x[0], tile0 = task.x[1];
       const int first_new = task.T - task.n;
       float sum = 0.f;
       if (steps > 0) {
-        for (int j = 0; ok && j < steps; ++j, ++rt) {
-          if ((rt & 1) != (uint32_t)wg) continue;
-          const uint32_t sb = rt % kSumBufs;
-          ok = __all_sync(kFull, mbar_wait(&sh.s_full[sb], (rt / kSumBufs) & 1));
+        for (int j = 0; j < steps; ++j, ++rt) {
+          const uint32_t x = 2 * rt + t, sb = x % kSumBufs;
+          ok = __all_sync(kFull, mbar_wait(&sh.s_full[sb], (x / kSumBufs) & 1));
           if (!ok) break;
           tc_fence_after();
           const uint32_t s_at = tmem + lanes + sb * 128;
@@ -383,29 +388,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           sum += (part[0] + part[1]) + (part[2] + part[3]);
         }
-        if (!((sh.page_mask[kt % kMaskRing] >> (row / P)) & 1)) sum = 0.f;
-        ++kt;
+        if (!ok) break;
+        if (!((sh.page_mask[(kt + t) % kMaskRing] >> (row / P)) & 1)) sum = 0.f;
+        kt += 2;
       }
-      // the two warpgroups' halves: the second hands its own over
-      const int buf = pieces & 1;
-      const uint32_t parity = (pieces >> 1) & 1;
-      ok = ok && __all_sync(kFull, wg == 1 ? mbar_wait(&sh.acc_empty[buf], parity ^ 1)
-                                           : mbar_wait(&sh.acc_full[buf], parity));
-      if (!ok) break;
-      if (wg == 1) {
-        sh.acc[buf][row] = sum;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.acc_full[buf]);
-      } else {
-        sum += sh.acc[buf][row];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
-        if (!task.whole) {
-          p.partials[(size_t)(2 * blockIdx.x + (task.u0 == 0 ? 1 : 0)) * kTileKeys + row] = sum;
-        } else if (slot < task.T) {
-          const size_t at = ((size_t)task.b * p.c.Hkv + task.h) * p.c.max_pages * P + slot;
-          p.w_out[at] = weight_before(p.w_in, p.decay, at, slot, first_new) + sum;
-        }
+      if (!task.whole) {
+        p.partials[(size_t)(2 * blockIdx.x + (task.u0 == 0 ? 1 : 0)) * kItemKeys + t * kTileKeys +
+                   row] = sum;
+      } else if (slot < task.T) {
+        const size_t at = ((size_t)task.b * p.c.Hkv + task.h) * p.c.max_pages * P + slot;
+        p.w_out[at] = weight_before(p.w_in, p.decay, at, slot, first_new) + sum;
       }
     }
     if (!(ok && reader.ok) && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
@@ -415,17 +407,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Adds up the pieces of the item that CTA blockIdx.x began, in CTA order.
-__global__ void __launch_bounds__(kTileKeys) weights_join_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(kItemKeys) weights_join_kernel(const ChunkParams p) {
   pdl_launch_dependents();
   pdl_wait_predecessor();
   const ChunkJoin jn = p.joins[blockIdx.x];
   if (jn.pieces < 2) return;
   const ChunkRequest r = chunk_request(p.c, jn.b, nullptr);
-  const int row = threadIdx.x, slot = jn.item * kTileKeys + row;
+  const int row = threadIdx.x, slot = jn.item * kItemKeys + row;
   if (slot >= r.T) return;
-  float sum = p.partials[(size_t)(2 * blockIdx.x + 1) * kTileKeys + row];
+  float sum = p.partials[(size_t)(2 * blockIdx.x + 1) * kItemKeys + row];
   for (int k = 1; k < jn.pieces; ++k)
-    sum += p.partials[(size_t)(2 * (blockIdx.x + k)) * kTileKeys + row];
+    sum += p.partials[(size_t)(2 * (blockIdx.x + k)) * kItemKeys + row];
   const size_t at = ((size_t)jn.b * p.c.Hkv + jn.h) * p.c.max_pages * p.c.P + slot;
   p.w_out[at] = weight_before(p.w_in, p.decay, at, slot, r.T - r.n) + sum;
 }
@@ -457,7 +449,7 @@ cudaError_t launch_chunk_t(const WeightArgs& a, cudaStream_t stream) {
   e = launch_pdl(chunk_weights_kernel<D, P>, dim3(a.num_sms), dim3(kThreads), smem, stream, tq, tk,
                  p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(weights_join_kernel, dim3(a.num_sms), dim3(kTileKeys), 0, stream, p);
+  return launch_pdl(weights_join_kernel, dim3(a.num_sms), dim3(kItemKeys), 0, stream, p);
 }
 
 // =============================================================== decode form
