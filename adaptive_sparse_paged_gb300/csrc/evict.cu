@@ -48,6 +48,7 @@ __device__ __forceinline__ uint32_t ordered(float w) {
 
 constexpr int kPerThread = 4;                       // slots of a thread in one step
 constexpr int kStep = kSelThreads * kPerThread;
+constexpr int kHeld = 6;                            // steps whose slots stay in registers
 
 // Exclusive prefix sum over the CTA's threads; `total` gets the whole sum.
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, uint32_t& total) {
@@ -105,6 +106,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
     }
     return x;
   };
+  // The first steps' weights are read once, all loads in flight; later ones (of segments
+  // over kHeld * kStep slots) again in every pass.
+  float4 held[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) held[k] = load4(k * kStep + tid * kPerThread, T);
   const int m = T - p.recent, need0 = p.keep - p.recent;  // need0 of the first m slots stay
   uint32_t prefix = 0;
   int need = need0;
@@ -112,9 +118,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
     for (int shift = 24; shift >= 0; shift -= 8) {
       for (int i = tid; i < 256 * 32; i += kSelThreads) hist[i] = 0;
       __syncthreads();
-      for (int i0 = 0; i0 < m; i0 += kStep) {
+      auto count = [&](int i0, const float4& x) {
         const int i = i0 + tid * kPerThread;
-        const float4 x = load4(i, m);
         const float y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -122,7 +127,12 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
           if (i + k < m && (shift == 24 || (u >> (shift + 8)) == prefix))
             atomicAdd(&hist[((u >> shift) & 255) * 32 + lane], 1);
         }
-      }
+      };
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k)
+        if (k * kStep < m) count(k * kStep, held[k]);
+      for (int i0 = kHeld * kStep; i0 < m; i0 += kStep)
+        count(i0, load4(i0 + tid * kPerThread, m));
       __syncthreads();
       // bin sums: a warp adds up eight bins, a lane a column
 #pragma unroll
@@ -167,9 +177,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
   if (all_equal) need = 0x7fffffff;
   int above_before = 0, equal_before = 0;
   int par = 0;
-  for (int i0 = 0; i0 < T; i0 += kStep, par ^= 1) {
+  float4 next = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto emit = [&](int i0, const float4& x) {
     const int i = i0 + tid * kPerThread;
-    const float4 x = load4(i, T);
     const float y[4] = {x.x, x.y, x.z, x.w};
     bool over[4], same[4];
     uint32_t cnt = 0;  // above in the low half, equal in the high half: at most 4096 each
@@ -196,6 +206,17 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
     }
     above_before += (int)(total & 0xffff);
     equal_before += (int)(total >> 16);
+    par ^= 1;
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (k * kStep < T) emit(k * kStep, held[k]);
+  // a step's slots are read before the step before is written: it writes lower slots only
+  if (kHeld * kStep < T) next = load4(kHeld * kStep + tid * kPerThread, T);
+  for (int i0 = kHeld * kStep; i0 < T; i0 += kStep) {
+    const float4 x = next;
+    next = load4(i0 + kStep + tid * kPerThread, T);
+    emit(i0, x);
   }
 }
 

@@ -19,7 +19,7 @@
 // product with the integer position wraps exactly modulo one turn, so that
 // position 2^31 is as exact as position 0 (in 32-bit floats an angle of 10^5
 // radians is off by 0.004).
-#include "asp_internal.cuh"
+#include "tc.cuh"
 
 namespace asp {
 namespace {
@@ -62,9 +62,21 @@ __device__ __forceinline__ float2 unpack(uint32_t x) {
   return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&x));
 }
 
-__device__ __forceinline__ void unpack4(uint2 v, float* f) {
-  const float2 lo = unpack(v.x), hi = unpack(v.y);
-  f[0] = lo.x, f[1] = lo.y, f[2] = hi.x, f[3] = hi.y;
+// The a and b of a lane's four pairs: its first four channels and its second four, or,
+// interleaved, the even and the odd ones.
+__device__ __forceinline__ void pairs(const uint2 (&v)[2], float* a, float* b, bool interleaved) {
+  const float2 f[4] = {unpack(v[0].x), unpack(v[0].y), unpack(v[1].x), unpack(v[1].y)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (interleaved) {
+      a[i] = f[i].x;
+      b[i] = f[i].y;
+    } else {
+      float* to = i < 2 ? a : b;
+      to[2 * (i & 1)] = f[i].x;
+      to[2 * (i & 1) + 1] = f[i].y;
+    }
+  }
 }
 __device__ __forceinline__ uint2 pack4(const float* f) {
   return make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
@@ -76,33 +88,69 @@ __device__ __forceinline__ uint2 load4(const uint16_t* p) {
 // A lane's eight channels of a row are two times four. Halves rotated against each
 // other: channels a + i and b + i are pair i; interleaved: eight in a row. Lanes
 // past the rotated channels hold eight plain ones.
-// x normed, weighted and rotated in place; kLanes lanes of a row.
-template <int kLanes>
-__device__ __forceinline__ void norm_rotate(float (&x)[8], const uint2 (&wb)[2], bool norm,
-                                            float inv_d, float eps, bool turns, bool interleaved,
-                                            const float2 (&cs)[4]) {
-  if (norm) {
-    float ss = 0.f;
+// Weight and rotation of a lane's four pairs as one linear map, the same for all rows of
+// a token: (a, b) -> (a ac - b bs, b bc + a as), with the weights in the factors. Halves
+// that do not turn have cosine 1 and sine 0. Two pairs to a register pair.
+struct Map {
+  float2 ac[2], bs[2], bc[2], as[2];
+};
+
+__device__ __forceinline__ Map make_map(const float4 (&cs)[2], const uint2 (&w)[2], bool weighted,
+                                        bool turns, bool interleaved) {
+  float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
+  if (weighted) pairs(w, wa, wb, interleaved);
+  const float co[4] = {cs[0].x, cs[0].z, cs[1].x, cs[1].z};
+  const float si[4] = {cs[0].y, cs[0].w, cs[1].y, cs[1].w};
+  Map m;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+  for (int i = 0; i < 2; ++i) {
+    const float2 a = make_float2(wa[2 * i], wa[2 * i + 1]), b = make_float2(wb[2 * i], wb[2 * i + 1]);
+    const float2 c = turns ? make_float2(co[2 * i], co[2 * i + 1]) : make_float2(1.f, 1.f);
+    const float2 n = turns ? make_float2(si[2 * i], si[2 * i + 1]) : make_float2(0.f, 0.f);
+    m.ac[i] = mul2(a, c);
+    m.bs[i] = mul2(b, make_float2(-n.x, -n.y));
+    m.bc[i] = mul2(b, c);
+    m.as[i] = mul2(a, n);
+  }
+  return m;
+}
+
+// A row: the lane's channels x (two times four) normed and mapped; kLanes lanes of a row.
+template <int kLanes, bool kInterleaved>
+__device__ __forceinline__ void norm_rotate(const uint2 (&x)[2], const Map& m, bool norm,
+                                            float inv_d, float eps, float (&y)[8]) {
+  float fa[4], fb[4];
+  pairs(x, fa, fb, kInterleaved);
+  float2 a[2], b[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    a[i] = make_float2(fa[2 * i], fa[2 * i + 1]);
+    b[i] = make_float2(fb[2 * i], fb[2 * i + 1]);
+  }
+  if (norm) {
+    float2 sq = mul2(a[0], a[0]);
+    sq = fma2(a[1], a[1], sq);
+    sq = fma2(b[0], b[0], sq);
+    sq = fma2(b[1], b[1], sq);
+    float ss = sq.x + sq.y;
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
     const float r = rsqrtf(fmaf(ss, inv_d, eps));
-    float w[8];
-    unpack4(wb[0], w);
-    unpack4(wb[1], w + 4);
+    const float2 rr = make_float2(r, r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-  }
-  if (turns) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // pairs (i, 4 + i), or (2i, 2i + 1) of the eight
-      const int ia = interleaved ? 2 * i : i, ib = interleaved ? 2 * i + 1 : 4 + i;
-      const float a = x[ia], b = x[ib];
-      x[ia] = a * cs[i].x - b * cs[i].y;
-      x[ib] = b * cs[i].x + a * cs[i].y;
+    for (int i = 0; i < 2; ++i) {
+      a[i] = mul2(a[i], rr);
+      b[i] = mul2(b[i], rr);
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 ya = fma2(b[i], m.bs[i], mul2(a[i], m.ac[i]));
+    const float2 yb = fma2(a[i], m.as[i], mul2(b[i], m.bc[i]));
+    y[kInterleaved ? 4 * i : 2 * i] = ya.x;
+    y[kInterleaved ? 4 * i + 1 : 4 + 2 * i] = yb.x;
+    y[kInterleaved ? 4 * i + 2 : 2 * i + 1] = ya.y;
+    y[kInterleaved ? 4 * i + 3 : 5 + 2 * i] = yb.y;
   }
 }
 
@@ -242,23 +290,23 @@ __global__ void __launch_bounds__(kThreads) norm_rotate_kernel(const Params p) {
     const uint16_t* q = reinterpret_cast<const uint16_t*>(smem + st * stage_bytes);
     const uint16_t* k = q + p.nq * D;
     const uint16_t* v = k + p.nk * D;
-    float2 cs[4];
+    float4 cs[2];
     if (turns) {
       const float4* src = reinterpret_cast<const float4*>(sh.turn + t * (D / 2) + 4 * l);
-      const float4 x = src[0], y = src[1];
-      cs[0] = make_float2(x.x, x.y), cs[1] = make_float2(x.z, x.w);
-      cs[2] = make_float2(y.x, y.y), cs[3] = make_float2(y.z, y.w);
+      cs[0] = src[0], cs[1] = src[1];
     }
-    auto row_at = [&](const uint16_t* base, int r, float (&x)[8]) {
-      unpack4(*reinterpret_cast<const uint2*>(base + r * D + ca), x);
-      unpack4(*reinterpret_cast<const uint2*>(base + r * D + cb), x + 4);
+    const Map mq = make_map(cs, wq, p.q_weight != nullptr, turns, kInterleaved);
+    auto row_at = [&](const uint16_t* base, int r, uint2 (&x)[2]) {
+      x[0] = *reinterpret_cast<const uint2*>(base + r * D + ca);
+      x[1] = *reinterpret_cast<const uint2*>(base + r * D + cb);
     };
 #pragma unroll 2
     for (int g = warp; g * kRows < nq; g += kWarps) {
       const int r = g * kRows + sub;
+      uint2 in[2];
       float x[8];
-      row_at(q, min(r, nq - 1), x);
-      norm_rotate<kLanes>(x, wq, p.q_weight != nullptr, inv_d, p.eps, turns, kInterleaved, cs);
+      row_at(q, min(r, nq - 1), in);
+      norm_rotate<kLanes, kInterleaved>(in, mq, p.q_weight != nullptr, inv_d, p.eps, x);
       if (r >= nq) continue;
       const size_t o = ((size_t)(row0 + t) * p.Hq + q0 + r) * D;
       if (p.q_out) {
@@ -271,9 +319,11 @@ __global__ void __launch_bounds__(kThreads) norm_rotate_kernel(const Params p) {
       }
     }
     if (mapped && k_mine) {
+      uint2 in[2];
       float x[8];
-      row_at(k, min(kh, nk - 1), x);
-      norm_rotate<kLanes>(x, wk, p.k_weight != nullptr, inv_d, p.eps, turns, kInterleaved, cs);
+      row_at(k, min(kh, nk - 1), in);
+      const Map mk = make_map(cs, wk, p.k_weight != nullptr, turns, kInterleaved);
+      norm_rotate<kLanes, kInterleaved>(in, mk, p.k_weight != nullptr, inv_d, p.eps, x);
       if (k_row) {
         uint16_t* dst = p.k + (k_block + (size_t)kh * P + (lo + t) % P) * D;
         const uint2 ya = pack4(x), yb = pack4(x + 4);
