@@ -4,16 +4,18 @@
 //
 //   y = x * rsqrt(mean(x^2) + eps) * weight;  (a, b) -> (a cos - b sin, b cos + a sin)
 //
-// One work item is one page of one request: the new tokens that fall into it.
-// Its CTA computes each token's cosines and sines once, in shared memory, for all
-// heads, while a loader thread streams the tokens' rows (contiguous in the packed
-// array) through a ring of shared-memory stages, so that what is in flight does
-// not cost registers: with the loads in registers the kernel took 110 us for 16k
-// tokens of 48 heads, and 173 where smaller register budgets made them spill.
-// Warps take rows; a row is d / 8 lanes wide, and a lane holds the two halves of
-// four rotated pairs, so a pair never crosses lanes. A warp keeps the same key
-// heads for all tokens, their channel minima and maxima in registers until the
-// page is done: the summary is written once, without atomics.
+// One work item is one page of one request: the new tokens that fall into it. CTAs
+// take items in turn; a loader warp looks the next ones up and streams their
+// tokens' rows (contiguous in the packed array) through a ring of shared-memory stages.
+// The angles of 16 tokens are computed once, in shared memory, for all heads.
+//
+// HBM gives the rows about as fast as the SMs can issue the arithmetic, so rows take few
+// instructions (d / 8 lanes hold a row, a lane the two halves of four rotated pairs, so
+// that a pair never crosses lanes; two-wide fp32 operations) and many warps cover one
+// another's latencies: two CTAs an SM, in registers that do not spill (with all of the
+// SM's memory given to the rings a spilled register comes back from L2). A warp keeps the
+// same key heads for all tokens of an item, their channel minima and maxima in registers
+// until the page is done: the summary is written once, without atomics.
 //
 // The angle: a frequency becomes a 64-bit fixed-point fraction of a turn, whose
 // product with the integer position wraps exactly modulo one turn, so that
@@ -24,8 +26,9 @@
 namespace asp {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 7;
 constexpr int kThreads = (kWarps + 1) * 32;  // and a loader
+constexpr int kCtas = 2;                     // CTAs of an SM
 constexpr int kMaxStages = 16;
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -45,7 +48,7 @@ struct Params {
   const int32_t* seq_lens;
   uint32_t* err;
   int B, Hq, Hkv, max_pages, num_phys, num_tokens;
-  int rot, nq, nk, stages;  // nq, nk: query and KV heads of a CTA
+  int rot, nq, nk, stages, items;  // nq, nk: query and KV heads of a CTA
   float eps;
 };
 
@@ -59,113 +62,83 @@ __device__ __forceinline__ int first_item(const int32_t* q_offsets, int b, int n
 }
 
 __device__ __forceinline__ float2 unpack(uint32_t x) {
-  return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&x));
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
 }
+__device__ __forceinline__ uint32_t pack(float2 f) { return pack_bf16(f.x, f.y); }
 
-// The a and b of a lane's four pairs: its first four channels and its second four, or,
-// interleaved, the even and the odd ones.
-__device__ __forceinline__ void pairs(const uint2 (&v)[2], float* a, float* b, bool interleaved) {
-  const float2 f[4] = {unpack(v[0].x), unpack(v[0].y), unpack(v[1].x), unpack(v[1].y)};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (interleaved) {
-      a[i] = f[i].x;
-      b[i] = f[i].y;
-    } else {
-      float* to = i < 2 ? a : b;
-      to[2 * (i & 1)] = f[i].x;
-      to[2 * (i & 1) + 1] = f[i].y;
-    }
-  }
-}
-__device__ __forceinline__ uint2 pack4(const float* f) {
-  return make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
-}
 __device__ __forceinline__ uint2 load4(const uint16_t* p) {
   return __ldg(reinterpret_cast<const uint2*>(p));
 }
 
-// A lane's eight channels of a row are two times four. Halves rotated against each
-// other: channels a + i and b + i are pair i; interleaved: eight in a row. Lanes
-// past the rotated channels hold eight plain ones.
-// Weight and rotation of a lane's four pairs as one linear map, the same for all rows of
-// a token: (a, b) -> (a ac - b bs, b bc + a as), with the weights in the factors. Halves
-// that do not turn have cosine 1 and sine 0. Two pairs to a register pair.
-struct Map {
-  float2 ac[2], bs[2], bc[2], as[2];
-};
-
-__device__ __forceinline__ Map make_map(const float4 (&cs)[2], const uint2 (&w)[2], bool weighted,
-                                        bool turns, bool interleaved) {
-  float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
-  if (weighted) pairs(w, wa, wb, interleaved);
-  const float co[4] = {cs[0].x, cs[0].z, cs[1].x, cs[1].z};
-  const float si[4] = {cs[0].y, cs[0].w, cs[1].y, cs[1].w};
-  Map m;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float2 a = make_float2(wa[2 * i], wa[2 * i + 1]), b = make_float2(wb[2 * i], wb[2 * i + 1]);
-    const float2 c = turns ? make_float2(co[2 * i], co[2 * i + 1]) : make_float2(1.f, 1.f);
-    const float2 n = turns ? make_float2(si[2 * i], si[2 * i + 1]) : make_float2(0.f, 0.f);
-    m.ac[i] = mul2(a, c);
-    m.bs[i] = mul2(b, make_float2(-n.x, -n.y));
-    m.bc[i] = mul2(b, c);
-    m.as[i] = mul2(a, n);
+// A lane's eight channels of a row, two to an element: 0, 1 its first four, 2, 3 its second
+// four. Halves rotated against each other: pair i is channel i of the first and of the
+// second four; interleaved: channels 2i and 2i + 1 of the eight.
+struct Row {
+  float2 f[4];
+  __device__ __forceinline__ void set(const uint2& a, const uint2& b) {
+    f[0] = unpack(a.x), f[1] = unpack(a.y), f[2] = unpack(b.x), f[3] = unpack(b.y);
   }
-  return m;
-}
-
-// A row: the lane's channels x (two times four) normed and mapped; kLanes lanes of a row.
-template <int kLanes, bool kInterleaved>
-__device__ __forceinline__ void norm_rotate(const uint2 (&x)[2], const Map& m, bool norm,
-                                            float inv_d, float eps, float (&y)[8]) {
-  float fa[4], fb[4];
-  pairs(x, fa, fb, kInterleaved);
-  float2 a[2], b[2];
+  __device__ __forceinline__ uint2 first() const { return make_uint2(pack(f[0]), pack(f[1])); }
+  __device__ __forceinline__ uint2 second() const { return make_uint2(pack(f[2]), pack(f[3])); }
+  // kLanes lanes of a row; w: the lane's weights, as bf16
+  template <int kLanes>
+  __device__ __forceinline__ void norm(const uint2 (&w)[2], float inv_d, float eps) {
+    float2 sq = mul2(f[0], f[0]);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    a[i] = make_float2(fa[2 * i], fa[2 * i + 1]);
-    b[i] = make_float2(fb[2 * i], fb[2 * i + 1]);
-  }
-  if (norm) {
-    float2 sq = mul2(a[0], a[0]);
-    sq = fma2(a[1], a[1], sq);
-    sq = fma2(b[0], b[0], sq);
-    sq = fma2(b[1], b[1], sq);
+    for (int i = 1; i < 4; ++i) sq = fma2(f[i], f[i], sq);
     float ss = sq.x + sq.y;
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
     const float r = rsqrtf(fmaf(ss, inv_d, eps));
     const float2 rr = make_float2(r, r);
+    Row wf;
+    wf.set(w[0], w[1]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      a[i] = mul2(a[i], rr);
-      b[i] = mul2(b[i], rr);
+    for (int i = 0; i < 4; ++i) f[i] = mul2(mul2(f[i], wf.f[i]), rr);
+  }
+  // cs: (cos, sin) of the four pairs
+  template <bool kInterleaved>
+  __device__ __forceinline__ void turn(const float4 (&cs)[2]) {
+    if (kInterleaved) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float c = i & 1 ? cs[i / 2].z : cs[i / 2].x, sn = i & 1 ? cs[i / 2].w : cs[i / 2].y;
+        f[i] = make_float2(f[i].x * c - f[i].y * sn, f[i].y * c + f[i].x * sn);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 a = f[i], b = f[2 + i];
+        const float2 c = make_float2(cs[i].x, cs[i].z), sn = make_float2(cs[i].y, cs[i].w);
+        f[i] = fma2(b, make_float2(-sn.x, -sn.y), mul2(a, c));
+        f[2 + i] = fma2(a, sn, mul2(b, c));
+      }
     }
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float2 ya = fma2(b[i], m.bs[i], mul2(a[i], m.ac[i]));
-    const float2 yb = fma2(a[i], m.as[i], mul2(b[i], m.bc[i]));
-    y[kInterleaved ? 4 * i : 2 * i] = ya.x;
-    y[kInterleaved ? 4 * i + 1 : 4 + 2 * i] = yb.x;
-    y[kInterleaved ? 4 * i + 2 : 2 * i + 1] = ya.y;
-    y[kInterleaved ? 4 * i + 3 : 5 + 2 * i] = yb.y;
-  }
-}
+};
+
+// A work item, found by the loader warp; b < 0: no more.
+struct Item {
+  int b, page, lo, cnt;  // the new slots lo .. lo + cnt - 1, all in this page
+  int row0, phys;        // the first's packed row; physical page, -1: none
+};
+constexpr int kItems = 3;      // items known ahead
+constexpr int kTurnTokens = 16;  // tokens whose angles are computed together
 
 // Shared memory of a CTA: the ring, then these.
-template <int D, int P>
+template <int D>
 struct Shared {
-  float2 turn[P * (D / 2)];             // (cos, sin) of [token of the page][pair]
-  unsigned long long turns_of[D / 2];   // 2^64 * inv_freq / (2 pi), modulo 2^64
-  uint64_t full[kMaxStages], empty[kMaxStages];
+  float2 turn[2][kTurnTokens * (D / 2)];  // (cos, sin) of [token][pair]
+  unsigned long long turns_of[D / 2];     // 2^64 * inv_freq / (2 pi), modulo 2^64
+  Item item[kItems];
+  uint64_t full[kMaxStages], empty[kMaxStages], item_full[kItems], item_empty[kItems], turn_full[2];
 };
 
 template <int D, int P, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) norm_rotate_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kCtas) norm_rotate_kernel(const Params p) {
   constexpr int kLanes = D / 8;        // lanes of one row
   constexpr int kRows = 32 / kLanes;   // rows a warp takes at once
+  static_assert(kWarps * kRows >= 8, "a group of key heads a warp at most");
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int sub = lane / kLanes, l = lane % kLanes;
@@ -173,95 +146,106 @@ __global__ void __launch_bounds__(kThreads) norm_rotate_kernel(const Params p) {
   const int q0 = blockIdx.y * p.nq, nq = max(0, min(p.nq, p.Hq - q0));
   const int k0 = blockIdx.y * p.nk, nk = max(0, min(p.nk, p.Hkv - k0));
   const int stage_bytes = (p.nq + 2 * p.nk) * D * 2;
-  Shared<D, P>& sh = *reinterpret_cast<Shared<D, P>*>(smem + p.stages * stage_bytes);
+  Shared<D>& sh = *reinterpret_cast<Shared<D>*>(smem + p.stages * stage_bytes);
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], kWarps);
     }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&sh.item_full[i], 1);
+      mbar_init(&sh.item_empty[i], kWarps);
+    }
+    mbar_init(&sh.turn_full[0], kWarps);
+    mbar_init(&sh.turn_full[1], kWarps);
     mbar_fence_init();
   }
   pdl_launch_dependents();
   pdl_wait_predecessor();
-
-  if (p.q_offsets && blockIdx.x == 0 && blockIdx.y == 0) {  // every request's rows are checked
-    for (int x = tid; x < p.B; x += kThreads)
-      new_rows(p.q_offsets, x, clamp_seq_len(p.seq_lens[x], p.max_pages, P, p.err), p.num_tokens,
-               p.err);
-  }
   const int half = p.rot / 2;
   if (tid < half) {
     double t = (double)p.inv_freq[tid] * 0.15915494309189533577;  // 1 / (2 pi)
     t -= floor(t);
     sh.turns_of[tid] = (unsigned long long)(t * 18446744073709551616.0);
   }
-
-  // the item's request: the last whose first item is not past it
-  int b, page_of_b;
-  if (p.q_offsets) {
-    int before = 0;
-    for (int x = 0; x < p.B; x += kThreads)
-      before += __syncthreads_count(x + tid < p.B && first_item<P>(p.q_offsets, x + tid,
-                                                                  p.num_tokens) <= (int)blockIdx.x);
-    b = before - 1;  // offsets that do not ascend: some request of the batch
-    if (b < 0) return;
-    page_of_b = blockIdx.x - first_item<P>(p.q_offsets, b, p.num_tokens);
-  } else {
-    b = blockIdx.x;
-    page_of_b = 0;
-  }
-  const int T = clamp_seq_len(p.seq_lens[b], p.max_pages, P, tid == 0 ? p.err : nullptr);
-  const NewRows nr = new_rows(p.q_offsets, b, T, p.num_tokens, tid == 0 ? p.err : nullptr);
-  const int first = T - nr.n;                       // slot of the first new token
-  const int page = first / P + page_of_b;
-  const int lo = max(first, page * P), hi = min(T, (page + 1) * P);
-  if (lo >= hi || page_of_b < 0) return;
-  const int row0 = nr.row0 + (lo - first), cnt = hi - lo;  // packed rows of the item
-  const int Hall = p.Hq + 2 * p.Hkv;
-  __syncthreads();  // barriers and turns_of are set
+  __syncthreads();
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ loader
-    if (lane != 0) return;
+    if (p.q_offsets && blockIdx.x == 0 && blockIdx.y == 0) {  // every request's rows are checked
+      for (int x = lane; x < p.B; x += 32)
+        new_rows(p.q_offsets, x, clamp_seq_len(p.seq_lens[x], p.max_pages, P, p.err),
+                 p.num_tokens, p.err);
+    }
     const uint32_t bytes = (uint32_t)(nq + 2 * nk) * D * 2;
-    if (bytes == 0) return;
-    int t = 0;
+    const int Hall = p.Hq + 2 * p.Hkv;
+    uint32_t tk = 0, n = 0;  // tokens loaded, items handed on
     bool ok = true;
-    for (; t < cnt; ++t) {
-      const int st = t % p.stages;
-      ok = mbar_wait(&sh.empty[st], ((t / p.stages) & 1) ^ 1);
+    for (int it = blockIdx.x; ok; it += gridDim.x) {
+      Item x{-1, 0, 0, 0, 0, -1};
+      if (it < p.items) {
+        // the item's request: the last whose first item is not past it
+        int b = it, page_of_b = 0;
+        if (p.q_offsets) {
+          int before = 0;
+          for (int y = lane; y < p.B; y += 32)
+            before += first_item<P>(p.q_offsets, y, p.num_tokens) <= it;
+          b = __reduce_add_sync(kFull, before) - 1;
+          if (b < 0) continue;  // offsets that do not ascend
+          page_of_b = it - first_item<P>(p.q_offsets, b, p.num_tokens);
+        }
+        uint32_t* err = lane == 0 ? p.err : nullptr;
+        const int T = clamp_seq_len(p.seq_lens[b], p.max_pages, P, err);
+        const NewRows nr = new_rows(p.q_offsets, b, T, p.num_tokens, err);
+        const int first = T - nr.n;  // slot of the first new token
+        x.page = first / P + page_of_b;
+        x.lo = max(first, x.page * P);
+        x.cnt = min(T, (x.page + 1) * P) - x.lo;
+        if (x.cnt <= 0 || page_of_b < 0) continue;
+        x.b = b;
+        x.row0 = nr.row0 + (x.lo - first);
+        x.phys = p.bt[(size_t)b * p.max_pages + x.page];
+        if (x.phys < 0 || x.phys >= p.num_phys) {
+          report(err, ASP_DEVERR_PAGE_RANGE);
+          x.phys = -1;
+        }
+      }
+      const int slot = n % kItems;
+      ok = __all_sync(kFull, mbar_wait(&sh.item_empty[slot], ((n / kItems) & 1) ^ 1));
       if (!ok) break;
-      const uint16_t* row = p.qkv + (size_t)(row0 + t) * Hall * D;
-      uint8_t* dst = smem + st * stage_bytes;
-      mbar_arrive_expect_tx(&sh.full[st], bytes);
-      if (nq > 0) bulk_g2s(dst, row + q0 * D, nq * D * 2, &sh.full[st]);
-      if (nk > 0) {
-        dst += p.nq * D * 2;
-        bulk_g2s(dst, row + (p.Hq + k0) * D, nk * D * 2, &sh.full[st]);
-        bulk_g2s(dst + p.nk * D * 2, row + (p.Hq + p.Hkv + k0) * D, nk * D * 2, &sh.full[st]);
+      if (lane == 0) {
+        sh.item[slot] = x;
+        mbar_arrive(&sh.item_full[slot]);
+      }
+      ++n;
+      if (x.b < 0) break;
+      if (bytes == 0) continue;
+      for (int t = 0; t < x.cnt; ++t, ++tk) {
+        const int st = tk % p.stages;
+        ok = __all_sync(kFull, mbar_wait(&sh.empty[st], ((tk / p.stages) & 1) ^ 1));
+        if (!ok) break;
+        if (lane == 0) {
+          const uint16_t* row = p.qkv + (size_t)(x.row0 + t) * Hall * D;
+          uint8_t* dst = smem + st * stage_bytes;
+          mbar_arrive_expect_tx(&sh.full[st], bytes);
+          if (nq > 0) bulk_g2s(dst, row + q0 * D, nq * D * 2, &sh.full[st]);
+          if (nk > 0) {
+            dst += p.nq * D * 2;
+            bulk_g2s(dst, row + (p.Hq + k0) * D, nk * D * 2, &sh.full[st]);
+            bulk_g2s(dst + p.nk * D * 2, row + (p.Hq + p.Hkv + k0) * D, nk * D * 2, &sh.full[st]);
+          }
+        }
       }
     }
+    if (!ok && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
     // the CTA's memory stays until its copies have ended
-    if (!ok) report(p.err, ASP_DEVERR_TIMEOUT);
-    for (int i = max(0, t - p.stages); i < t; ++i)
-      mbar_wait(&sh.full[i % p.stages], (i / p.stages) & 1);
+    if (bytes && lane == 0)
+      for (uint32_t i = tk > (uint32_t)p.stages ? tk - p.stages : 0; i < tk; ++i)
+        mbar_wait(&sh.full[i % p.stages], (i / p.stages) & 1);
     return;
   }
 
-  for (int i = tid; i < cnt * half; i += kWarps * 32) {
-    const int t = i / half, f = i % half;
-    const int pos = p.positions ? p.positions[row0 + t] : lo + t;
-    const unsigned long long phase = sh.turns_of[f] * (unsigned long long)(long long)pos;
-    float s, c;
-    sincospif((float)(int)(phase >> 32) * 4.656612873077393e-10f, &s, &c);  // 2 * 2^-32 half turns
-    sh.turn[t * (D / 2) + f] = make_float2(c, s);
-  }
-  const int phys = p.bt[(size_t)b * p.max_pages + page];
-  const bool mapped = phys >= 0 && phys < p.num_phys;
-  if (!mapped && tid == 0) report(p.err, ASP_DEVERR_PAGE_RANGE);
-  named_bar_sync(1, kWarps * 32);
-
-  // the lane's channels, and its weights
+  // the lane's channels and weights
   const bool turns = 8 * l < p.rot, split = turns && !kInterleaved;
   const int ca = split ? 4 * l : 8 * l, cb = split ? half + 4 * l : 8 * l + 4;
   const float inv_d = 1.0f / D;
@@ -274,88 +258,116 @@ __global__ void __launch_bounds__(kThreads) norm_rotate_kernel(const Params p) {
     wk[0] = load4(p.k_weight + ca);
     wk[1] = load4(p.k_weight + cb);
   }
-  // rows of this warp: query rows (warp + 8 i) * kRows + sub, one group of key heads,
-  // and, from the other end, groups of value heads
-  const int kh = warp * kRows + sub;
-  const bool k_mine = warp * kRows < nk, k_row = kh < nk;
-  const size_t k_block = mapped ? ((size_t)phys * p.Hkv + k0) * P : 0;
-  // folding starts from values that any key replaces
-  uint2 mn[2] = {make_uint2(0x7f807f80u, 0x7f807f80u), make_uint2(0x7f807f80u, 0x7f807f80u)};
-  uint2 mx[2] = {make_uint2(0xff80ff80u, 0xff80ff80u), make_uint2(0xff80ff80u, 0xff80ff80u)};
+  // The warp's rows of a stage, kRows at a time: the groups of key heads go to the first
+  // warps, those of query heads on from there in turn, those of value heads from the last.
+  const int k_groups = ceil_div(nk, kRows);
+  const int kh = warp * kRows + sub, vh = (kWarps - 1 - warp) * kRows + sub;
+  const bool k_mine = warp < k_groups, k_row = kh < nk;
+  const int q_first = (warp - k_groups + kWarps) % kWarps;
+  uint32_t tk = 0, blk = 0;
   bool ok = true;
-  for (int t = 0; t < cnt; ++t) {
-    const int st = t % p.stages;
-    if (nq + nk > 0) ok = __all_sync(kFull, mbar_wait(&sh.full[st], (t / p.stages) & 1));
+  for (uint32_t n = 0; ok; ++n) {
+    const int slot = n % kItems;
+    ok = __all_sync(kFull, mbar_wait(&sh.item_full[slot], (n / kItems) & 1));
     if (!ok) break;
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(smem + st * stage_bytes);
-    const uint16_t* k = q + p.nq * D;
-    const uint16_t* v = k + p.nk * D;
-    float4 cs[2];
-    if (turns) {
-      const float4* src = reinterpret_cast<const float4*>(sh.turn + t * (D / 2) + 4 * l);
-      cs[0] = src[0], cs[1] = src[1];
-    }
-    const Map mq = make_map(cs, wq, p.q_weight != nullptr, turns, kInterleaved);
-    auto row_at = [&](const uint16_t* base, int r, uint2 (&x)[2]) {
-      x[0] = *reinterpret_cast<const uint2*>(base + r * D + ca);
-      x[1] = *reinterpret_cast<const uint2*>(base + r * D + cb);
-    };
-#pragma unroll 2
-    for (int g = warp; g * kRows < nq; g += kWarps) {
-      const int r = g * kRows + sub;
-      uint2 in[2];
-      float x[8];
-      row_at(q, min(r, nq - 1), in);
-      norm_rotate<kLanes, kInterleaved>(in, mq, p.q_weight != nullptr, inv_d, p.eps, x);
-      if (r >= nq) continue;
-      const size_t o = ((size_t)(row0 + t) * p.Hq + q0 + r) * D;
-      if (p.q_out) {
-        *reinterpret_cast<uint2*>(p.q_out + o + ca) = pack4(x);
-        *reinterpret_cast<uint2*>(p.q_out + o + cb) = pack4(x + 4);
-      }
-      if (p.q_out_f32) {
-        *reinterpret_cast<float4*>(p.q_out_f32 + o + ca) = make_float4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<float4*>(p.q_out_f32 + o + cb) = make_float4(x[4], x[5], x[6], x[7]);
-      }
-    }
-    if (mapped && k_mine) {
-      uint2 in[2];
-      float x[8];
-      row_at(k, min(kh, nk - 1), in);
-      const Map mk = make_map(cs, wk, p.k_weight != nullptr, turns, kInterleaved);
-      norm_rotate<kLanes, kInterleaved>(in, mk, p.k_weight != nullptr, inv_d, p.eps, x);
-      if (k_row) {
-        uint16_t* dst = p.k + (k_block + (size_t)kh * P + (lo + t) % P) * D;
-        const uint2 ya = pack4(x), yb = pack4(x + 4);
-        *reinterpret_cast<uint2*>(dst + ca) = ya;
-        *reinterpret_cast<uint2*>(dst + cb) = yb;
-        mn[0] = vmin(mn[0], ya), mn[1] = vmin(mn[1], yb);
-        mx[0] = vmax(mx[0], ya), mx[1] = vmax(mx[1], yb);
-      }
-    }
-    if (mapped) {
-      const int vh = (kWarps - 1 - warp) * kRows + sub;  // nk <= 8: one group at most
-      if (vh < nk)
-        *reinterpret_cast<uint4*>(p.v + (k_block + (size_t)vh * P + (lo + t) % P) * D + 8 * l) =
-            *reinterpret_cast<const uint4*>(v + vh * D + 8 * l);
-    }
+    const Item it = sh.item[slot];
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.empty[st]);
-  }
-  if (!ok) {
-    if (lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
-    return;
-  }
-  if (!mapped || !k_row) return;
-  uint16_t* s = p.summ + (((size_t)b * p.Hkv + k0 + kh) * p.max_pages + page) * 2 * D;
-  const bool fresh = lo == page * P;
+    if (lane == 0) mbar_arrive(&sh.item_empty[slot]);
+    if (it.b < 0) break;
+    const bool mapped = it.phys >= 0;
+    const size_t k_block = mapped ? ((size_t)it.phys * p.Hkv + k0) * P : 0;
+    // folding starts from values that any key replaces
+    constexpr uint32_t kInf = 0x7f807f80u, kNegInf = 0xff80ff80u;
+    uint2 mn[2] = {make_uint2(kInf, kInf), make_uint2(kInf, kInf)};
+    uint2 mx[2] = {make_uint2(kNegInf, kNegInf), make_uint2(kNegInf, kNegInf)};
+    for (int t = 0; t < it.cnt; ++t, ++tk) {
+      const float2* turn = sh.turn[(blk - 1) & 1];
+      if (t % kTurnTokens == 0) {
+        // the angles of the next tokens, into the table that no warp reads any more: all
+        // have passed the barrier of the one between
+        float2* to = sh.turn[blk & 1];
+        turn = to;
+        const int cnt = min(kTurnTokens, it.cnt - t);
+        for (int i = tid; i < cnt * half; i += kWarps * 32) {
+          const int tt = t + i / half, f = i % half;
+          const int pos = p.positions ? p.positions[it.row0 + tt] : it.lo + tt;
+          const unsigned long long phase = sh.turns_of[f] * (unsigned long long)(long long)pos;
+          float sn, c;
+          // 2 * 2^-32 half turns
+          sincospif((float)(int)(phase >> 32) * 4.656612873077393e-10f, &sn, &c);
+          to[i / half * (D / 2) + f] = make_float2(c, sn);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.turn_full[blk & 1]);
+        ok = __all_sync(kFull, mbar_wait(&sh.turn_full[blk & 1], (blk >> 1) & 1));
+        if (!ok) break;
+        ++blk;
+      }
+      const int st = tk % p.stages;
+      if (nq + nk > 0) ok = __all_sync(kFull, mbar_wait(&sh.full[st], (tk / p.stages) & 1));
+      if (!ok) break;
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(smem + st * stage_bytes);
+      const uint16_t* k = q + p.nq * D;
+      float4 cs[2];
+      if (turns) {
+        const float4* src =
+            reinterpret_cast<const float4*>(turn + t % kTurnTokens * (D / 2) + 4 * l);
+        cs[0] = src[0], cs[1] = src[1];
+      }
+      auto make = [&](const uint16_t* src, const uint2 (&w)[2], bool normed, Row& x) {
+        x.set(*reinterpret_cast<const uint2*>(src + ca), *reinterpret_cast<const uint2*>(src + cb));
+        if (normed) x.norm<kLanes>(w, inv_d, p.eps);
+        if (turns) x.turn<kInterleaved>(cs);
+      };
+      const size_t slot = (size_t)((it.lo + t) % P) * D;
+      if (mapped && k_mine) {
+        Row x;
+        make(k + min(kh, nk - 1) * D, wk, p.k_weight != nullptr, x);
+        if (k_row) {
+          uint16_t* dst = p.k + (k_block + (size_t)kh * P) * D + slot;
+          const uint2 a = x.first(), b = x.second();
+          *reinterpret_cast<uint2*>(dst + ca) = a;
+          *reinterpret_cast<uint2*>(dst + cb) = b;
+          mn[0] = vmin(mn[0], a), mn[1] = vmin(mn[1], b);
+          mx[0] = vmax(mx[0], a), mx[1] = vmax(mx[1], b);
+        }
+      }
+      for (int r0 = q_first * kRows; r0 < nq; r0 += kWarps * kRows) {
+        const int r = r0 + sub;
+        Row x;
+        make(q + min(r, nq - 1) * D, wq, p.q_weight != nullptr, x);
+        if (r >= nq) continue;
+        const size_t o = ((size_t)(it.row0 + t) * p.Hq + q0 + r) * D;
+        if (p.q_out) {
+          *reinterpret_cast<uint2*>(p.q_out + o + ca) = x.first();
+          *reinterpret_cast<uint2*>(p.q_out + o + cb) = x.second();
+        }
+        if (p.q_out_f32) {
+          *reinterpret_cast<float4*>(p.q_out_f32 + o + ca) =
+              make_float4(x.f[0].x, x.f[0].y, x.f[1].x, x.f[1].y);
+          *reinterpret_cast<float4*>(p.q_out_f32 + o + cb) =
+              make_float4(x.f[2].x, x.f[2].y, x.f[3].x, x.f[3].y);
+        }
+      }
+      if (mapped && vh < nk)
+        *reinterpret_cast<uint4*>(p.v + (k_block + (size_t)vh * P) * D + slot + 8 * l) =
+            *reinterpret_cast<const uint4*>(k + (p.nk + vh) * D + 8 * l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty[st]);
+    }
+    if (!ok) break;
+    if (!mapped || !k_row) continue;
+    uint16_t* s = p.summ + (((size_t)it.b * p.Hkv + k0 + kh) * p.max_pages + it.page) * 2 * D;
+    const bool fresh = it.lo == it.page * P;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint2* smin = reinterpret_cast<uint2*>(s + (i ? cb : ca));
-    uint2* smax = reinterpret_cast<uint2*>(s + D + (i ? cb : ca));
-    *smin = fresh ? mn[i] : vmin(*smin, mn[i]);
-    *smax = fresh ? mx[i] : vmax(*smax, mx[i]);
+    for (int i = 0; i < 2; ++i) {
+      uint2* smin = reinterpret_cast<uint2*>(s + (i ? cb : ca));
+      uint2* smax = reinterpret_cast<uint2*>(s + D + (i ? cb : ca));
+      *smin = fresh ? mn[i] : vmin(*smin, mn[i]);
+      *smax = fresh ? mx[i] : vmax(*smax, mx[i]);
+    }
   }
+  if (!ok && lane == 0) report(p.err, ASP_DEVERR_TIMEOUT);
 }
 
 template <int D, int P>
@@ -363,22 +375,25 @@ cudaError_t launch_t(const NormRotateArgs& a, cudaStream_t stream) {
   const asp_paged_kv& kv = *a.kv;
   const int items = a.q_offsets ? a.num_tokens / P + 2 * kv.batch : kv.batch;
   // Few items: split their heads over several CTAs (each computes the angles
-  // again) until there are about four CTAs an SM, but not below a step of query rows for every warp.
-  const int split = max(1, min(4 * a.num_sms / items, kv.num_q_heads * D / (kWarps * 256)));
+  // again) until there are about four CTAs an SM, but not below a step of query
+  // rows for every warp. Many: kCtas an SM take them in turn, so that the next
+  // item is looked up and its rows are loaded while the last is worked on.
+  const int split = max(1, min(4 * a.num_sms / items, kv.num_q_heads * D / (8 * 256)));
+  const int ctas = min(items, split == 1 ? kCtas * a.num_sms : items);
   const int nq = ceil_div(kv.num_q_heads, split), nk = ceil_div(kv.num_kv_heads, split);
   const int stage_bytes = (nq + 2 * nk) * D * 2;
-  // as many stages as an item has tokens, in a third of an SM's shared memory at most
+  // up to sixteen tokens in a third of an SM's shared memory
   constexpr int kBudget = 72 * 1024;
-  const int stages = max(2, min(min(kMaxStages, P), kBudget / stage_bytes));
+  const int stages = max(2, min(kMaxStages, kBudget / stage_bytes));
   Params p{a.qkv, a.q_offsets, a.positions, a.q_weight, a.k_weight, a.inv_freq, a.q_out,
            a.q_out_f32, kv.k_cache, kv.v_cache, kv.summaries, kv.block_table, kv.seq_lens, a.err,
            kv.batch, kv.num_q_heads, kv.num_kv_heads, kv.max_pages, kv.num_phys_pages,
-           a.num_tokens, a.rotary_dim, nq, nk, stages, a.eps};
+           a.num_tokens, a.rotary_dim, nq, nk, stages, items, a.eps};
   auto kernel = a.interleaved ? norm_rotate_kernel<D, P, true> : norm_rotate_kernel<D, P, false>;
-  const int smem = stages * stage_bytes + (int)sizeof(Shared<D, P>);
-  cudaError_t e = set_max_dynamic_smem((const void*)kernel, kBudget + (int)sizeof(Shared<D, P>));
+  const int smem = stages * stage_bytes + (int)sizeof(Shared<D>);
+  cudaError_t e = set_max_dynamic_smem((const void*)kernel, kBudget + (int)sizeof(Shared<D>));
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(items, split), dim3(kThreads), smem, stream, p);
+  return launch_pdl(kernel, dim3(ctas, split), dim3(kThreads), smem, stream, p);
 }
 
 }  // namespace
