@@ -347,13 +347,14 @@ def asp_coverage_select_noalloc(kv: PagedKV, q: torch.Tensor, gamma: float, budg
             "asp_coverage_select_noalloc")
 
 
-def _weights_shape(kv: PagedKV):
+def weights_shape(kv: PagedKV):
+    """Shape of the attention weights of this cache: [B, Hkv, max_pages * P]."""
     return (kv.batch, kv.num_kv_heads, kv.max_pages * kv.page_size)
 
 
 def new_weights(kv: PagedKV) -> torch.Tensor:
     """Zeroed attention weights [B, Hkv, max_pages * P] fp32 for this cache."""
-    return torch.zeros(_weights_shape(kv), dtype=torch.float32, device=kv.device)
+    return torch.zeros(weights_shape(kv), dtype=torch.float32, device=kv.device)
 
 
 def _need_rows(kv: PagedKV, t: torch.Tensor, name: str, heads: int) -> int:
@@ -365,10 +366,10 @@ def _need_rows(kv: PagedKV, t: torch.Tensor, name: str, heads: int) -> int:
 
 
 def _need_weights(kv: PagedKV, w_in, w_out) -> int | None:
-    _need(w_out, "w_out", torch.float32, kv.device, _weights_shape(kv))
+    _need(w_out, "w_out", torch.float32, kv.device, weights_shape(kv))
     if w_in is None:
         return None
-    _need(w_in, "w_in", torch.float32, kv.device, _weights_shape(kv))
+    _need(w_in, "w_in", torch.float32, kv.device, weights_shape(kv))
     return w_in.data_ptr()
 
 
@@ -471,9 +472,9 @@ def asp_weight_evict(kv: PagedKV, weights: torch.Tensor, keep: int, recent: int,
                      dst_table: torch.Tensor, w_out: torch.Tensor, kept: torch.Tensor,
                      new_lens: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """Keeps the `recent` newest and the heaviest other tokens of every head, `keep` in all."""
-    _need(weights, "weights", torch.float32, kv.device, _weights_shape(kv))
+    _need(weights, "weights", torch.float32, kv.device, weights_shape(kv))
     _need(dst_table, "dst_table", torch.int32, kv.device, (kv.batch, kv.max_pages))
-    _need(w_out, "w_out", torch.float32, kv.device, _weights_shape(kv))
+    _need(w_out, "w_out", torch.float32, kv.device, weights_shape(kv))
     _need(kept, "kept", torch.int32, kv.device, (kv.batch, kv.num_kv_heads, int(keep)))
     _need(new_lens, "new_lens", torch.int32, kv.device, (kv.batch,))
     _need(ws, "ws", torch.uint8, kv.device)

@@ -1,4 +1,4 @@
-"""One decode step over L layers, optionally captured into a single CUDA graph.
+"""One decode step, or one chunk of new tokens, over L layers, optionally captured into a CUDA graph.
 
 Per layer: asp_coverage_select (one cluster kernel, or score + select kernels) then asp_sparse_decode
 (self-planning attention), and optionally asp_page_summarize in APPEND mode
@@ -24,11 +24,15 @@ def _check_shape(name, t, shape):
 
 class DecodeStep:
     def __init__(self, kvs, q, gamma: float, budget: int = 0, sm_scale: float | None = None,
-                 append=None):
+                 append=None, weights=None, decay: float = 1.0):
         """kvs: list of PagedKV (one per layer, same shape); q: fp32 [L, B, Hq, d].
 
         append: optional (k_new, v_new), bf16 [L, B, Hkv, d] each, written with
         APPEND before each layer's selection.
+        weights: optional fp32 [L, B, Hkv, max_pages * P], the attention weight every
+        cached token has received so far: after each layer's attention it becomes
+        decay * weights + what this step gave (asp_decode_weights, in place; a
+        replay adds again).
         """
         self.kvs = list(kvs)
         if not self.kvs:
@@ -45,6 +49,9 @@ class DecodeStep:
         self.gamma, self.budget = float(gamma), int(budget)
         self.sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(kv0.head_dim)
         self.append = append
+        if weights is not None:
+            _check_shape("weights", weights, (L,) + tuple(B.weights_shape(kv0)))
+        self.weights, self.decay = weights, float(decay)
         self.lists = torch.zeros((L, kv0.batch, kv0.num_kv_heads, kv0.max_pages), dtype=torch.int32,
                                  device=dev)
         self.lens = torch.zeros((L, kv0.batch, kv0.num_kv_heads), dtype=torch.int32, device=dev)
@@ -56,11 +63,12 @@ class DecodeStep:
 
     # kernel launches of one step, per layer: the selection's (one cluster
     # kernel, or a score pass and a select kernel; select alone at gamma = 1),
-    # the decode, and the append kernel when enabled
+    # the decode, the append kernel when enabled, and the two of the weights
     @property
     def launches_per_step(self) -> int:
         per, _ = B.asp_select_plan(self.kvs[0], self.gamma, self.budget)
-        return len(self.kvs) * (per + 1 + (1 if self.append is not None else 0))
+        return len(self.kvs) * (per + 1 + (1 if self.append is not None else 0) +
+                                (2 if self.weights is not None else 0))
 
     def run_layer(self, l: int, stream=None, events=None):
         kv = self.kvs[l]
@@ -77,6 +85,10 @@ class DecodeStep:
                             self.out[l], self.lse[l], self.ws, stream)
         if events is not None:
             events[2].record(stream)
+        if self.weights is not None:
+            B.asp_decode_weights(kv, self.q[l], self.lists[l], self.lens[l], self.lse[l],
+                                 self.sm_scale, self.decay, self.weights[l], self.weights[l],
+                                 self.ws, stream)
 
     def run(self, stream=None):
         for l in range(len(self.kvs)):
@@ -186,3 +198,97 @@ class DecodeLoop:
 
     def replay(self):
         self.graph.replay()
+
+
+class ChunkStep:
+    """One chunk of new tokens (whole prompts, parts of them, drafted tokens) over L layers.
+
+    Per layer: the norms, the rotation and the write of the chunk's projected rows into
+    the cache and its summaries (asp_norm_rotate_append), causal attention over the whole
+    cache (asp_chunk_attention) and, on request, the attention weight that every cached
+    token received (asp_chunk_weights), which `evict` goes by. The layers share one
+    workspace; nothing returns to the host, so a step can be captured and replayed with
+    other rows, offsets and lengths in the same buffers. Nothing of it knows those on the
+    host: q_offsets and the caches' seq_lens (which count the new tokens) say what is new.
+    """
+
+    def __init__(self, kvs, qkv, q_offsets, inv_freq=None, q_weight=None, k_weight=None,
+                 positions=None, eps: float = 1e-6, interleaved: bool = False,
+                 sm_scale: float | None = None, weights=None, decay: float = 1.0):
+        """kvs: list of PagedKV (one per layer, same shape); qkv: bf16 [L, N, Hq + 2 Hkv, d];
+        q_offsets: int32 [B + 1]; inv_freq: fp32 [rotary_dim / 2] or None; q_weight, k_weight:
+        bf16 [L, d] or None; positions: int32 [N] or None (the slots); weights: fp32
+        [L, B, Hkv, max_pages * P] or None, becomes decay * weights + what the chunk gave."""
+        self.kvs = list(kvs)
+        if not self.kvs:
+            raise ValueError("kvs must hold at least one layer")
+        kv0 = self.kvs[0]
+        L = len(self.kvs)
+        n = int(qkv.shape[1]) if qkv.dim() == 4 else -1
+        _check_shape("qkv", qkv, (L, n, kv0.num_q_heads + 2 * kv0.num_kv_heads, kv0.head_dim))
+        _check_shape("q_offsets", q_offsets, (kv0.batch + 1,))
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None:
+                _check_shape(name, w, (L, kv0.head_dim))
+        if weights is not None:
+            _check_shape("weights", weights, (L,) + tuple(B.weights_shape(kv0)))
+        self.qkv, self.q_offsets, self.inv_freq = qkv, q_offsets, inv_freq
+        self.q_weight, self.k_weight, self.positions = q_weight, k_weight, positions
+        self.eps, self.interleaved = float(eps), bool(interleaved)
+        self.sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(kv0.head_dim)
+        self.weights, self.decay = weights, float(decay)
+        shape = (L, n, kv0.num_q_heads, kv0.head_dim)
+        self.q = torch.zeros(shape, dtype=torch.bfloat16, device=kv0.device)
+        self.out = torch.zeros(shape, dtype=torch.bfloat16, device=kv0.device)
+        self.lse = torch.zeros(shape[:3], dtype=torch.float32, device=kv0.device)
+        self.ws = B.new_workspace(kv0)
+        self.graph = None
+
+    def run_layer(self, l: int, stream=None):
+        kv = self.kvs[l]
+        B.asp_norm_rotate_append(kv, self.qkv[l], self.q_offsets, self.positions,
+                                 None if self.q_weight is None else self.q_weight[l],
+                                 None if self.k_weight is None else self.k_weight[l], self.eps,
+                                 self.inv_freq, self.interleaved, self.q[l], self.ws, stream)
+        B.asp_chunk_attention(kv, self.q[l], self.q_offsets, self.sm_scale, self.out[l],
+                              self.lse[l], self.ws, stream)
+        if self.weights is not None:
+            B.asp_chunk_weights(kv, self.q[l], self.q_offsets, self.lse[l], self.sm_scale,
+                                self.decay, self.weights[l], self.weights[l], self.ws, stream)
+
+    def run(self, stream=None):
+        for l in range(len(self.kvs)):
+            self.run_layer(l, stream)
+
+    def capture(self):
+        """Captures the step into a CUDA graph (call `run` once before: it loads the kernels)."""
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            self.run()
+        self.graph = g
+        return g
+
+    def replay(self):
+        self.graph.replay()
+
+
+def evict(kvs, weights, keep: int, recent: int, ws, dst_table=None, stream=None):
+    """Cuts every layer's cache back to `keep` tokens a request (asp_weight_evict).
+
+    weights: fp32 [L, B, Hkv, max_pages * P], moved along in place; dst_table: int32
+    [B, max_pages] of pages that the caches' table does not use, or None: in place. Returns
+    (kept int32 [L, B, Hkv, keep], new_lens int32 [B]): the caller then goes on with
+    new_lens as seq_lens and, where one was given, dst_table as the block table."""
+    kvs = list(kvs)
+    if not kvs:
+        raise ValueError("kvs must hold at least one layer")
+    kv0 = kvs[0]
+    _check_shape("weights", weights, (len(kvs),) + tuple(B.weights_shape(kv0)))
+    kept = torch.full((len(kvs), kv0.batch, kv0.num_kv_heads, int(keep)), -1, dtype=torch.int32,
+                      device=kv0.device)
+    new_lens = torch.zeros(kv0.batch, dtype=torch.int32, device=kv0.device)
+    for l, kv in enumerate(kvs):
+        B.asp_weight_evict(kv, weights[l], keep, recent,
+                           kv.block_table if dst_table is None else dst_table, weights[l], kept[l],
+                           new_lens, ws, stream)
+    return kept, new_lens
