@@ -265,6 +265,11 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const Params p
       if (q * 32 + lane < kWarpRows && i < n) {
         src[q] = row_of(from, kept[i]);
         dst[q] = row_of(to, i);
+        // a copy of the source table: in place without its order, which is not done
+        if (!in_order && dst[q] >= 0 && to[i / P] == from[i / P]) {
+          report(p.err, ASP_DEVERR_PAGE_RANGE);
+          dst[q] = -1;
+        }
       }
     }
   };
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const Params p
         d = r < 32 ? d0 : d1;
       }
       to_row[u] = s >= 0 ? d : -1;
-      if (s >= 0) {
+      if (s >= 0 && d >= 0) {
         have |= 1u << u;
         x[u] = __ldcg(reinterpret_cast<const uint2*>(cache + (size_t)s * D));
       }
@@ -298,7 +303,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const Params p
     for (int u = 0; u < kGroup; ++u)
       if (to_row[u] >= 0) *reinterpret_cast<uint2*>(cache + (size_t)to_row[u] * D) = x[u];
     if (!is_k) continue;
-    uint2 mn = make_uint2(0x7f807f80u, 0x7f807f80u), mx = make_uint2(0xff80ff80u, 0xff80ff80u);
+    const uint2 inf = make_uint2(0x7f807f80u, 0x7f807f80u);  // folding starts from +-infinity
+    const uint2 neg_inf = make_uint2(0xff80ff80u, 0xff80ff80u);
+    uint2 mn = inf, mx = neg_inf;
 #pragma unroll
     for (int u = 0; u < kGroup; ++u)
       if (have >> u & 1) {
@@ -320,7 +327,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const Params p
       }
       __syncthreads();
     }
-    if (first % P == 0 && first < n) {
+    const bool none = mn.x == inf.x && mn.y == inf.y && mx.x == neg_inf.x && mx.y == neg_inf.y;
+    if (first % P == 0 && first < n && !none) {  // none: no row of the page was moved
       uint16_t* s = p.summ + ((size_t)seg * p.max_pages + first / P) * 2 * D + c0;
       *reinterpret_cast<uint2*>(s) = mn;
       *reinterpret_cast<uint2*>(s + D) = mx;

@@ -119,11 +119,12 @@ int32_t asp_abi_version(void);
 const char* asp_status_string(asp_status status);
 
 /*
- * Workspace bytes needed by asp_coverage_select / asp_sparse_decode /
- * asp_page_summarize for this shape on the CURRENT device (the decode grid
- * is sized from its SM count). Writes the size to *bytes. The workspace is a
- * caller-owned device buffer, 256-byte aligned, that must be zeroed once with
- * asp_workspace_init before first use. It holds the device error word,
+ * Workspace bytes needed by every call below that takes one, for this shape on
+ * the CURRENT device (the grids are sized from its SM count; the partial results
+ * of asp_chunk_attention are most of it, 41 MB on 152 SMs at head_dim 128).
+ * Writes the size to *bytes. The workspace is a caller-owned device buffer,
+ * 256-byte aligned, that must be zeroed once with asp_workspace_init before
+ * first use. It holds the device error word,
  * per-call scratch (page scores, the decode's partial results) that every
  * call rewrites before reading, and one arrival count per segment that the
  * decode leaves at zero when it ends, so graph replay is safe. Calls that
@@ -393,7 +394,8 @@ asp_status asp_decode_weights(const asp_paged_kv* kv, const float* q, const int3
  * kept      : int32 [B, Hkv, keep] out; entries from n on are untouched.
  * new_lens  : int32 [B] out; not the seq_lens buffer.
  * An out-of-range entry of either table sets ASP_DEVERR_PAGE_RANGE; the rows it
- * holds are not moved.
+ * holds are not moved. In place is asked for by the pointer: another buffer with
+ * block_table's own pages in their places sets the same bit and moves nothing.
  */
 asp_status asp_weight_evict(const asp_paged_kv* kv, const float* weights, int32_t keep,
                             int32_t recent, const int32_t* dst_table, float* w_out, int32_t* kept,

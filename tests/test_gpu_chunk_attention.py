@@ -173,6 +173,54 @@ def test_many_requests(cuda_device):
     check(batch, out, lse)
 
 
+def test_more_requests_than_threads(cuda_device):
+    """Every thread of the plan holds several requests; most have a row or none."""
+    tokens = [1 + (i * 37) % 40 for i in range(1500)]
+    news = [min(t, (i * 5) % 3) for i, t in enumerate(tokens)]
+    batch = R.Batch(cuda_device, tokens, news, 2, 1, 64, 16, seed=15)
+    batch.to_device()
+    out, lse = call(batch)
+    assert B.asp_get_device_error(batch.ws) == 0
+    check(batch, out, lse)
+
+
+def test_rows_of_no_request_may_hold_anything(cuda_device):
+    """The tiles of rows reach past a request's last row: what lies there does not come in."""
+    batch = R.Batch(cuda_device, [90, 61], [37, 5], 8, 2, 64, 16, seed=16, lead=4, tail=9)
+    batch.q[:4] = math.nan
+    batch.q[-9:] = math.inf
+    batch.to_device()
+    out, lse = call(batch)
+    check(batch, out, lse)
+
+
+def test_lengths_and_offsets_that_change_between_replays(cuda_device):
+    """A captured call follows the device's lengths and offsets, from many rows to none."""
+    batch = R.Batch(cuda_device, [900, 300], [200, 100], 8, 2, 64, 16, seed=17)
+    batch.to_device()
+    q = batch.q.to(cuda_device)
+    out = guards.guarded((batch.N, 8, 64), torch.bfloat16, cuda_device, fill=7.0)
+    lse = guards.guarded((batch.N, 8), torch.float32, cuda_device, fill=7.0)
+    args = (batch.kv, q, batch.offs_dev, batch.scale, out, lse, batch.ws)
+    B.asp_chunk_attention(*args)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.asp_chunk_attention(*args)
+    for tokens, news in (([900, 300], [200, 100]), ([512, 17], [1, 17]), ([900, 0], [300, 0]),
+                         ([5, 300], [0, 0]), ([128, 300], [128, 172])):
+        batch.tokens, batch.news = tokens, news
+        batch.offs = [0, news[0], news[0] + news[1]]
+        batch.lens_dev.copy_(torch.tensor(tokens, dtype=torch.int32))
+        batch.offs_dev.copy_(torch.tensor(batch.offs, dtype=torch.int32))
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert B.asp_get_device_error(batch.ws) == 0
+        check(batch, out, lse)
+
+
 def test_another_stream_and_graphs_that_share_a_workspace(cuda_device):
     """Two graphs over one workspace, replayed in turn on a stream of their own."""
     a = R.Batch(cuda_device, [3000], [5], 8, 2, 128, 16, seed=13)

@@ -136,6 +136,20 @@ def test_bad_pages(cuda_device):
     assert kept[0, 0].tolist() == list(range(100, 200))
 
 
+def test_a_copy_of_the_table_is_refused(cuda_device):
+    """In place is asked for by the table itself: a copy of it would be moved out of order."""
+    batch = R.Batch(cuda_device, [200], [0], 2, 2, 64, 16, seed=9)
+    kv = batch.to_device()
+    w = torch.rand((1, 2, batch.max_pages * 16), device=cuda_device)
+    kept = torch.zeros((1, 2, 100), dtype=torch.int32, device=cuda_device)
+    lens = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    batch.summ_dev.fill_(3.0)
+    B.asp_weight_evict(kv, w, 100, 10, batch.table_dev.clone(), w, kept, lens, batch.ws)
+    assert B.asp_get_device_error(batch.ws) == B.ASP_DEVERR_PAGE_RANGE
+    assert same(batch.k_dev.cpu(), batch.k) and same(batch.v_dev.cpu(), batch.v)
+    assert bool((batch.summ_dev == 3.0).all())
+
+
 def test_graph_replay(cuda_device):
     """Into other pages the call can be repeated: a graph of it, replayed, leaves the same."""
     batch = R.Batch(cuda_device, [500, 300], [0, 0], 2, 2, 64, 16, seed=7, max_pages=64)

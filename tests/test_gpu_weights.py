@@ -102,6 +102,35 @@ def test_chunk_no_rows_bad_pages_and_masked_rows(cuda_device):
     assert torch.equal(w[..., :50].cpu(), 0.5 * w_in[..., :50])
 
 
+def test_chunk_rows_of_no_request_may_hold_anything(cuda_device):
+    batch = R.Batch(cuda_device, [90, 300], [37, 5], 8, 2, 64, 16, seed=7, lead=4, tail=9)
+    lse = lse_of(batch, batch.q)
+    lse[:4], lse[-9:] = math.nan, math.inf
+    want, tol = R.chunk_weights(batch, batch.q, lse, 1.0, None)
+    batch.q[:4], batch.q[-9:] = math.nan, math.inf
+    kv = batch.to_device()
+    w = guards.guarded((2, 2, batch.max_pages * 16), torch.float32, cuda_device, fill=FILL)
+    B.asp_chunk_weights(kv, batch.q.to(cuda_device), batch.offs_dev, lse.to(cuda_device),
+                        batch.scale, 1.0, None, w, batch.ws)
+    assert B.asp_get_device_error(batch.ws) == 0
+    check(batch, w, want, tol)
+
+
+def test_chunk_more_requests_than_threads(cuda_device):
+    tokens = [1 + (i * 37) % 40 for i in range(1200)]
+    news = [min(t, (i * 5) % 3) for i, t in enumerate(tokens)]
+    batch = R.Batch(cuda_device, tokens, news, 2, 1, 64, 16, seed=8)
+    kv = batch.to_device()
+    lse = lse_of(batch, batch.q).nan_to_num(0.0)
+    start = torch.rand((batch.B, 1, batch.max_pages * 16), generator=batch.gen)
+    want, tol = R.chunk_weights(batch, batch.q, lse, 0.5, start)
+    w = guards.guarded(start.shape, torch.float32, cuda_device, fill=FILL)
+    B.asp_chunk_weights(kv, batch.q.to(cuda_device), batch.offs_dev, lse.to(cuda_device),
+                        batch.scale, 0.5, start.to(cuda_device), w, batch.ws)
+    assert B.asp_get_device_error(batch.ws) == 0
+    check(batch, w, want, tol)
+
+
 # ------------------------------------------------------------------ decode form
 def decode_case(dev, tokens, Hq, Hkv, d, P, share, seed):
     news = [min(1, t) for t in tokens]
@@ -199,6 +228,21 @@ def test_decode_after_the_sparse_decode(cuda_device):
     assert B.asp_get_device_error(batch.ws) == 0
     total = w.double().sum(-1).cpu()
     assert bool(((total - 4.0).abs() <= 4 * 2.0 ** -12).all()), total
+
+
+def test_decode_more_segments_than_threads(cuda_device):
+    tokens = [(i * 37) % 60 for i in range(700)]
+    batch, q, lists, lens = decode_case(cuda_device, tokens, 4, 2, 64, 16, 0.5, seed=23)
+    kv = batch.to_device()
+    start = torch.rand((batch.B, 2, batch.max_pages * 16), generator=batch.gen)
+    lse = decode_form(batch, q, lists, lens, None, 0.5, start)[2]
+    want, tol, _ = decode_form(batch, q, lists, lens, lse, 0.5, start)
+    w = guards.guarded(start.shape, torch.float32, cuda_device, fill=FILL)
+    dev = cuda_device
+    B.asp_decode_weights(kv, q.to(dev), lists.to(dev), lens.to(dev), lse.to(dev), batch.scale, 0.5,
+                         start.to(dev), w, batch.ws)
+    assert B.asp_get_device_error(batch.ws) == 0
+    check(batch, w, want, tol)
 
 
 def test_decode_bad_lists_and_pages(cuda_device):
