@@ -10,7 +10,6 @@ any function fails loudly (build it with adaptive_sparse_paged_gb300.build).
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -143,20 +142,25 @@ def _stream_ptr(device: torch.device, stream=None) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-_HERE = contextlib.nullcontext()
-
-
-def _on(device: torch.device):
-    """Makes `device` the current one; entering a device that already is costs more than a check."""
-    if torch.cuda.current_device() == device.index:
-        return _HERE
-    return torch.cuda.device(device)
+def _run(name: str, device: torch.device, *args) -> None:
+    """Calls an entry point with `device` current and raises on its status."""
+    fn = getattr(_lib or load_library(), name)
+    if torch._C._cuda_getDevice() == device.index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status != ASP_OK:
+        raise AspError(status, name)
 
 
 def _need(t: torch.Tensor, name: str, dtype, device, shape=None):
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
-            and (shape is None or t.shape == shape) and t.is_contiguous()):
-        return
+    try:  # what is right is seen first and cheaply; the rest finds out what is not
+        if (t.dtype is dtype and t.get_device() == device.index
+                and (shape is None or t.shape == shape) and t.is_contiguous()):
+            return
+    except (AttributeError, RuntimeError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -224,17 +228,13 @@ def asp_abi_version() -> int:
 
 def asp_workspace_size(kv: PagedKV) -> int:
     out = ctypes.c_size_t(0)
-    with _on(kv.device):
-        _check(load_library().asp_workspace_size(kv.ref, ctypes.byref(out)), "asp_workspace_size")
+    _run("asp_workspace_size", kv.device, kv.ref, ctypes.byref(out))
     return int(out.value)
 
 
 def asp_workspace_init(ws: torch.Tensor, stream=None) -> None:
     _need(ws, "ws", torch.uint8, ws.device)
-    with _on(ws.device):
-        _check(load_library().asp_workspace_init(ws.data_ptr(), ws.numel(),
-                                                 _stream_ptr(ws.device, stream)),
-               "asp_workspace_init")
+    _run("asp_workspace_init", ws.device, ws.data_ptr(), ws.numel(), _stream_ptr(ws.device, stream))
 
 
 def asp_page_summarize(kv: PagedKV, mode: int, k_new, v_new, ws: torch.Tensor, stream=None) -> None:
@@ -246,10 +246,8 @@ def asp_page_summarize(kv: PagedKV, mode: int, k_new, v_new, ws: torch.Tensor, s
     else:
         kp = vp = None
     _need(ws, "ws", torch.uint8, kv.device)
-    with _on(kv.device):
-        _check(load_library().asp_page_summarize(kv.ref, int(mode), kp, vp, ws.data_ptr(),
-                                                 ws.numel(), _stream_ptr(kv.device, stream)),
-               "asp_page_summarize")
+    _run("asp_page_summarize", kv.device, kv.ref, int(mode), kp, vp, ws.data_ptr(), ws.numel(),
+         _stream_ptr(kv.device, stream))
 
 
 def asp_coverage_select(kv: PagedKV, q: torch.Tensor, gamma: float, budget: int,
@@ -259,11 +257,9 @@ def asp_coverage_select(kv: PagedKV, q: torch.Tensor, gamma: float, budget: int,
     _need(lists, "lists", torch.int32, kv.device, (kv.batch, kv.num_kv_heads, kv.max_pages))
     _need(lens, "lens", torch.int32, kv.device, (kv.batch, kv.num_kv_heads))
     _need(ws, "ws", torch.uint8, kv.device)
-    with _on(kv.device):
-        _check(load_library().asp_coverage_select(
-            kv.ref, q.data_ptr(), ctypes.c_float(gamma), int(budget), lists.data_ptr(),
-            lens.data_ptr(), ws.data_ptr(), ws.numel(), _stream_ptr(kv.device, stream)),
-            "asp_coverage_select")
+    _run("asp_coverage_select", kv.device, kv.ref, q.data_ptr(), float(gamma), int(budget),
+         lists.data_ptr(), lens.data_ptr(), ws.data_ptr(), ws.numel(), _stream_ptr(kv.device,
+         stream))
 
 
 def asp_coverage_select_append(kv: PagedKV, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -277,20 +273,16 @@ def asp_coverage_select_append(kv: PagedKV, k_new: torch.Tensor, v_new: torch.Te
     _need(lists, "lists", torch.int32, kv.device, (kv.batch, kv.num_kv_heads, kv.max_pages))
     _need(lens, "lens", torch.int32, kv.device, (kv.batch, kv.num_kv_heads))
     _need(ws, "ws", torch.uint8, kv.device)
-    with _on(kv.device):
-        _check(load_library().asp_coverage_select_append(
-            kv.ref, k_new.data_ptr(), v_new.data_ptr(), q.data_ptr(), ctypes.c_float(gamma),
-            int(budget), lists.data_ptr(), lens.data_ptr(), ws.data_ptr(), ws.numel(),
-            _stream_ptr(kv.device, stream)), "asp_coverage_select_append")
+    _run("asp_coverage_select_append", kv.device, kv.ref, k_new.data_ptr(), v_new.data_ptr(),
+         q.data_ptr(), float(gamma), int(budget), lists.data_ptr(), lens.data_ptr(), ws.data_ptr(),
+         ws.numel(), _stream_ptr(kv.device, stream))
 
 
 def asp_select_plan(kv: PagedKV, gamma: float, budget: int = 0, append: bool = False):
     """(kernels one selection call launches, cluster CTAs per segment or 0)."""
     k, c = ctypes.c_int32(0), ctypes.c_int32(0)
-    with _on(kv.device):
-        _check(load_library().asp_select_plan(kv.ref, ctypes.c_float(gamma), int(budget),
-                                              int(bool(append)), ctypes.byref(k),
-                                              ctypes.byref(c)), "asp_select_plan")
+    _run("asp_select_plan", kv.device, kv.ref, float(gamma), int(budget), int(bool(append)),
+         ctypes.byref(k), ctypes.byref(c))
     return int(k.value), int(c.value)
 
 
@@ -301,11 +293,8 @@ def asp_page_scores(kv: PagedKV, q: torch.Tensor, scores: torch.Tensor, ws: torc
     _need(scores, "scores", torch.float32, kv.device,
           (kv.batch, kv.num_kv_heads, kv.max_pages))
     _need(ws, "ws", torch.uint8, kv.device)
-    with _on(kv.device):
-        _check(load_library().asp_page_scores(kv.ref, q.data_ptr(), scores.data_ptr(),
-                                              ws.data_ptr(), ws.numel(),
-                                              _stream_ptr(kv.device, stream)),
-               "asp_page_scores")
+    _run("asp_page_scores", kv.device, kv.ref, q.data_ptr(), scores.data_ptr(), ws.data_ptr(),
+         ws.numel(), _stream_ptr(kv.device, stream))
 
 
 def asp_sparse_decode(kv: PagedKV, q: torch.Tensor, lists: torch.Tensor, lens: torch.Tensor,
@@ -317,11 +306,9 @@ def asp_sparse_decode(kv: PagedKV, q: torch.Tensor, lists: torch.Tensor, lens: t
     _need(out, "out", torch.float32, kv.device, (kv.batch, kv.num_q_heads, kv.head_dim))
     _need(lse, "lse", torch.float32, kv.device, (kv.batch, kv.num_q_heads))
     _need(ws, "ws", torch.uint8, kv.device)
-    with _on(kv.device):
-        _check(load_library().asp_sparse_decode(
-            kv.ref, q.data_ptr(), lists.data_ptr(), lens.data_ptr(), ctypes.c_float(sm_scale),
-            out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(),
-            _stream_ptr(kv.device, stream)), "asp_sparse_decode")
+    _run("asp_sparse_decode", kv.device, kv.ref, q.data_ptr(), lists.data_ptr(), lens.data_ptr(),
+         float(sm_scale), out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(),
+         _stream_ptr(kv.device, stream))
 
 
 def asp_coverage_select_noalloc(kv: PagedKV, q: torch.Tensor, gamma: float, budget: int,
@@ -340,11 +327,8 @@ def asp_coverage_select_noalloc(kv: PagedKV, q: torch.Tensor, gamma: float, budg
     if dev_error is not None:
         _need(dev_error, "dev_error", torch.int32, kv.device, (1,))
         err_ptr = dev_error.data_ptr()
-    with _on(kv.device):
-        _check(load_library().asp_coverage_select_noalloc(
-            kv.ref, q.data_ptr(), ctypes.c_float(gamma), int(budget), lists.data_ptr(),
-            lens.data_ptr(), err_ptr, _stream_ptr(kv.device, stream)),
-            "asp_coverage_select_noalloc")
+    _run("asp_coverage_select_noalloc", kv.device, kv.ref, q.data_ptr(), float(gamma), int(budget),
+         lists.data_ptr(), lens.data_ptr(), err_ptr, _stream_ptr(kv.device, stream))
 
 
 def weights_shape(kv: PagedKV):
@@ -361,8 +345,9 @@ def _need_rows(kv: PagedKV, t: torch.Tensor, name: str, heads: int) -> int:
     """Packed bf16 rows [num_tokens, heads, d]; returns num_tokens."""
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError(f"{name} must be a tensor [num_tokens, {heads}, {kv.head_dim}]")
-    _need(t, name, torch.bfloat16, kv.device, (t.shape[0], heads, kv.head_dim))
-    return int(t.shape[0])
+    n = t.size(0)
+    _need(t, name, torch.bfloat16, kv.device, (n, heads, kv.head_dim))
+    return n
 
 
 def _need_weights(kv: PagedKV, w_in, w_out) -> int | None:
@@ -382,38 +367,39 @@ def asp_norm_rotate_append(kv: PagedKV, qkv: torch.Tensor, q_offsets, positions,
     [N] or None (the slots); q_weight, k_weight: bf16 [d] or None (not normed);
     inv_freq: fp32 [rotary_dim / 2] or None (no rotation); q_out: bf16 or fp32
     [N, Hq, d], the normed and rotated queries."""
+    dev = kv.device
     n = _need_rows(kv, qkv, "qkv", kv.num_q_heads + 2 * kv.num_kv_heads)
+    offs_ptr = pos_ptr = qw_ptr = kw_ptr = freq_ptr = None
+    rotary_dim = 0
     if q_offsets is not None:
-        _need(q_offsets, "q_offsets", torch.int32, kv.device, (kv.batch + 1,))
+        _need(q_offsets, "q_offsets", torch.int32, dev, (kv.batch + 1,))
+        offs_ptr = q_offsets.data_ptr()
     if positions is not None:
-        _need(positions, "positions", torch.int32, kv.device, (n,))
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need(w, name, torch.bfloat16, kv.device, (kv.head_dim,))
+        _need(positions, "positions", torch.int32, dev, (n,))
+        pos_ptr = positions.data_ptr() or None
+    if q_weight is not None:
+        _need(q_weight, "q_weight", torch.bfloat16, dev, (kv.head_dim,))
+        qw_ptr = q_weight.data_ptr()
+    if k_weight is not None:
+        _need(k_weight, "k_weight", torch.bfloat16, dev, (kv.head_dim,))
+        kw_ptr = k_weight.data_ptr()
     if inv_freq is not None:
-        _need(inv_freq, "inv_freq", torch.float32, kv.device, (inv_freq.numel(),))
-    if not isinstance(q_out, torch.Tensor) or q_out.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError("q_out must be a torch.bfloat16 or torch.float32 tensor")
-    _need(q_out, "q_out", q_out.dtype, kv.device, (n, kv.num_q_heads, kv.head_dim))
-    _need(ws, "ws", torch.uint8, kv.device)
-
-    def ptr(t):
-        return None if t is None else t.data_ptr()
-
-    half = q_out.dtype == torch.bfloat16
-    with _on(kv.device):
-        _check(load_library().asp_norm_rotate_append(
-            kv.ref, _rows_ptr(qkv), ptr(q_offsets), n, ptr(positions), ptr(q_weight),
-            ptr(k_weight), ctypes.c_float(eps), ptr(inv_freq),
-            0 if inv_freq is None else 2 * inv_freq.numel(), int(bool(interleaved)),
-            _rows_ptr(q_out) if half else None, None if half else _rows_ptr(q_out), ws.data_ptr(),
-            ws.numel(), _stream_ptr(kv.device, stream)), "asp_norm_rotate_append")
+        _need(inv_freq, "inv_freq", torch.float32, dev)
+        freq_ptr, rotary_dim = inv_freq.data_ptr(), 2 * inv_freq.numel()
+    half = getattr(q_out, "dtype", None) is torch.bfloat16
+    _need(q_out, "q_out", torch.bfloat16 if half else torch.float32, dev,
+          (n, kv.num_q_heads, kv.head_dim))
+    _need(ws, "ws", torch.uint8, dev)
+    out_ptr = _rows_ptr(q_out)
+    _run("asp_norm_rotate_append", dev, kv.ref, _rows_ptr(qkv), offs_ptr, n, pos_ptr, qw_ptr, kw_ptr,
+         float(eps), freq_ptr, rotary_dim, int(bool(interleaved)), out_ptr if half else None,
+         None if half else out_ptr, ws.data_ptr(), ws.numel(), _stream_ptr(dev, stream))
 
 
 def _rows_ptr(t: torch.Tensor) -> int:
     """data_ptr of packed rows; a tensor without rows has none, and the library
     wants an aligned non-null one that it never reads."""
-    return t.data_ptr() if t.numel() else 256
+    return t.data_ptr() or 256
 
 
 def asp_chunk_attention(kv: PagedKV, q: torch.Tensor, q_offsets: torch.Tensor, sm_scale: float,
@@ -425,11 +411,9 @@ def asp_chunk_attention(kv: PagedKV, q: torch.Tensor, q_offsets: torch.Tensor, s
     _need(out, "out", torch.bfloat16, kv.device, (n, kv.num_q_heads, kv.head_dim))
     _need(lse, "lse", torch.float32, kv.device, (n, kv.num_q_heads))
     _need(ws, "ws", torch.uint8, kv.device)
-    with _on(kv.device):
-        _check(load_library().asp_chunk_attention(
-            kv.ref, _rows_ptr(q), q_offsets.data_ptr(), n, ctypes.c_float(sm_scale),
-            _rows_ptr(out), _rows_ptr(lse), ws.data_ptr(), ws.numel(),
-            _stream_ptr(kv.device, stream)), "asp_chunk_attention")
+    _run("asp_chunk_attention", kv.device, kv.ref, _rows_ptr(q), q_offsets.data_ptr(), n,
+         float(sm_scale), _rows_ptr(out), _rows_ptr(lse), ws.data_ptr(), ws.numel(),
+         _stream_ptr(kv.device, stream))
 
 
 def asp_chunk_weights(kv: PagedKV, q: torch.Tensor, q_offsets: torch.Tensor, lse: torch.Tensor,
@@ -441,11 +425,9 @@ def asp_chunk_weights(kv: PagedKV, q: torch.Tensor, q_offsets: torch.Tensor, lse
     _need(lse, "lse", torch.float32, kv.device, (n, kv.num_q_heads))
     w_ptr = _need_weights(kv, w_in, w_out)
     _need(ws, "ws", torch.uint8, kv.device)
-    with _on(kv.device):
-        _check(load_library().asp_chunk_weights(
-            kv.ref, _rows_ptr(q), q_offsets.data_ptr(), n, _rows_ptr(lse),
-            ctypes.c_float(sm_scale), ctypes.c_float(decay), w_ptr, w_out.data_ptr(),
-            ws.data_ptr(), ws.numel(), _stream_ptr(kv.device, stream)), "asp_chunk_weights")
+    _run("asp_chunk_weights", kv.device, kv.ref, _rows_ptr(q), q_offsets.data_ptr(), n,
+         _rows_ptr(lse), float(sm_scale), float(decay), w_ptr, w_out.data_ptr(), ws.data_ptr(),
+         ws.numel(), _stream_ptr(kv.device, stream))
 
 
 def asp_decode_weights(kv: PagedKV, q: torch.Tensor, lists, lens, lse: torch.Tensor,
@@ -461,11 +443,9 @@ def asp_decode_weights(kv: PagedKV, q: torch.Tensor, lists, lens, lse: torch.Ten
     _need(lse, "lse", torch.float32, kv.device, (kv.batch, kv.num_q_heads))
     w_ptr = _need_weights(kv, w_in, w_out)
     _need(ws, "ws", torch.uint8, kv.device)
-    with _on(kv.device):
-        _check(load_library().asp_decode_weights(
-            kv.ref, q.data_ptr(), lists_ptr, lens_ptr, lse.data_ptr(), ctypes.c_float(sm_scale),
-            ctypes.c_float(decay), w_ptr, w_out.data_ptr(), ws.data_ptr(), ws.numel(),
-            _stream_ptr(kv.device, stream)), "asp_decode_weights")
+    _run("asp_decode_weights", kv.device, kv.ref, q.data_ptr(), lists_ptr, lens_ptr, lse.data_ptr(),
+         float(sm_scale), float(decay), w_ptr, w_out.data_ptr(), ws.data_ptr(), ws.numel(),
+         _stream_ptr(kv.device, stream))
 
 
 def asp_weight_evict(kv: PagedKV, weights: torch.Tensor, keep: int, recent: int,
@@ -478,11 +458,9 @@ def asp_weight_evict(kv: PagedKV, weights: torch.Tensor, keep: int, recent: int,
     _need(kept, "kept", torch.int32, kv.device, (kv.batch, kv.num_kv_heads, int(keep)))
     _need(new_lens, "new_lens", torch.int32, kv.device, (kv.batch,))
     _need(ws, "ws", torch.uint8, kv.device)
-    with _on(kv.device):
-        _check(load_library().asp_weight_evict(
-            kv.ref, weights.data_ptr(), int(keep), int(recent), dst_table.data_ptr(),
-            w_out.data_ptr(), kept.data_ptr(), new_lens.data_ptr(), ws.data_ptr(), ws.numel(),
-            _stream_ptr(kv.device, stream)), "asp_weight_evict")
+    _run("asp_weight_evict", kv.device, kv.ref, weights.data_ptr(), int(keep), int(recent),
+         dst_table.data_ptr(), w_out.data_ptr(), kept.data_ptr(), new_lens.data_ptr(),
+         ws.data_ptr(), ws.numel(), _stream_ptr(kv.device, stream))
 
 
 def asp_selftest_wait_timeout(ws: torch.Tensor, stream=None) -> None:
@@ -490,16 +468,14 @@ def asp_selftest_wait_timeout(ws: torch.Tensor, stream=None) -> None:
     and sets ASP_DEVERR_TIMEOUT in `ws`'s error word (read it with
     asp_get_device_error)."""
     _need(ws, "ws", torch.uint8, ws.device)
-    with _on(ws.device):
-        _check(load_library().asp_selftest_wait_timeout(ws.data_ptr(), ws.numel(),
-                                                        _stream_ptr(ws.device, stream)),
-               "asp_selftest_wait_timeout")
+    _run("asp_selftest_wait_timeout", ws.device, ws.data_ptr(), ws.numel(),
+         _stream_ptr(ws.device, stream))
 
 
 def asp_get_device_error(ws: torch.Tensor, stream=None) -> int:
     """Synchronises the stream and returns (and clears) the device error mask."""
     code = ctypes.c_uint32(0)
-    with _on(ws.device):
+    with torch.cuda.device(ws.device):
         st = load_library().asp_get_device_error(ws.data_ptr(), ctypes.byref(code),
                                                  _stream_ptr(ws.device, stream))
     if st not in (ASP_OK, ASP_EDEVICE):
