@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait_predecessor();
   const uint32_t tmem = sh.tmem;
   chunk_plan<RowCut>(p.c, &sh.start, sh.scratch, p.err);
-  const int g = p.c.g, tile_tokens = kTileRows / g;
+  const int g = p.c.g, tile_tokens = kTileRows >> p.c.lg;
   ChunkReader reader(sh.tasks);
   ChunkTask task;  // x: units of its two tiles of rows, its first token, its end
 
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = p.scale_log2;
     uint32_t phase_s = 0, phase_o = 0, units_seen = 0;
     bool ok = true;
-    const int row_tok = row / g, row_head = row % g;
+    const int row_tok = row >> p.c.lg, row_head = row & (g - 1);
     while (ok && reader.next(task)) {
       const int n = t == 0 ? task.x[0] : task.x[1];
       const int tok = task.x[2] + t * tile_tokens + row_tok;
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const Params p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = p.c.g, row = blockIdx.y * 32 + lane;
   const ChunkRequest r = chunk_request(p.c, jn.b, nullptr);
-  const int tok0 = jn.item * (kChunkRows / g);
+  const int tok0 = jn.item * (kChunkRows >> p.c.lg);
   const size_t slot_floats = chunk_slot_floats(D);
   const float* first = p.partials + (size_t)(2 * blockIdx.x + 1) * slot_floats + row;
   const float* rest = p.partials + (size_t)(2 * blockIdx.x) * slot_floats + row;
@@ -576,15 +576,15 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const Params p) {
   for (int i = 0; i < kCols; ++i)
     *reinterpret_cast<uint2*>(tile + lane * kPitch + 4 * (warp * kCols + i)) =
         make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
-  if (warp == 0 && tok0 + row / g < r.n)
-    p.lse[(size_t)(r.row0 + tok0 + row / g) * p.Hq + jn.h * g + row % g] =
+  if (warp == 0 && tok0 + (row >> p.c.lg) < r.n)
+    p.lse[(size_t)(r.row0 + tok0 + (row >> p.c.lg)) * p.Hq + jn.h * g + (row & (g - 1))] =
         L == 0.f ? -INFINITY : M * 0.69314718055994530942f + logf(L);
   __syncthreads();
   constexpr int kPieces = D / 8;  // of 16 bytes
   for (int i = threadIdx.x; i < 32 * kPieces; i += 256) {
     const int rr = blockIdx.y * 32 + i / kPieces;
-    if (tok0 + rr / g >= r.n) break;
-    const size_t at = (size_t)(r.row0 + tok0 + rr / g) * p.Hq + jn.h * g + rr % g;
+    if (tok0 + (rr >> p.c.lg) >= r.n) break;
+    const size_t at = (size_t)(r.row0 + tok0 + (rr >> p.c.lg)) * p.Hq + jn.h * g + (rr & (g - 1));
     *reinterpret_cast<uint4*>(p.out + at * D + 8 * (i % kPieces)) =
         *reinterpret_cast<const uint4*>(tile + i / kPieces * kPitch + 8 * (i % kPieces));
   }
@@ -606,7 +606,7 @@ cudaError_t launch_t(const ChunkAttentionArgs& a, cudaStream_t stream) {
   if ((e = encode_bf16_3d_swizzled(&tv, kv.v_cache, {64, rows, D / 64}, {2 * D, 128},
                                    {64, (unsigned)P, (unsigned)(D / 64)})) != cudaSuccess)
     return e;
-  Params p{{a.q_offsets, kv.seq_lens, kv.batch, kv.num_kv_heads, g, kv.max_pages, P, a.num_tokens,
+  Params p{{a.q_offsets, kv.seq_lens, kv.batch, kv.num_kv_heads, g, chunk_log2(g), kv.max_pages, P, a.num_tokens,
             chunk_inverse(a.num_sms)},
            kv.block_table, a.out, a.lse, a.joins, a.partials, a.err, kv.num_q_heads,
            kv.num_phys_pages, a.sm_scale, a.sm_scale * 1.4426950408889634f};

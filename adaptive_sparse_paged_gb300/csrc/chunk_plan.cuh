@@ -16,13 +16,15 @@
 namespace asp {
 
 constexpr int kTileKeys = 128;
-constexpr int kTileRows = 128;
+constexpr int kTileRows = 128, kLogTileRows = 7;
+constexpr int kLogChunkRows = 8;
+static_assert(1 << kLogTileRows == kTileRows && 1 << kLogChunkRows == kChunkRows);
 constexpr int kItemKeys = 2 * kTileKeys;
 
 struct ChunkDims {
   const int32_t* q_offsets;
   const int32_t* seq_lens;
-  int B, Hkv, g, max_pages, P, num_tokens;
+  int B, Hkv, g, lg, max_pages, P, num_tokens;  // lg: log2(g)
   unsigned long long inv_ctas;  // chunk_inverse of the grid
 };
 
@@ -36,31 +38,34 @@ __device__ __forceinline__ ChunkRequest chunk_request(const ChunkDims& c, int b,
   return ChunkRequest{T, r.n, r.row0};
 }
 
+// lg: log2 of the group. The plan divides by shifts: it stands before all other work of a
+// call, and a division by a value that is not known when the code is compiled is some forty
+// dependent instructions.
 struct RowCut {
   // Units of rows whose last token is `last` (counted in the chunk).
   static __device__ __forceinline__ int units_to(const ChunkRequest& r, int last) {
     return (r.T - r.n + last) / kTileKeys + 1;
   }
-  static __device__ __forceinline__ int items(const ChunkRequest& r, int g) {
-    return ceil_div(r.n, kChunkRows / g);
+  static __device__ __forceinline__ int items(const ChunkRequest& r, int lg) {
+    return (r.n + (kChunkRows >> lg) - 1) >> (kLogChunkRows - lg);
   }
-  static __device__ __forceinline__ int units(const ChunkRequest& r, int g, int item) {
-    return units_to(r, min(r.n, (item + 1) * (kChunkRows / g)) - 1);
+  static __device__ __forceinline__ int units(const ChunkRequest& r, int lg, int item) {
+    return units_to(r, min(r.n, (item + 1) * (kChunkRows >> lg)) - 1);
   }
   // Units of a head's first m items.
-  static __device__ __forceinline__ long long before(const ChunkRequest& r, int g, int m) {
-    const int tpi = kChunkRows / g, all = items(r, g);
+  static __device__ __forceinline__ long long before(const ChunkRequest& r, int lg, int m) {
+    const int tpi = kChunkRows >> lg, all = items(r, lg);
     const int whole = m < all ? m : all - 1;  // items that end on their last possible token
     long long sum = 0;
     if (whole > 0) {
       // item i of them has floor((a + tpi (i + 1) - 1) / 128) + 1 units; the floors
       // repeat, plus `step`, every `period` items
-      const int a = r.T - r.n, period = tpi < kTileKeys ? kTileKeys / tpi : 1;
-      const int step = tpi < kTileKeys ? 1 : tpi / kTileKeys;
+      const int a = r.T - r.n, lp = max(0, lg - 1), period = 1 << lp;
+      const int step = max(1, tpi / kTileKeys);
       for (int s = 0; s < period; ++s) {
-        const long long cnt = (whole - s + period - 1) / period;
+        const long long cnt = (whole - s + period - 1) >> lp;
         if (cnt <= 0) break;
-        sum += cnt * ((a + tpi * (s + 1) - 1) / kTileKeys + 1) + step * cnt * (cnt - 1) / 2;
+        sum += cnt * ((a + tpi * (s + 1) - 1) / kTileKeys + 1) + step * (cnt * (cnt - 1) >> 1);
       }
     }
     if (m == all && all > 0) sum += units_to(r, r.n - 1);
@@ -73,25 +78,25 @@ struct KeyCut {
     return ceil_div(r.T, kItemKeys);
   }
   // First tile of rows that sees a key of the item.
-  static __device__ __forceinline__ int first_tile(const ChunkRequest& r, int g, int item) {
-    return max(0, item * kItemKeys - (r.T - r.n)) / (kTileRows / g);
+  static __device__ __forceinline__ int first_tile(const ChunkRequest& r, int lg, int item) {
+    return max(0, item * kItemKeys - (r.T - r.n)) >> (kLogTileRows - lg);
   }
-  static __device__ __forceinline__ int tiles(const ChunkRequest& r, int g) {
-    return ceil_div(r.n, kTileRows / g);
+  static __device__ __forceinline__ int tiles(const ChunkRequest& r, int lg) {
+    return (r.n + (kTileRows >> lg) - 1) >> (kLogTileRows - lg);
   }
   // A request without new rows still has its weights carried over: one empty unit.
-  static __device__ __forceinline__ int units(const ChunkRequest& r, int g, int item) {
-    return r.n == 0 ? 1 : tiles(r, g) - first_tile(r, g, item);
+  static __device__ __forceinline__ int units(const ChunkRequest& r, int lg, int item) {
+    return r.n == 0 ? 1 : tiles(r, lg) - first_tile(r, lg, item);
   }
-  static __device__ __forceinline__ long long before(const ChunkRequest& r, int g, int m) {
+  static __device__ __forceinline__ long long before(const ChunkRequest& r, int lg, int m) {
     if (r.n == 0) return m;
-    const int a = r.T - r.n, nq = tiles(r, g);
-    const int full = min(m, a / kItemKeys + 1);  // items that every tile of rows sees
+    const int a = r.T - r.n, nq = tiles(r, lg), seen = a / kItemKeys + 1;
+    const int full = min(m, seen);   // items that every tile of rows sees
     long long sum = (long long)full * nq;
-    const long long cut = m - full;              // the others: 2 g tiles fewer each time
+    const long long cut = m - full;  // the others: 2 g tiles fewer each time
     if (cut > 0)
-      sum += cut * (nq - (kItemKeys * (a / kItemKeys + 1) - a) / (kTileRows / g)) -
-             kItemKeys / kTileRows * g * (cut * (cut - 1) / 2);
+      sum += cut * (nq - ((kItemKeys * seen - a) >> (kLogTileRows - lg))) -
+             ((long long)(kItemKeys / kTileRows) << lg) * (cut * (cut - 1) >> 1);
     return sum;
   }
 };
@@ -115,12 +120,14 @@ struct ChunkShares {
     return c;
   }
 };
+inline int chunk_log2(int g) { return g == 8 ? 3 : g == 4 ? 2 : g == 2 ? 1 : 0; }
 // 2^64 / G rounded up (G > 1: the devices of this library have 152 SMs).
 inline unsigned long long chunk_inverse(int G) { return ~0ull / (unsigned)G + 1; }
 
 // Where a CTA's share begins: unit `u` of item (b, h, item); and the share.
 struct ChunkStart {
   int b, h, item, u;
+  ChunkRequest r;
   long long first, count;
   ChunkShares shares;
 };
@@ -135,7 +142,7 @@ __device__ __forceinline__ void chunk_plan(const ChunkDims& c, ChunkStart* start
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     const ChunkRequest r = chunk_request(c, b, blockIdx.x == 0 ? err : nullptr);
-    mine += (long long)c.Hkv * Cut::before(r, c.g, Cut::items(r, c.g));
+    mine += (long long)c.Hkv * Cut::before(r, c.lg, Cut::items(r, c.lg));
   }
   long long x = mine;
 #pragma unroll
@@ -158,8 +165,8 @@ __device__ __forceinline__ void chunk_plan(const ChunkDims& c, ChunkStart* start
     long long at = before;
     for (int b = b0; b < b1; ++b) {
       const ChunkRequest r = chunk_request(c, b, nullptr);
-      const int items = Cut::items(r, c.g);
-      const long long head = Cut::before(r, c.g, items);
+      const int items = Cut::items(r, c.lg);
+      const long long head = Cut::before(r, c.lg, items);
       if (first >= at + c.Hkv * head) {
         at += c.Hkv * head;
         continue;
@@ -170,9 +177,9 @@ __device__ __forceinline__ void chunk_plan(const ChunkDims& c, ChunkStart* start
       int lo = 0, hi = items - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (Cut::before(r, c.g, mid) <= in_h) lo = mid; else hi = mid - 1;
+        if (Cut::before(r, c.lg, mid) <= in_h) lo = mid; else hi = mid - 1;
       }
-      *start = ChunkStart{b, h, lo, (int)(in_h - Cut::before(r, c.g, lo)), first, count, shares};
+      *start = ChunkStart{b, h, lo, (int)(in_h - Cut::before(r, c.lg, lo)), r, first, count, shares};
       break;
     }
   }
@@ -191,13 +198,13 @@ struct ChunkWalk {
   __device__ __forceinline__ ChunkWalk(const ChunkDims& dims, const ChunkStart& s)
       : c(dims), left(s.count), at(s.first), b(s.b), h(s.h), item(s.item) {
     if (left <= 0) return;
-    r = chunk_request(c, b, nullptr);
-    items = Cut::items(r, c.g);
+    r = s.r;
+    items = Cut::items(r, c.lg);
     u0 = s.u;
     set();
   }
   __device__ __forceinline__ void set() {
-    units = Cut::units(r, c.g, item);
+    units = Cut::units(r, c.lg, item);
     u1 = (int)min((long long)units, u0 + left);
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
@@ -217,7 +224,7 @@ struct ChunkWalk {
             return;
           }
           r = chunk_request(c, b, nullptr);
-          items = Cut::items(r, c.g);
+          items = Cut::items(r, c.lg);
         } while (items == 0);
       }
     }

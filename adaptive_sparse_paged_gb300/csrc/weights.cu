@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait_predecessor();
   const uint32_t tmem = sh.tmem;
   chunk_plan<KeyCut>(p.c, &sh.start, sh.scratch, p.err);
-  const int g = p.c.g, tile_tokens = kTileRows / g;
+  const int g = p.c.g, tile_tokens = kTileRows >> p.c.lg;
   ChunkReader reader(sh.tasks);
   ChunkTask task;  // x: row tiles of the piece, the first of them
 
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           sh.tasks, p.c, sh.start, p.joins + blockIdx.x,
           [&](const ChunkWalk<KeyCut>& w, ChunkTask& t) {
             t.x[0] = w.r.n > 0 ? w.u1 - w.u0 : 0;
-            t.x[1] = KeyCut::first_tile(w.r, g, w.item) + w.u0;
+            t.x[1] = KeyCut::first_tile(w.r, p.c.lg, w.item) + w.u0;
           });
       if (!ok) report(p.err, ASP_DEVERR_TIMEOUT);
     }
@@ -158,8 +158,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int row_tok[4], row_at[4];  // the lane's rows in a tile: token, and place in lse
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      row_tok[i] = (lane * 4 + i) / g;
-      row_at[i] = row_tok[i] * p.Hq + (lane * 4 + i) % g;
+      row_tok[i] = (lane * 4 + i) >> p.c.lg;
+      row_at[i] = row_tok[i] * p.Hq + ((lane * 4 + i) & (g - 1));
     }
     bool ok = true;
     while (ok && reader.next(task)) {
@@ -438,7 +438,7 @@ cudaError_t launch_chunk_t(const WeightArgs& a, cudaStream_t stream) {
                               {64, (unsigned)g, (unsigned)(kTileRows / g)});
   if (e != cudaSuccess) return e;
   if ((e = encode_bf16_2d_swizzled(&tk, kv.k_cache, D, cache_rows, 64, P)) != cudaSuccess) return e;
-  ChunkParams p{{a.q_offsets, kv.seq_lens, kv.batch, kv.num_kv_heads, g, kv.max_pages, P,
+  ChunkParams p{{a.q_offsets, kv.seq_lens, kv.batch, kv.num_kv_heads, g, chunk_log2(g), kv.max_pages, P,
                  a.num_tokens, chunk_inverse(a.num_sms)},
                 kv.block_table, a.lse, a.w_in, a.w_out, a.joins, a.partials, a.err, kv.num_q_heads,
                 kv.num_phys_pages, a.sm_scale * kLog2e, 1.0f / a.sm_scale, a.decay};
