@@ -87,6 +87,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
   float* wo = p.w_out + (size_t)seg * p.max_pages * P;
   int32_t* kept = p.kept + (size_t)seg * p.keep;
   if (seg % p.Hkv == 0 && tid == 0) p.new_lens[b] = min(T, p.keep);
+  if (p.src_table != p.dst_table) {
+    // a copy of the source table would be in place without its order: not done
+    const size_t at = (size_t)b * p.max_pages;
+    const int n = min(T, p.keep);
+    int same = 0;
+    for (int q = tid; q * P < n; q += kSelThreads)
+      same |= p.dst_table[at + q] == p.src_table[at + q] && p.dst_table[at + q] >= 0;
+    if (__syncthreads_or(same)) {
+      if (tid == 0) report(p.err, ASP_DEVERR_PAGE_RANGE);
+      for (int i = tid; i < n; i += kSelThreads) kept[i] = -1;
+      return;
+    }
+  }
   if (T <= p.keep) {
     for (int i = tid; i < T; i += kSelThreads) {
       kept[i] = i;
@@ -263,13 +276,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const Params p
       const int i = t * kTile + warp * kWarpRows + q * 32 + lane;
       src[q] = dst[q] = -1;
       if (q * 32 + lane < kWarpRows && i < n) {
-        src[q] = row_of(from, kept[i]);
+        const int s = kept[i];  // negative: the segment is not moved
+        src[q] = s >= 0 ? row_of(from, s) : -1;
         dst[q] = row_of(to, i);
-        // a copy of the source table: in place without its order, which is not done
-        if (!in_order && dst[q] >= 0 && to[i / P] == from[i / P]) {
-          report(p.err, ASP_DEVERR_PAGE_RANGE);
-          dst[q] = -1;
-        }
       }
     }
   };
@@ -292,8 +301,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const Params p
         d = r < 32 ? d0 : d1;
       }
       to_row[u] = s >= 0 ? d : -1;
-      if (s >= 0 && d >= 0) {
-        have |= 1u << u;
+      if (s >= 0) {  // loaded whether or not it has a place to go: places come later
         x[u] = __ldcg(reinterpret_cast<const uint2*>(cache + (size_t)s * D));
       }
     }
@@ -301,7 +309,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const Params p
     if (in_order) __syncthreads();  // every row of the tile is read before one is written
 #pragma unroll
     for (int u = 0; u < kGroup; ++u)
-      if (to_row[u] >= 0) *reinterpret_cast<uint2*>(cache + (size_t)to_row[u] * D) = x[u];
+      if (to_row[u] >= 0) {
+        *reinterpret_cast<uint2*>(cache + (size_t)to_row[u] * D) = x[u];
+        have |= 1u << u;
+      }
     if (!is_k) continue;
     const uint2 inf = make_uint2(0x7f807f80u, 0x7f807f80u);  // folding starts from +-infinity
     const uint2 neg_inf = make_uint2(0xff80ff80u, 0xff80ff80u);

@@ -147,7 +147,7 @@ def test_a_copy_of_the_table_is_refused(cuda_device):
     B.asp_weight_evict(kv, w, 100, 10, batch.table_dev.clone(), w, kept, lens, batch.ws)
     assert B.asp_get_device_error(batch.ws) == B.ASP_DEVERR_PAGE_RANGE
     assert same(batch.k_dev.cpu(), batch.k) and same(batch.v_dev.cpu(), batch.v)
-    assert bool((batch.summ_dev == 3.0).all())
+    assert bool((batch.summ_dev == 3.0).all()) and bool((kept == -1).all())
 
 
 def test_graph_replay(cuda_device):
