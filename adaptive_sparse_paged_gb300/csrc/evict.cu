@@ -1,8 +1,9 @@
 // evict.cu - eviction by accumulated attention weight: per (request, KV head)
 // the newest tokens and the heaviest of the others stay, in their order.
 //
-// select: one CTA per segment finds the weight of rank keep - recent by four
-// 8-bit radix passes over the order-preserving integer image of the weights.
+// select: a cluster of one to eight CTAs per segment, each with a part of its slots in
+// registers, finds the weight of rank keep - recent by four 8-bit radix passes over the
+// order-preserving integer image of the weights; the CTAs add up one another's bins.
 // Weights share few exponents, so most of a warp falls into one bin: every lane
 // counts in a column of its own, [bin][lane], and no two lanes of a warp meet.
 // One more walk ranks what stays (the slots above that weight, and of its equals
@@ -15,6 +16,8 @@
 // CTA owns some channels (64 to 256 bytes) of every K or V row of a segment and
 // walks its slots alone, so that the order needs no word between CTAs. Into other
 // pages there is no order to keep, and the slots are split over CTAs too.
+#include <cooperative_groups.h>
+
 #include "asp_internal.cuh"
 
 namespace asp {
@@ -48,7 +51,7 @@ __device__ __forceinline__ uint32_t ordered(float w) {
 
 constexpr int kPerThread = 4;                       // slots of a thread in one step
 constexpr int kStep = kSelThreads * kPerThread;
-constexpr int kHeld = 6;                            // steps whose slots stay in registers
+constexpr int kHeld = 4;                            // steps whose slots stay in registers
 
 // Exclusive prefix sum over the CTA's threads; `total` gets the whole sum.
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, uint32_t& total) {
@@ -73,20 +76,25 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, 
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params p, int P) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   __shared__ int hist[256 * 32];           // [bin][lane]
-  __shared__ int bins[256];
+  __shared__ int bins[2][256];             // this CTA's, read by the cluster; two passes' worth
+  __shared__ int all_bins[256];
+  __shared__ int counts[2];                // this CTA's slots above and equal
   __shared__ uint32_t warp_sums[2][kSelThreads / 32];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need, s_in_bin;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int seg = blockIdx.x, b = seg / p.Hkv;
+  const int seg = blockIdx.x / C, b = seg / p.Hkv;
   pdl_launch_dependents();
   pdl_wait_predecessor();
   const int T = clamp_seq_len(p.seq_lens[b], p.max_pages, P, tid == 0 ? p.err : nullptr);
   const float* w = p.weights + (size_t)seg * p.max_pages * P;  // 16-byte aligned: P % 16 == 0
   float* wo = p.w_out + (size_t)seg * p.max_pages * P;
   int32_t* kept = p.kept + (size_t)seg * p.keep;
-  if (seg % p.Hkv == 0 && tid == 0) p.new_lens[b] = min(T, p.keep);
+  if (seg % p.Hkv == 0 && rank == 0 && tid == 0) p.new_lens[b] = min(T, p.keep);
   if (p.src_table != p.dst_table) {
     // a copy of the source table would be in place without its order: not done
     const size_t at = (size_t)b * p.max_pages;
@@ -101,7 +109,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
     }
   }
   if (T <= p.keep) {
-    for (int i = tid; i < T; i += kSelThreads) {
+    for (int i = rank * kSelThreads + tid; i < T; i += C * kSelThreads) {
       kept[i] = i;
       wo[i] = w[i];
     }
@@ -119,12 +127,15 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
     }
     return x;
   };
-  // The first steps' weights are read once, all loads in flight; later ones (of segments
-  // over kHeld * kStep slots) again in every pass.
+  // This CTA's slots: [s0, s1). The first steps' weights are read once, all loads in flight;
+  // later ones (of parts over kHeld * kStep slots) again in every pass.
+  const int span = ceil_div(T, C * kPerThread) * kPerThread;
+  const int s0 = min(T, rank * span), s1 = min(T, s0 + span);
   float4 held[kHeld];
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k) held[k] = load4(k * kStep + tid * kPerThread, T);
+  for (int k = 0; k < kHeld; ++k) held[k] = load4(s0 + k * kStep + tid * kPerThread, s1);
   const int m = T - p.recent, need0 = p.keep - p.recent;  // need0 of the first m slots stay
+  const int m1 = min(m, s1);
   uint32_t prefix = 0;
   int need = need0;
   if (need0 > 0) {
@@ -137,28 +148,37 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t u = ordered(y[k]);
-          if (i + k < m && (shift == 24 || (u >> (shift + 8)) == prefix))
+          if (i + k < m1 && (shift == 24 || (u >> (shift + 8)) == prefix))
             atomicAdd(&hist[((u >> shift) & 255) * 32 + lane], 1);
         }
       };
 #pragma unroll
       for (int k = 0; k < kHeld; ++k)
-        if (k * kStep < m) count(k * kStep, held[k]);
-      for (int i0 = kHeld * kStep; i0 < m; i0 += kStep)
-        count(i0, load4(i0 + tid * kPerThread, m));
+        if (s0 + k * kStep < m1) count(s0 + k * kStep, held[k]);
+      for (int i0 = s0 + kHeld * kStep; i0 < m1; i0 += kStep)
+        count(i0, load4(i0 + tid * kPerThread, s1));
       __syncthreads();
       // bin sums: a warp adds up eight bins, a lane a column
 #pragma unroll
       for (int k = 0; k < 256 / (kSelThreads / 32); ++k) {
         const int bin = warp * (256 / (kSelThreads / 32)) + k;
         const int n = __reduce_add_sync(kFull, hist[bin * 32 + lane]);
-        if (lane == 0) bins[bin] = n;
+        if (lane == 0) bins[(shift >> 3) & 1][bin] = n;
+      }
+      int* const own_bins = bins[(shift >> 3) & 1];
+      if (C > 1) {
+        cluster.sync();
+        if (tid < 256) {
+          int n = 0;
+          for (int r = 0; r < C; ++r) n += cluster.map_shared_rank(own_bins, r)[tid];
+          all_bins[tid] = n;
+        }
       }
       __syncthreads();
       if (warp == 0) {  // the bin of rank `need` from the top; lane i holds bins 8 i .. 8 i + 7
         int n[8], mine = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mine += n[k] = bins[lane * 8 + k];
+        for (int k = 0; k < 8; ++k) mine += n[k] = (C > 1 ? all_bins : own_bins)[lane * 8 + k];
         int above = mine;  // inclusive sum from this lane's bins to the top
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -188,7 +208,44 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
   // whole bin stays (need 0 after it), equals of its lower edge stay too.
   const bool all_equal = need0 > 0 && need == 0;
   if (all_equal) need = 0x7fffffff;
+  // What the CTAs of the slots before keep: each counts its own. The barrier also says that
+  // every part in registers has been read, before any slot is written in place.
   int above_before = 0, equal_before = 0;
+  if (C > 1) {
+    uint32_t mine = 0;  // above in the low half, equal in the high half: 16 of a thread, or
+                        // as many as the steps read again give, under 2^16 together
+    auto tally = [&](int i0, const float4& x) {
+      const int i = i0 + tid * kPerThread;
+      const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t u = ordered(y[k]);
+        const bool in = i + k < m1 && need0 > 0;
+        mine += ((i + k >= m && i + k < s1) || (in && u > prefix) ? 1u : 0u) +
+                (in && u == prefix ? 0x10000u : 0u);
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (s0 + k * kStep < s1) tally(s0 + k * kStep, held[k]);
+    for (int i0 = s0 + kHeld * kStep; i0 < s1; i0 += kStep)
+      tally(i0, load4(i0 + tid * kPerThread, s1));
+    if (tid < 2) counts[tid] = 0;
+    __syncthreads();
+    const int over_n = __reduce_add_sync(kFull, (int)(mine & 0xffff));
+    const int same_n = __reduce_add_sync(kFull, (int)(mine >> 16));
+    if (lane == 0) {
+      atomicAdd(&counts[0], over_n);
+      atomicAdd(&counts[1], same_n);
+    }
+    cluster.sync();
+    for (int r = 0; r < rank; ++r) {
+      const int* theirs = cluster.map_shared_rank(&counts[0], r);
+      above_before += theirs[0];
+      equal_before += theirs[1];
+    }
+    cluster.sync();  // every CTA has read the others' counts: they may end
+  }
   int par = 0;
   float4 next = make_float4(0.f, 0.f, 0.f, 0.f);
   auto emit = [&](int i0, const float4& x) {
@@ -199,8 +256,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t u = ordered(y[k]);
-      const bool in = i + k < m && need0 > 0;
-      over[k] = (i + k >= m && i + k < T) || (in && u > prefix);
+      const bool in = i + k < m1 && need0 > 0;
+      over[k] = (i + k >= m && i + k < s1) || (in && u > prefix);
       same[k] = in && u == prefix;
       cnt += (over[k] ? 1u : 0u) + (same[k] ? 0x10000u : 0u);
     }
@@ -223,12 +280,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
   };
 #pragma unroll
   for (int k = 0; k < kHeld; ++k)
-    if (k * kStep < T) emit(k * kStep, held[k]);
+    if (s0 + k * kStep < s1) emit(s0 + k * kStep, held[k]);
   // a step's slots are read before the step before is written: it writes lower slots only
-  if (kHeld * kStep < T) next = load4(kHeld * kStep + tid * kPerThread, T);
-  for (int i0 = kHeld * kStep; i0 < T; i0 += kStep) {
+  const int more = s0 + kHeld * kStep;
+  if (more < s1) next = load4(more + tid * kPerThread, s1);
+  for (int i0 = more; i0 < s1; i0 += kStep) {
     const float4 x = next;
-    next = load4(i0 + kStep + tid * kPerThread, T);
+    next = load4(i0 + kStep + tid * kPerThread, s1);
     emit(i0, x);
   }
 }
@@ -371,8 +429,25 @@ cudaError_t launch_t(const EvictArgs& a, cudaStream_t stream) {
   const int segments = kv.batch * kv.num_kv_heads;
   cudaError_t e = set_max_dynamic_smem((const void*)evict_select_kernel, 0);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(evict_select_kernel, dim3(segments), dim3(kSelThreads), 0, stream, p, P);
-  if (e != cudaSuccess) return e;
+  // CTAs of a segment: as many as the GPU holds at once, with 8192 slots each at least. In
+  // place the whole segment has to be in registers (a CTA writes slots that another reads);
+  // what is too long for that is left to one CTA.
+  const long long capacity = (long long)kv.max_pages * P;
+  int C = 1;
+  while (C < 8 && 2 * C * segments <= a.num_sms && capacity > 8192ll * C) C *= 2;
+  if (p.weights == p.w_out && capacity > (long long)C * kHeld * kStep) C = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(segments * C);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)C, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 2 : 1;
+  if ((e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, P)) != cudaSuccess) return e;
   // Whole rows where the segments alone fill the GPU; in place with fewer of them,
   // slices of 64 bytes make up for it.
   const bool few = p.src_table == p.dst_table && segments < a.num_sms;

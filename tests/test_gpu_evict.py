@@ -119,6 +119,18 @@ def test_long_segments(cuda_device):
     run(cuda_device, [40000, 70001], 1, 64, 64, 39999, 5, False, seed=4)
 
 
+@pytest.mark.parametrize("tokens,keep", [([20000], 9000), ([9000, 16385], 8192), ([70000], 50000),
+                                         ([140000, 3], 70000)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_several_blocks_a_segment(cuda_device, tokens, keep, in_place):
+    """Few segments: several blocks share one, in registers or reading it again."""
+    def ties(batch, slots):
+        u = torch.rand((batch.B, batch.Hkv, slots), generator=batch.gen)
+        return torch.where(u < 0.5, (u * 20).floor(), u)
+    run(cuda_device, tokens, 1, 64, 16, keep, 100, in_place, ties, seed=keep, same_w=in_place)
+    run(cuda_device, tokens, 1, 64, 16, keep, keep, in_place, seed=keep + 1, same_w=not in_place)
+
+
 def test_many_segments(cuda_device):
     tokens = [20 + (i * 13) % 150 for i in range(150)]
     run(cuda_device, tokens, 8, 64, 16, 64, 10, True, seed=5)
