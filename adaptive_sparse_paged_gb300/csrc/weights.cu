@@ -17,11 +17,17 @@
 // itself: read from shared memory for every element it cost as much as the products. An item that several CTAs share leaves its partial sums in the
 // workspace; a second, small kernel adds them up.
 //
+// Measured: 2048 rows over 32768 tokens (32 query, 8 KV heads, d = 128) in 0.38 ms, 1.40
+// PFLOP/s; a product of 128 x 128 takes some 85 cycles a step where 64 are the tensor cores'
+// own, the port of tensor memory being shared with the sums' reads. 733 us with keys in
+// shared memory and the lse read an element at a time.
+//
 // Decode form (decode_weights_kernel): one token a request, fp32 queries, page
 // lists. The keys are read once and the kernel is bound by HBM, so the tiles of
 // all lists form one sequence, two CTAs an SM take equal shares of it, and the
 // queries (at most 8 heads of a group, each as three bf16 terms that add up to
-// its 24 bits) ride along as 32 columns.
+// its 24 bits) ride along as 32 columns. Measured: 30% of the pages of 4 x 131072
+// tokens in 48 us, 6.0 TB/s; all of 8 x 4096 in 10.3 us.
 #include "chunk_plan.cuh"
 #include "tc.cuh"
 
