@@ -209,9 +209,12 @@ class PagedKV:
             self.block_table.data_ptr(), self.seq_lens.data_ptr(), b, int(self.num_q_heads),
             hkv, d, p, max_pages, n)
 
-    @property
-    def ref(self):
-        return ctypes.byref(self.struct)
+        # shapes and reference that every call asks for
+        self.ref = ctypes.byref(self.struct)
+        self.q_shape = (b, int(self.num_q_heads), d)
+        self.lens_shape, self.lists_shape = (b, hkv), (b, hkv, max_pages)
+        self.offsets_shape = (b + 1,)
+        self.weights_shape = (b, hkv, max_pages * p)
 
 
 def new_summaries(k_cache: torch.Tensor, block_table: torch.Tensor) -> torch.Tensor:
@@ -253,9 +256,9 @@ def asp_page_summarize(kv: PagedKV, mode: int, k_new, v_new, ws: torch.Tensor, s
 def asp_coverage_select(kv: PagedKV, q: torch.Tensor, gamma: float, budget: int,
                         lists: torch.Tensor, lens: torch.Tensor, ws: torch.Tensor,
                         stream=None) -> None:
-    _need(q, "q", torch.float32, kv.device, (kv.batch, kv.num_q_heads, kv.head_dim))
-    _need(lists, "lists", torch.int32, kv.device, (kv.batch, kv.num_kv_heads, kv.max_pages))
-    _need(lens, "lens", torch.int32, kv.device, (kv.batch, kv.num_kv_heads))
+    _need(q, "q", torch.float32, kv.device, kv.q_shape)
+    _need(lists, "lists", torch.int32, kv.device, kv.lists_shape)
+    _need(lens, "lens", torch.int32, kv.device, kv.lens_shape)
     _need(ws, "ws", torch.uint8, kv.device)
     _run("asp_coverage_select", kv.device, kv.ref, q.data_ptr(), float(gamma), int(budget),
          lists.data_ptr(), lens.data_ptr(), ws.data_ptr(), ws.numel(), _stream_ptr(kv.device,
@@ -269,9 +272,9 @@ def asp_coverage_select_append(kv: PagedKV, k_new: torch.Tensor, v_new: torch.Te
     shp = (kv.batch, kv.num_kv_heads, kv.head_dim)
     _need(k_new, "k_new", torch.bfloat16, kv.device, shp)
     _need(v_new, "v_new", torch.bfloat16, kv.device, shp)
-    _need(q, "q", torch.float32, kv.device, (kv.batch, kv.num_q_heads, kv.head_dim))
-    _need(lists, "lists", torch.int32, kv.device, (kv.batch, kv.num_kv_heads, kv.max_pages))
-    _need(lens, "lens", torch.int32, kv.device, (kv.batch, kv.num_kv_heads))
+    _need(q, "q", torch.float32, kv.device, kv.q_shape)
+    _need(lists, "lists", torch.int32, kv.device, kv.lists_shape)
+    _need(lens, "lens", torch.int32, kv.device, kv.lens_shape)
     _need(ws, "ws", torch.uint8, kv.device)
     _run("asp_coverage_select_append", kv.device, kv.ref, k_new.data_ptr(), v_new.data_ptr(),
          q.data_ptr(), float(gamma), int(budget), lists.data_ptr(), lens.data_ptr(), ws.data_ptr(),
@@ -289,9 +292,9 @@ def asp_select_plan(kv: PagedKV, gamma: float, budget: int = 0, append: bool = F
 def asp_page_scores(kv: PagedKV, q: torch.Tensor, scores: torch.Tensor, ws: torch.Tensor,
                     stream=None) -> None:
     """Per-page scores [B, Hkv, max_pages] fp32 (entries past N_b untouched)."""
-    _need(q, "q", torch.float32, kv.device, (kv.batch, kv.num_q_heads, kv.head_dim))
+    _need(q, "q", torch.float32, kv.device, kv.q_shape)
     _need(scores, "scores", torch.float32, kv.device,
-          (kv.batch, kv.num_kv_heads, kv.max_pages))
+          kv.lists_shape)
     _need(ws, "ws", torch.uint8, kv.device)
     _run("asp_page_scores", kv.device, kv.ref, q.data_ptr(), scores.data_ptr(), ws.data_ptr(),
          ws.numel(), _stream_ptr(kv.device, stream))
@@ -300,10 +303,10 @@ def asp_page_scores(kv: PagedKV, q: torch.Tensor, scores: torch.Tensor, ws: torc
 def asp_sparse_decode(kv: PagedKV, q: torch.Tensor, lists: torch.Tensor, lens: torch.Tensor,
                       sm_scale: float, out: torch.Tensor, lse: torch.Tensor, ws: torch.Tensor,
                       stream=None) -> None:
-    _need(q, "q", torch.float32, kv.device, (kv.batch, kv.num_q_heads, kv.head_dim))
-    _need(lists, "lists", torch.int32, kv.device, (kv.batch, kv.num_kv_heads, kv.max_pages))
-    _need(lens, "lens", torch.int32, kv.device, (kv.batch, kv.num_kv_heads))
-    _need(out, "out", torch.float32, kv.device, (kv.batch, kv.num_q_heads, kv.head_dim))
+    _need(q, "q", torch.float32, kv.device, kv.q_shape)
+    _need(lists, "lists", torch.int32, kv.device, kv.lists_shape)
+    _need(lens, "lens", torch.int32, kv.device, kv.lens_shape)
+    _need(out, "out", torch.float32, kv.device, kv.q_shape)
     _need(lse, "lse", torch.float32, kv.device, (kv.batch, kv.num_q_heads))
     _need(ws, "ws", torch.uint8, kv.device)
     _run("asp_sparse_decode", kv.device, kv.ref, q.data_ptr(), lists.data_ptr(), lens.data_ptr(),
@@ -320,9 +323,9 @@ def asp_coverage_select_noalloc(kv: PagedKV, q: torch.Tensor, gamma: float, budg
     size limit and the rule that overlapping calls must be serialised.
     dev_error: optional int32 [1] device tensor that collects device error bits.
     """
-    _need(q, "q", torch.float32, kv.device, (kv.batch, kv.num_q_heads, kv.head_dim))
-    _need(lists, "lists", torch.int32, kv.device, (kv.batch, kv.num_kv_heads, kv.max_pages))
-    _need(lens, "lens", torch.int32, kv.device, (kv.batch, kv.num_kv_heads))
+    _need(q, "q", torch.float32, kv.device, kv.q_shape)
+    _need(lists, "lists", torch.int32, kv.device, kv.lists_shape)
+    _need(lens, "lens", torch.int32, kv.device, kv.lens_shape)
     err_ptr = None
     if dev_error is not None:
         _need(dev_error, "dev_error", torch.int32, kv.device, (1,))
@@ -333,7 +336,7 @@ def asp_coverage_select_noalloc(kv: PagedKV, q: torch.Tensor, gamma: float, budg
 
 def weights_shape(kv: PagedKV):
     """Shape of the attention weights of this cache: [B, Hkv, max_pages * P]."""
-    return (kv.batch, kv.num_kv_heads, kv.max_pages * kv.page_size)
+    return kv.weights_shape
 
 
 def new_weights(kv: PagedKV) -> torch.Tensor:
@@ -351,10 +354,10 @@ def _need_rows(kv: PagedKV, t: torch.Tensor, name: str, heads: int) -> int:
 
 
 def _need_weights(kv: PagedKV, w_in, w_out) -> int | None:
-    _need(w_out, "w_out", torch.float32, kv.device, weights_shape(kv))
+    _need(w_out, "w_out", torch.float32, kv.device, kv.weights_shape)
     if w_in is None:
         return None
-    _need(w_in, "w_in", torch.float32, kv.device, weights_shape(kv))
+    _need(w_in, "w_in", torch.float32, kv.device, kv.weights_shape)
     return w_in.data_ptr()
 
 
@@ -372,7 +375,7 @@ def asp_norm_rotate_append(kv: PagedKV, qkv: torch.Tensor, q_offsets, positions,
     offs_ptr = pos_ptr = qw_ptr = kw_ptr = freq_ptr = None
     rotary_dim = 0
     if q_offsets is not None:
-        _need(q_offsets, "q_offsets", torch.int32, dev, (kv.batch + 1,))
+        _need(q_offsets, "q_offsets", torch.int32, dev, kv.offsets_shape)
         offs_ptr = q_offsets.data_ptr()
     if positions is not None:
         _need(positions, "positions", torch.int32, dev, (n,))
@@ -407,7 +410,7 @@ def asp_chunk_attention(kv: PagedKV, q: torch.Tensor, q_offsets: torch.Tensor, s
                         stream=None) -> None:
     """Causal attention of the new tokens' rows q (bf16 [N, Hq, d]) over the cache."""
     n = _need_rows(kv, q, "q", kv.num_q_heads)
-    _need(q_offsets, "q_offsets", torch.int32, kv.device, (kv.batch + 1,))
+    _need(q_offsets, "q_offsets", torch.int32, kv.device, kv.offsets_shape)
     _need(out, "out", torch.bfloat16, kv.device, (n, kv.num_q_heads, kv.head_dim))
     _need(lse, "lse", torch.float32, kv.device, (n, kv.num_q_heads))
     _need(ws, "ws", torch.uint8, kv.device)
@@ -421,7 +424,7 @@ def asp_chunk_weights(kv: PagedKV, q: torch.Tensor, q_offsets: torch.Tensor, lse
                       stream=None) -> None:
     """w_out = decay * w_in + the attention weight each cached token got from the rows q."""
     n = _need_rows(kv, q, "q", kv.num_q_heads)
-    _need(q_offsets, "q_offsets", torch.int32, kv.device, (kv.batch + 1,))
+    _need(q_offsets, "q_offsets", torch.int32, kv.device, kv.offsets_shape)
     _need(lse, "lse", torch.float32, kv.device, (n, kv.num_q_heads))
     w_ptr = _need_weights(kv, w_in, w_out)
     _need(ws, "ws", torch.uint8, kv.device)
@@ -434,11 +437,11 @@ def asp_decode_weights(kv: PagedKV, q: torch.Tensor, lists, lens, lse: torch.Ten
                        sm_scale: float, decay: float, w_in, w_out: torch.Tensor, ws: torch.Tensor,
                        stream=None) -> None:
     """w_out = decay * w_in + the attention weight of a decode step (lists and lens None: every page)."""
-    _need(q, "q", torch.float32, kv.device, (kv.batch, kv.num_q_heads, kv.head_dim))
+    _need(q, "q", torch.float32, kv.device, kv.q_shape)
     lists_ptr = lens_ptr = None
     if lists is not None or lens is not None:
-        _need(lists, "lists", torch.int32, kv.device, (kv.batch, kv.num_kv_heads, kv.max_pages))
-        _need(lens, "lens", torch.int32, kv.device, (kv.batch, kv.num_kv_heads))
+        _need(lists, "lists", torch.int32, kv.device, kv.lists_shape)
+        _need(lens, "lens", torch.int32, kv.device, kv.lens_shape)
         lists_ptr, lens_ptr = lists.data_ptr(), lens.data_ptr()
     _need(lse, "lse", torch.float32, kv.device, (kv.batch, kv.num_q_heads))
     w_ptr = _need_weights(kv, w_in, w_out)
@@ -452,9 +455,9 @@ def asp_weight_evict(kv: PagedKV, weights: torch.Tensor, keep: int, recent: int,
                      dst_table: torch.Tensor, w_out: torch.Tensor, kept: torch.Tensor,
                      new_lens: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """Keeps the `recent` newest and the heaviest other tokens of every head, `keep` in all."""
-    _need(weights, "weights", torch.float32, kv.device, weights_shape(kv))
+    _need(weights, "weights", torch.float32, kv.device, kv.weights_shape)
     _need(dst_table, "dst_table", torch.int32, kv.device, (kv.batch, kv.max_pages))
-    _need(w_out, "w_out", torch.float32, kv.device, weights_shape(kv))
+    _need(w_out, "w_out", torch.float32, kv.device, kv.weights_shape)
     _need(kept, "kept", torch.int32, kv.device, (kv.batch, kv.num_kv_heads, int(keep)))
     _need(new_lens, "new_lens", torch.int32, kv.device, (kv.batch,))
     _need(ws, "ws", torch.uint8, kv.device)

@@ -133,55 +133,77 @@ struct ChunkStart {
 };
 
 // Fills *start (shared memory) for this CTA; every thread of the block calls it.
-// scratch: one long long for each warp.
+// scratch: one long long for each warp. Two passes over a thread's requests through one loop:
+// the first adds their units up, the second, once the shares are known, finds the one where
+// this CTA's begins. (The plan is code that runs once, before everything else, so what it
+// costs is mostly its fetching: there is one copy of Cut::before in it.)
 template <typename Cut>
 __device__ __forceinline__ void chunk_plan(const ChunkDims& c, ChunkStart* start, long long* scratch,
                                            uint32_t* err) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int per = ceil_div(c.B, nt), b0 = min(c.B, tid * per), b1 = min(c.B, b0 + per);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    const ChunkRequest r = chunk_request(c, b, blockIdx.x == 0 ? err : nullptr);
-    mine += (long long)c.Hkv * Cut::before(r, c.lg, Cut::items(r, c.lg));
-  }
-  long long x = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) scratch[warp] = x;
   if (tid == 0) start->count = 0;
-  __syncthreads();
-  long long before = 0, total = 0;
-  for (int w = 0; w < nt / 32; ++w) {
-    if (w < warp) before += scratch[w];
-    total += scratch[w];
-  }
-  before += x - mine;
-  const ChunkShares shares(total, gridDim.x, c.inv_ctas);
-  const long long first = shares.begin(blockIdx.x), count = shares.begin(blockIdx.x + 1) - first;
-  if (count > 0 && first >= before && first < before + mine) {
-    long long at = before;
-    for (int b = b0; b < b1; ++b) {
-      const ChunkRequest r = chunk_request(c, b, nullptr);
-      const int items = Cut::items(r, c.lg);
-      const long long head = Cut::before(r, c.lg, items);
-      if (first >= at + c.Hkv * head) {
-        at += c.Hkv * head;
-        continue;
+  if (blockIdx.x != 0) err = nullptr;
+  ChunkShares shares;
+  long long mine = 0, at = 0, first = 0, count = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    bool found = false;
+#pragma unroll 1
+    for (int b = b0; b < b1 && !found; ++b) {
+      const ChunkRequest r = chunk_request(c, b, err);
+      int lo = 0, hi = Cut::items(r, c.lg), x = hi, h = -1;  // h < 0: x is all of a head's items
+      long long in_h = 0, lo_units = 0;
+#pragma unroll 1
+      while (true) {
+        const long long v = Cut::before(r, c.lg, x);
+        if (h < 0) {
+          const long long all = c.Hkv * v;
+          if (pass == 0) {
+            mine += all;
+            break;
+          }
+          if (first >= at + all) {
+            at += all;
+            break;
+          }
+          in_h = first - at;
+          for (h = 0; in_h >= v; in_h -= v) ++h;  // fewer than Hkv <= 8 steps
+          --hi;
+        } else if (v <= in_h) {
+          lo = x;
+          lo_units = v;
+        } else {
+          hi = x - 1;
+        }
+        if (lo >= hi) {
+          *start = ChunkStart{b, h, lo, (int)(in_h - lo_units), r, first, count, shares};
+          found = true;
+          break;
+        }
+        x = (lo + hi + 1) >> 1;
       }
-      int h = 0;
-      long long in_h = first - at;
-      for (; in_h >= head; in_h -= head) ++h;  // fewer than Hkv <= 8 steps
-      int lo = 0, hi = items - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (Cut::before(r, c.lg, mid) <= in_h) lo = mid; else hi = mid - 1;
-      }
-      *start = ChunkStart{b, h, lo, (int)(in_h - Cut::before(r, c.lg, lo)), r, first, count, shares};
-      break;
     }
+    if (pass == 1) break;
+    long long sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    if (lane == 31) scratch[warp] = sum;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < nt / 32; ++w) {
+      if (w < warp) at += scratch[w];
+      total += scratch[w];
+    }
+    at += sum - mine;
+    shares = ChunkShares(total, gridDim.x, c.inv_ctas);
+    first = shares.begin(blockIdx.x);
+    count = shares.begin(blockIdx.x + 1) - first;
+    err = nullptr;
+    if (count <= 0 || first < at || first >= at + mine) break;
   }
   __syncthreads();
 }

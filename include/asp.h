@@ -317,8 +317,8 @@ asp_status asp_norm_rotate_append(const asp_paged_kv* kv, const uint16_t* qkv,
  *   lse[r,h]   = log sum_{s <= t} exp(sm_scale * q[r,h].k_s)
  * with t = T_b - n_b + i the slot of row r = q_offsets[b] + i.
  * q   : bf16 [num_tokens, Hq, d], 16-byte aligned.
- * out : bf16 [num_tokens, Hq, d], 16-byte aligned; lse : fp32 [num_tokens, Hq]
- *       (natural log).
+ * out : bf16 [num_tokens, Hq, d], 16-byte aligned, not overlapping q;
+ * lse : fp32 [num_tokens, Hq] (natural log).
  * Slots past T_b are never used, whatever they hold; pages with an
  * out-of-range table entry are skipped (ASP_DEVERR_PAGE_RANGE); a row that
  * sees no valid page gets out = 0, lse = -inf. V of the request's own tokens
