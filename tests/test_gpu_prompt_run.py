@@ -175,6 +175,47 @@ def test_prompt_evict_decode(cuda_device):
         pos = [p + 1 for p in pos]
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_two_streams_at_once(cuda_device, dim):
+    """Calls with workspaces of their own on two streams: the same results as one by one."""
+    dev = cuda_device
+    batch = R.Batch(dev, [1500, 700, 64], [300, 60, 1], 8, 2, dim, 16, seed=31)
+    kv = batch.to_device()
+    q = batch.q.to(dev)
+    qd = torch.randn((3, 8, dim), generator=batch.gen).to(dev)
+    other = B.new_workspace(kv)
+
+    def outputs():
+        return [torch.zeros((batch.N, 8, dim), dtype=torch.bfloat16, device=dev),
+                torch.zeros((batch.N, 8), device=dev), B.new_weights(kv), B.new_weights(kv)]
+
+    def first(o, ws, stream=None):
+        B.asp_chunk_attention(kv, q, batch.offs_dev, batch.scale, o[0], o[1], ws, stream)
+
+    def second(o, lse, ws, stream=None):
+        B.asp_chunk_weights(kv, q, batch.offs_dev, lse, batch.scale, 1.0, None, o[2], ws, stream)
+        B.asp_decode_weights(kv, qd, None, None, lse[:3].contiguous(), batch.scale, 1.0, None, o[3],
+                             ws, stream)
+
+    want = outputs()
+    first(want, batch.ws)
+    second(want, want[1], batch.ws)
+    torch.cuda.synchronize()
+    lse3 = want[1]
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    got = outputs()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(a):
+            first(got, batch.ws)
+        with torch.cuda.stream(b):
+            second(got, lse3, other)
+    torch.cuda.synchronize()
+    assert B.asp_get_device_error(batch.ws) == 0 and B.asp_get_device_error(other) == 0
+    for x, y in zip(want, got):
+        assert torch.equal(x, y)
+
+
 def test_shape_checks(cuda_device):
     model = Model(cuda_device, [40, 20], seed=2)
     kvs = model.kvs([40, 20])
