@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4*>(v + (e / 8) * (P * 128) + (e % 8) * 16) =
                     make_uint4(0, 0, 0, 0);
             }
+            __syncwarp();
             fence_proxy_async_smem();
           }
         }
@@ -435,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(i == 0 ? &sh.p_half[t] : &sh.p_full[t]);
+          __syncwarp();
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
@@ -489,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (dst[k])
               *reinterpret_cast<uint4*>(dst[k] + 32 * i + 8 * q) =
                   make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
+          __syncwarp();
         }
         if (mine) p.lse[at] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
       } else {
@@ -504,12 +507,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t o[32];
           tmem_ld32(o_at + 32 * i, o);
           tmem_wait_ld(o);
-          if (!mine) continue;
+          if (mine) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[(8 * i + e) * kChunkRows] =
-                make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                            __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+            for (int e = 0; e < 8; ++e)
+              dst[(8 * i + e) * kChunkRows] =
+                  make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                              __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+          }
+          __syncwarp();
         }
       }
       tc_fence_before();  // the next piece's first product writes O after the next P arrives

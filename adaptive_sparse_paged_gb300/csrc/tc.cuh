@@ -26,7 +26,9 @@ __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// 32 columns of this warp's 32 lanes: thread i holds lane 32 * (warp % 4) + i.
+// 32 columns of this warp's 32 lanes: thread i holds lane 32 * (warp % 4) + i. These and
+// the waits are warp-aligned: all lanes have to come to them together, so a branch that
+// not every lane takes is followed by __syncwarp() (or a vote of the whole warp) first.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "

@@ -800,6 +800,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
 #pragma unroll
           for (int i = 0; i < kMaxGroup; ++i) nl[i] = sh.lse[buf][i];
         }
+        __syncwarp();
         tc_fence_after();
         uint32_t s[32];
         tmem_ld32(tmem + lanes + sb * kQueryCols, s);

@@ -256,3 +256,20 @@ def test_another_stream_and_graphs_that_share_a_workspace(cuda_device):
     assert B.asp_get_device_error(ws) == 0
     for x, (out, lse) in zip((a, c), outs):
         check(x, out, lse)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,P", [(2, 1, 64, 16), (8, 2, 128, 16), (4, 4, 128, 64), (8, 1, 64, 32)])
+@pytest.mark.parametrize("tokens,news", [
+    ([4099], [3]),               # a split item whose rows end inside a warp
+    ([131, 77], [131, 77]),      # whole items that do, over a last tile with empty slots
+    ([2051, 1500], [37, 291])])  # both
+def test_rows_that_end_inside_a_warp(cuda_device, Hq, Hkv, d, P, tokens, news):
+    """Some lanes of a warp have a row, a key or a place to write, and others have none."""
+    batch = R.Batch(cuda_device, tokens, news, Hq, Hkv, d, P, seed=sum(news), lead=1, tail=2)
+    batch.to_device()
+    out, lse = call(batch)
+    for _ in range(3):
+        again, lse_again = call(batch)
+        assert torch.equal(again, out) and torch.equal(lse_again, lse)
+    assert B.asp_get_device_error(batch.ws) == 0
+    check(batch, out, lse)

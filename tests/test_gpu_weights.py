@@ -264,3 +264,25 @@ def test_decode_bad_lists_and_pages(cuda_device):
     batch.table_dev[0, 0] = -1
     B.asp_decode_weights(*args())
     assert B.asp_get_device_error(batch.ws) == B.ASP_DEVERR_PAGE_RANGE
+
+
+@pytest.mark.parametrize("d,P", [(64, 16), (128, 64)])
+def test_decode_keys_that_end_inside_a_warp(cuda_device, d, P):
+    """Lanes with a key beside lanes of unlisted pages and of slots past the last token."""
+    batch, q, lists, lens = decode_case(cuda_device, [1003, 21, 5 * P + 1], 4, 2, d, P, 0.4, seed=d)
+    kv = batch.to_device()
+    start = torch.rand((batch.B, 2, batch.max_pages * P), generator=batch.gen)
+    dev = cuda_device
+    for ls, ln in ((lists, lens), (None, None)):
+        lse = decode_form(batch, q, ls, ln, None, 0.5, start)[2]
+        want, tol, _ = decode_form(batch, q, ls, ln, lse, 0.5, start)
+        first = None
+        for _ in range(3):
+            w = guards.guarded(start.shape, torch.float32, dev, fill=FILL)
+            B.asp_decode_weights(kv, q.to(dev), None if ls is None else ls.to(dev),
+                                 None if ln is None else ln.to(dev), lse.to(dev), batch.scale, 0.5,
+                                 start.to(dev), w, batch.ws)
+            assert first is None or torch.equal(first, w)
+            first = w
+        assert B.asp_get_device_error(batch.ws) == 0
+        check(batch, w, want, tol)
