@@ -56,6 +56,13 @@ constexpr int kChunkRows = 256;
 struct ChunkJoin {
   int b, h, item, pieces;  // pieces 0: no item begins here that other CTAs end
 };
+// Whether the join that CTA `cta` of `ctas` left names pieces of this call. A CTA that gives up
+// a wait leaves none (pieces 0), and nothing else that may lie in the workspace is followed.
+__host__ __device__ inline bool chunk_join_valid(const ChunkJoin& j, int batch, int kv_heads, int cta,
+                                                 int ctas) {
+  return j.pieces >= 2 && j.pieces <= ctas - cta && j.b >= 0 && j.b < batch && j.h >= 0 &&
+         j.h < kv_heads && j.item >= 0;
+}
 struct WsLayout {
   size_t arrivals_off = 0;
   size_t scores_off = 0;

@@ -536,11 +536,11 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const Params p) {
   __shared__ __align__(16) uint16_t tile[32 * kPitch];
   pdl_launch_dependents();
   pdl_wait_predecessor();
-  const ChunkJoin jn = p.joins[blockIdx.x];
-  if (jn.pieces < 2) return;
+  ChunkJoin jn;
+  ChunkRequest r;
+  if (!chunk_join<RowCut>(p.c, p.joins, p.err, jn, r)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = p.c.g, row = blockIdx.y * 32 + lane;
-  const ChunkRequest r = chunk_request(p.c, jn.b, nullptr);
   const int tok0 = jn.item * (kChunkRows >> p.c.lg);
   const size_t slot_floats = chunk_slot_floats(D);
   const float* first = p.partials + (size_t)(2 * blockIdx.x + 1) * slot_floats + row;

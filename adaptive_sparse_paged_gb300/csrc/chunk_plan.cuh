@@ -280,13 +280,15 @@ __device__ __forceinline__ void chunk_tasks_init(ChunkTasks& r, int readers) {
   }
 }
 
-// The handing thread: fill(walk, task) sets task.x. Returns false where a wait ran out.
+// The handing thread: fill(walk, task) sets task.x. Returns false where a wait ran out; *join
+// then says that there is nothing to join, whatever an earlier call left there.
 template <typename Cut, typename Fill>
 __device__ __forceinline__ bool chunk_hand_out(ChunkTasks& r, const ChunkDims& c,
                                                const ChunkStart& start, ChunkJoin* join,
                                                Fill fill) {
   ChunkWalk<Cut> w(c, start);
   ChunkJoin jn{0, 0, 0, 0};
+  *join = jn;
   for (uint32_t i = 0;; ++i) {
     const int slot = i % kTaskRing;
     if (!mbar_wait(&r.empty[slot], ((i / kTaskRing) & 1) ^ 1)) return false;
@@ -329,5 +331,19 @@ struct ChunkReader {
     return t.b >= 0;
   }
 };
+
+// The joining kernels: the join that CTA blockIdx.x of the kernel before left, if there is one
+// to follow, and its request. A wait that ran out in any CTA may have left partials of an
+// earlier call: then nothing is joined.
+template <typename Cut>
+__device__ __forceinline__ bool chunk_join(const ChunkDims& c, const ChunkJoin* joins,
+                                           const uint32_t* err, ChunkJoin& jn, ChunkRequest& r) {
+  const uint32_t bits = *err;
+  jn = joins[blockIdx.x];
+  if (!chunk_join_valid(jn, c.B, c.Hkv, blockIdx.x, gridDim.x) || (bits & ASP_DEVERR_TIMEOUT))
+    return false;
+  r = chunk_request(c, jn.b, nullptr);
+  return jn.item < Cut::items(r, c.lg);
+}
 
 }  // namespace asp

@@ -416,9 +416,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(kItemKeys) weights_join_kernel(const ChunkParams p) {
   pdl_launch_dependents();
   pdl_wait_predecessor();
-  const ChunkJoin jn = p.joins[blockIdx.x];
-  if (jn.pieces < 2) return;
-  const ChunkRequest r = chunk_request(p.c, jn.b, nullptr);
+  ChunkJoin jn;
+  ChunkRequest r;
+  if (!chunk_join<KeyCut>(p.c, p.joins, p.err, jn, r)) return;
   const int row = threadIdx.x, slot = jn.item * kItemKeys + row;
   if (slot >= r.T) return;
   float sum = p.partials[(size_t)(2 * blockIdx.x + 1) * kItemKeys + row];

@@ -69,7 +69,8 @@ typedef enum asp_status {
 #define ASP_DEVERR_LIST_RANGE 0x2u /* lists entry outside [0, N_b): page skipped */
 #define ASP_DEVERR_LEN_RANGE 0x4u  /* lens[b,h] outside [0, N_b]: clamped */
 #define ASP_DEVERR_SEQ_RANGE 0x8u  /* seq_lens[b] outside [0, max_pages*P]: clamped */
-#define ASP_DEVERR_TIMEOUT 0x10u   /* a bounded on-chip wait ran out: the kernel stopped early */
+#define ASP_DEVERR_TIMEOUT 0x10u   /* a bounded on-chip wait ran out: the kernel stopped early. While it is
+                                      set the chunk calls leave unwritten what several thread blocks share */
 #define ASP_DEVERR_OFFSET_RANGE 0x20u /* q_offsets not ascending in [0, num_tokens], or more new rows than seq_lens: request skipped */
 
 /* A cudaStream_t, passed as an opaque pointer. NULL is the legacy default stream. */
