@@ -70,7 +70,8 @@ class DecodeStep:
         return len(self.kvs) * (per + 1 + (1 if self.append is not None else 0) +
                                 (2 if self.weights is not None else 0))
 
-    def run_layer(self, l: int, stream=None, events=None):
+    def run_layer(self, l: int, stream=None, events=None, w_out=None):
+        """w_out: where layer l's weights go instead of back to where they come from."""
         kv = self.kvs[l]
         if self.append is not None:
             B.asp_page_summarize(kv, B.ASP_SUMMARIZE_APPEND, self.append[0][l], self.append[1][l],
@@ -87,19 +88,24 @@ class DecodeStep:
             events[2].record(stream)
         if self.weights is not None:
             B.asp_decode_weights(kv, self.q[l], self.lists[l], self.lens[l], self.lse[l],
-                                 self.sm_scale, self.decay, self.weights[l], self.weights[l],
-                                 self.ws, stream)
+                                 self.sm_scale, self.decay, self.weights[l],
+                                 self.weights[l] if w_out is None else w_out, self.ws, stream)
 
     def run(self, stream=None):
         for l in range(len(self.kvs)):
             self.run_layer(l, stream)
 
     def capture(self):
-        """Captures one full step into a CUDA graph (warm up first)."""
+        """Captures one full step into a CUDA graph, after a warm-up step of its own that leaves
+        `weights` as they are."""
         s = torch.cuda.Stream(device=self.kvs[0].device)
         s.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(s):
-            self.run()  # warm-up outside capture: sets kernel attributes, loads modules
+            # warm-up outside capture: sets kernel attributes, loads modules. A step adds to its
+            # weights, so this one's go into a layer's worth of scratch.
+            scratch = None if self.weights is None else torch.empty_like(self.weights[0])
+            for l in range(len(self.kvs)):
+                self.run_layer(l, w_out=scratch)
         torch.cuda.current_stream().wait_stream(s)
         torch.cuda.synchronize()
         g = torch.cuda.CUDAGraph()
@@ -261,7 +267,9 @@ class ChunkStep:
             self.run_layer(l, stream)
 
     def capture(self):
-        """Captures the step into a CUDA graph (call `run` once before: it loads the kernels)."""
+        """Captures the step into a CUDA graph (call `run` once before: it loads the kernels).
+        That run is a step like any other: it adds the chunk's part to `weights`, and a replay
+        adds again."""
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             self.run()

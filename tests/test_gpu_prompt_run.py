@@ -245,3 +245,38 @@ def test_shape_checks(cuda_device):
     with pytest.raises(TypeError):
         B.asp_norm_rotate_append(kvs[0], good[0], offs, None, None, None, 1e-6, None, False,
                                  q.half(), ws)
+
+
+@pytest.mark.parametrize("decay", [1.0, 0.5])
+def test_capture_leaves_the_weights_alone(cuda_device, decay):
+    """capture() and one replay give what one run() gives, the weights among it."""
+    dev = cuda_device
+    model = Model(dev, [160, 100], seed=5)
+    lens = [150, 77]
+    for l in range(L):
+        model.k[l].copy_(torch.randn(model.k[l].shape, generator=model.gen))
+        model.v[l].copy_(torch.randn(model.v[l].shape, generator=model.gen))
+    kvs = model.kvs(lens)
+    q = torch.randn((L, 2, Hq, d), generator=model.gen).to(dev)
+    new = torch.randn((2, L, 2, Hkv, d), generator=model.gen).to(torch.bfloat16).to(dev)
+    ws = B.new_workspace(kvs[0])
+    for kv in kvs:
+        B.asp_page_summarize(kv, B.ASP_SUMMARIZE_BULK, None, None, ws)
+    start = torch.rand((L,) + tuple(B.weights_shape(kvs[0])), generator=model.gen).to(dev)
+    for b, t in enumerate(lens):
+        start[:, b, :, t:] = math.nan  # not read
+    weights = guards.guarded_like(start, "weights")
+    step = DecodeStep(kvs, q, 0.9, append=(new[0], new[1]), weights=weights, decay=decay)
+    step.run()
+    want = weights.clone()
+    step.run()
+    twice = weights.clone()
+    weights.copy_(start)
+    step.capture()
+    torch.cuda.synchronize()
+    assert torch.equal(weights.view(torch.int32), start.view(torch.int32)), "capture changed the weights"
+    for once in (want, twice):
+        step.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(weights.view(torch.int32), once.view(torch.int32))
+    assert B.asp_get_device_error(step.ws) == 0
