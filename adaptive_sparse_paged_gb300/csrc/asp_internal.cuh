@@ -129,25 +129,26 @@ __device__ __forceinline__ int clamp_seq_len(int T, int max_pages, int P, uint32
 // Request b's rows of a packed batch of new tokens: [row0, row0 + n), the last
 // n of its T cached tokens. q_offsets null: one row per request. Offsets that
 // do not ascend within [0, num_tokens], or that give more rows than T, set
-// ASP_DEVERR_OFFSET_RANGE and leave the request without rows.
+// ASP_DEVERR_OFFSET_RANGE and leave the request without rows, `bad` set: it is skipped.
 struct NewRows {
   int row0, n;
+  bool bad;
 };
 __device__ __forceinline__ NewRows new_rows(const int32_t* q_offsets, int b, int T, int num_tokens,
                                             uint32_t* err) {
-  NewRows r{b, 1};
+  NewRows r{b, 1, false};
   if (q_offsets) {
     r.row0 = q_offsets[b];
     const int end = q_offsets[b + 1];
     r.n = end - r.row0;
     if (r.row0 < 0 || end < r.row0 || end > num_tokens) {
       report(err, ASP_DEVERR_OFFSET_RANGE);
-      return NewRows{0, 0};
+      return NewRows{0, 0, true};
     }
   }
   if (r.n > T) {
     if (q_offsets) report(err, ASP_DEVERR_OFFSET_RANGE);  // an empty request has no row to skip
-    return NewRows{0, 0};
+    return NewRows{0, 0, q_offsets != nullptr};
   }
   return r;
 }

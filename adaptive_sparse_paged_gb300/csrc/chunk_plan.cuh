@@ -28,14 +28,15 @@ struct ChunkDims {
   unsigned long long inv_ctas;  // chunk_inverse of the grid
 };
 
-// One request: its tokens, and its rows.
+// One request: its tokens, and its rows. One that is skipped has no tokens either, so that no
+// cut has items of it.
 struct ChunkRequest {
   int T, n, row0;
 };
 __device__ __forceinline__ ChunkRequest chunk_request(const ChunkDims& c, int b, uint32_t* err) {
   const int T = clamp_seq_len(c.seq_lens[b], c.max_pages, c.P, err);
   const NewRows r = new_rows(c.q_offsets, b, T, c.num_tokens, err);
-  return ChunkRequest{T, r.n, r.row0};
+  return ChunkRequest{r.bad ? 0 : T, r.n, r.row0};
 }
 
 // lg: log2 of the group. The plan divides by shifts: it stands before all other work of a

@@ -273,7 +273,8 @@ asp_status asp_sparse_decode(const asp_paged_kv* kv, const float* q,
  * outside [q_offsets[0], q_offsets[batch]) are neither read nor written.
  * Offsets that do not ascend within [0, num_tokens], or that give a request
  * more rows than seq_lens[b], set ASP_DEVERR_OFFSET_RANGE: that request is
- * skipped, and others of the call may be. num_tokens may be 0; at most ASP_MAX_NEW_TOKENS.
+ * skipped (nothing of it is written, its weights neither), and others of the
+ * call may be. num_tokens may be 0; at most ASP_MAX_NEW_TOKENS.
  * ------------------------------------------------------------------------
  */
 #define ASP_MAX_NEW_TOKENS (1 << 22)

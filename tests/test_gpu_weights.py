@@ -131,6 +131,47 @@ def test_chunk_more_requests_than_threads(cuda_device):
     check(batch, w, want, tol)
 
 
+@pytest.mark.parametrize("offs,skipped", [([0, 41, 61], [0, 1]), ([0, 30, 20], [1]),
+                                          ([-1, 40, 60], [0]), ([0, 40, 62], [1])])
+def test_chunk_a_request_with_bad_offsets_is_skipped(cuda_device, offs, skipped):
+    """In place: its weights neither decay nor change, its entries of new tokens are not read."""
+    batch = R.Batch(cuda_device, [40, 20], [40, 20], 8, 2, 64, 16, seed=9)
+    kv = batch.to_device()
+    lse = torch.zeros((batch.N, 8), device=cuda_device)
+    w = guards.guarded((2, 2, batch.max_pages * 16), torch.float32, cuda_device, fill=FILL)
+    batch.offs_dev.copy_(torch.tensor(offs, dtype=torch.int32))
+    B.asp_chunk_weights(kv, batch.q.to(cuda_device), batch.offs_dev, lse, batch.scale, 0.5, w, w,
+                        batch.ws)
+    assert B.asp_get_device_error(batch.ws) == B.ASP_DEVERR_OFFSET_RANGE
+    for b in skipped:
+        assert bool((w[b] == FILL).all()), b
+
+
+def test_chunk_skipped_requests_among_many(cuda_device):
+    """Requests with more rows than tokens: the others' weights are what they are without them."""
+    tokens = [1 + (i * 37) % 600 for i in range(60)]
+    news = [min(t, 1 + (i * 29) % 90) for i, t in enumerate(tokens)]
+    batch = R.Batch(cuda_device, tokens, news, 4, 2, 64, 16, seed=19)
+    kv = batch.to_device()
+    bad = list(range(0, 60, 7))
+    lens = torch.tensor(tokens, dtype=torch.int32)
+    for b in bad:
+        lens[b] = news[b] - 1
+    batch.lens_dev.copy_(lens)
+    lse = lse_of(batch, batch.q)
+    start = torch.rand((batch.B, 2, batch.max_pages * 16), generator=batch.gen)
+    want, tol = R.chunk_weights(batch, batch.q, lse, 0.5, start)
+    w = guards.guarded(start.shape, torch.float32, cuda_device, fill=FILL)
+    B.asp_chunk_weights(kv, batch.q.to(cuda_device), batch.offs_dev, lse.to(cuda_device),
+                        batch.scale, 0.5, start.to(cuda_device), w, batch.ws)
+    assert B.asp_get_device_error(batch.ws) == B.ASP_DEVERR_OFFSET_RANGE
+    for b, t in enumerate(tokens):
+        if b in bad:
+            assert bool((w[b] == FILL).all()), b
+        else:
+            R.close(w[b, :, :t].cpu(), want[b, :, :t], tol[b, :, :t], "weights")
+
+
 # ------------------------------------------------------------------ decode form
 def decode_case(dev, tokens, Hq, Hkv, d, P, share, seed):
     news = [min(1, t) for t in tokens]
