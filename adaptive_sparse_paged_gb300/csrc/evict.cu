@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
   const float* w = p.weights + (size_t)seg * p.max_pages * P;  // 16-byte aligned: P % 16 == 0
   float* wo = p.w_out + (size_t)seg * p.max_pages * P;
   int32_t* kept = p.kept + (size_t)seg * p.keep;
-  if (seg % p.Hkv == 0 && rank == 0 && tid == 0) p.new_lens[b] = min(T, p.keep);
+  const bool tells = seg % p.Hkv == 0 && rank == 0 && tid == 0;  // the request's new length
   if (p.src_table != p.dst_table) {
     // a copy of the source table would be in place without its order: not done
     const size_t at = (size_t)b * p.max_pages;
@@ -107,10 +107,12 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
       same |= p.dst_table[at + q] == p.src_table[at + q] && p.dst_table[at + q] >= 0;
     if (__syncthreads_or(same)) {
       if (tid == 0) report(p.err, ASP_DEVERR_PAGE_RANGE);
+      if (tells) p.new_lens[b] = T;  // nothing moved: it is as long as it was
       for (int i = tid; i < n; i += kSelThreads) kept[i] = -1;
       return;
     }
   }
+  if (tells) p.new_lens[b] = min(T, p.keep);
   if (T <= p.keep) {
     for (int i = rank * kSelThreads + tid; i < T; i += C * kSelThreads) {
       kept[i] = i;

@@ -162,6 +162,29 @@ def test_a_copy_of_the_table_is_refused(cuda_device):
     assert bool((batch.summ_dev == 3.0).all()) and bool((kept == -1).all())
 
 
+def test_a_refused_request_keeps_its_length(cuda_device):
+    """One request's table is a copy, the other's pages are its own: the first stays as long as
+    it was, the second is cut."""
+    batch = R.Batch(cuda_device, [200, 150], [0, 0], 2, 2, 64, 16, seed=12)
+    for name in ("k", "v"):
+        c = getattr(batch, name)
+        setattr(batch, name, torch.cat([c, torch.zeros((7, 2, 16, 64), dtype=torch.bfloat16)]))
+    dst = batch.table.clone()
+    dst[1, :7] = torch.arange(batch.n_phys, batch.n_phys + 7)
+    batch.n_phys += 7
+    kv = batch.to_device()
+    w = torch.rand((2, 2, batch.max_pages * 16), generator=batch.gen)
+    w_dev = w.to(cuda_device)
+    kept = torch.zeros((2, 2, 100), dtype=torch.int32, device=cuda_device)
+    lens = torch.zeros(2, dtype=torch.int32, device=cuda_device)
+    B.asp_weight_evict(kv, w_dev, 100, 10, dst.to(cuda_device), w_dev, kept, lens, batch.ws)
+    assert B.asp_get_device_error(batch.ws) == B.ASP_DEVERR_PAGE_RANGE
+    assert lens.tolist() == [200, 100]
+    assert bool((kept[0] == -1).all()) and torch.equal(w_dev[0].cpu(), w[0])
+    for h in range(2):
+        assert kept[1, h].tolist() == R.evict_ids(w[1, h], 150, 100, 10)
+
+
 def test_graph_replay(cuda_device):
     """Into other pages the call can be repeated: a graph of it, replayed, leaves the same."""
     batch = R.Batch(cuda_device, [500, 300], [0, 0], 2, 2, 64, 16, seed=7, max_pages=64)
