@@ -78,11 +78,51 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, 
   return __shfl_sync(kFull, z - w, warp) + y - x;
 }
 
+constexpr int kLogPageSlots = 13;  // of the set of pages below: it takes the place of the bins
+
+// Whether any page of `dst` is one of `src`'s; entries that are no page at all do not count. The
+// whole CTA asks. The pages of `src` go into a set in shared memory, at most half as many at a
+// time as it has slots, so that a free slot always ends a search.
+__device__ __forceinline__ bool share_pages(const int32_t* src, int n_src, const int32_t* dst,
+                                            int n_dst, int num_phys, int* set) {
+  constexpr int kSlots = 1 << kLogPageSlots, kRound = kSlots / 2;
+  auto slot_of = [](int page) { return (int)(page * 2654435769u >> (32 - kLogPageSlots)); };
+  int shared = 0;
+  for (int r0 = 0; r0 < n_src; r0 += kRound) {
+    for (int i = threadIdx.x; i < kSlots; i += kSelThreads) set[i] = -1;
+    __syncthreads();
+    const int r1 = min(n_src, r0 + kRound);
+    for (int i = r0 + threadIdx.x; i < r1; i += kSelThreads) {
+      const int page = src[i];
+      if (page < 0 || page >= num_phys) continue;
+      int at = slot_of(page);
+      while (true) {
+        const int there = atomicCAS(&set[at], -1, page);
+        if (there == -1 || there == page) break;
+        at = (at + 1) & (kSlots - 1);
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_dst; i += kSelThreads) {
+      const int page = dst[i];
+      if (page < 0 || page >= num_phys) continue;
+      for (int at = slot_of(page); set[at] != -1; at = (at + 1) & (kSlots - 1))
+        if (set[at] == page) {
+          shared = 1;
+          break;
+        }
+    }
+    __syncthreads();
+  }
+  return __syncthreads_or(shared);
+}
+
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params p, int P) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   __shared__ int hist[256 * 32];           // [bin][lane]
+  static_assert(256 * 32 == 1 << kLogPageSlots, "the set of pages lies there first");
   __shared__ int bins[2][256];             // this CTA's, read by the cluster; two passes' worth
   __shared__ int all_bins[256];
   __shared__ int counts[2];                // this CTA's slots above and equal
@@ -99,13 +139,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
   int32_t* kept = p.kept + (size_t)seg * p.keep;
   const bool tells = seg % p.Hkv == 0 && rank == 0 && tid == 0;  // the request's new length
   if (p.src_table != p.dst_table) {
-    // a copy of the source table would be in place without its order: not done
+    // pages of the request's own would be written before they are read: not done
     const size_t at = (size_t)b * p.max_pages;
     const int n = min(T, p.keep);
-    int same = 0;
-    for (int q = tid; q * P < n; q += kSelThreads)
-      same |= p.dst_table[at + q] == p.src_table[at + q] && p.dst_table[at + q] >= 0;
-    if (__syncthreads_or(same)) {
+    if (share_pages(p.src_table + at, ceil_div(T, P), p.dst_table + at, ceil_div(n, P), p.num_phys,
+                    hist)) {
       if (tid == 0) report(p.err, ASP_DEVERR_PAGE_RANGE);
       if (tells) p.new_lens[b] = T;  // nothing moved: it is as long as it was
       for (int i = tid; i < n; i += kSelThreads) kept[i] = -1;

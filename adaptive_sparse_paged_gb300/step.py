@@ -286,7 +286,9 @@ def evict(kvs, weights, keep: int, recent: int, ws, dst_table=None, stream=None)
     weights: fp32 [L, B, Hkv, max_pages * P], moved along in place; dst_table: int32
     [B, max_pages] of pages that the caches' table does not use, or None: in place. Returns
     (kept int32 [L, B, Hkv, keep], new_lens int32 [B]): the caller then goes on with
-    new_lens as seq_lens and, where one was given, dst_table as the block table."""
+    new_lens as seq_lens and, where one was given, dst_table as the block table. A request
+    for which dst_table names pages of its own stays as it is: its kept is -1, new_lens has
+    its old length, and the workspace's error word says so."""
     kvs = list(kvs)
     if not kvs:
         raise ValueError("kvs must hold at least one layer")

@@ -396,9 +396,10 @@ asp_status asp_decode_weights(const asp_paged_kv* kv, const float* q, const int3
  * kept      : int32 [B, Hkv, keep] out; entries from n on are untouched.
  * new_lens  : int32 [B] out; not the seq_lens buffer.
  * An out-of-range entry of either table sets ASP_DEVERR_PAGE_RANGE; the rows it
- * holds are not moved. In place is asked for by the pointer: another buffer with
- * block_table's own pages in their places sets the same bit, moves nothing,
- * leaves kept at -1 and new_lens[b] at T_b.
+ * holds are not moved. In place is asked for by the pointer: for a request whose
+ * entries in another buffer name any of the pages that hold its own tokens, in
+ * whatever order, the call sets the same bit, moves nothing, leaves kept at -1
+ * and new_lens[b] at T_b. Pages of other requests are not looked for.
  */
 asp_status asp_weight_evict(const asp_paged_kv* kv, const float* weights, int32_t keep,
                             int32_t recent, const int32_t* dst_table, float* w_out, int32_t* kept,

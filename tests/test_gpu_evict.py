@@ -185,6 +185,64 @@ def test_a_refused_request_keeps_its_length(cuda_device):
         assert kept[1, h].tolist() == R.evict_ids(w[1, h], 150, 100, 10)
 
 
+@pytest.mark.parametrize("kind", ["shifted", "reversed", "last of one", "last of many", "none"])
+@pytest.mark.parametrize("P", [16, 64])
+def test_a_table_with_pages_of_its_own_is_refused(cuda_device, kind, P):
+    """Any page of the request's own, wherever it stands, and however many pages there are."""
+    T, keep = (5000 * P - 3, 9 * P) if kind == "last of many" else (40 * P, 20 * P - 1)
+    batch = R.Batch(cuda_device, [1], [0], 1, 1, 64, P, seed=13, max_pages=-(-T // P))
+    n_pages, n_new = -(-T // P), -(-keep // P)
+    n_phys = n_pages + n_new + 1
+    perm = torch.randperm(n_phys, generator=batch.gen).to(torch.int32)
+    batch.table = perm[:n_pages][None].contiguous()
+    own, dst = batch.table[0], torch.full_like(batch.table, -1)
+    dst[0, :n_new] = perm[n_pages:n_pages + n_new]
+    if kind == "shifted":
+        dst[0, :n_new] = own[-n_new:]
+    elif kind == "reversed":
+        dst[0, :n_new] = own[:n_new].flip(0)
+    elif kind != "none":
+        dst[0, n_new - 1] = own[-1]
+    batch.tokens, batch.n_phys = [T], n_phys
+    gen = torch.Generator(device=cuda_device).manual_seed(3)
+    k = torch.randn((n_phys, 1, P, 64), generator=gen, device=cuda_device).to(torch.bfloat16)
+    batch.k, batch.v = k, k + 1
+    batch.to_device()
+    batch.summ_dev.fill_(3.0)
+    w = torch.rand((1, 1, n_pages * P), generator=gen, device=cuda_device)
+    w_out = torch.full_like(w, 5.0)
+    kept = torch.zeros((1, 1, keep), dtype=torch.int32, device=cuda_device)
+    lens = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    B.asp_weight_evict(batch.kv, w, keep, 10, dst.to(cuda_device), w_out, kept, lens, batch.ws)
+    if kind == "none":
+        assert B.asp_get_device_error(batch.ws) == 0 and lens.tolist() == [keep]
+        assert kept[0, 0].tolist() == R.evict_ids(w[0, 0].cpu(), T, keep, 10)
+        return
+    assert B.asp_get_device_error(batch.ws) == B.ASP_DEVERR_PAGE_RANGE
+    assert lens.tolist() == [T] and bool((kept == -1).all()) and bool((w_out == 5.0).all())
+    assert torch.equal(batch.k_dev, k) and torch.equal(batch.v_dev, k + 1)
+    assert bool((batch.summ_dev == 3.0).all())
+
+
+def test_entries_that_are_no_pages_are_not_shared(cuda_device):
+    """The same bad entry in both tables is a bad page, not one of the request's own."""
+    batch = R.Batch(cuda_device, [200], [0], 2, 2, 64, 16, seed=14)
+    for name in ("k", "v"):
+        c = getattr(batch, name)
+        setattr(batch, name, torch.cat([c, torch.zeros((7, 2, 16, 64), dtype=torch.bfloat16)]))
+    dst = torch.full_like(batch.table, -1)
+    dst[0, :7] = torch.arange(batch.n_phys, batch.n_phys + 7)
+    batch.n_phys += 7
+    batch.table[0, 2] = dst[0, 2] = 1 << 30
+    kv = batch.to_device()
+    w = torch.rand((1, 2, batch.max_pages * 16), device=cuda_device)
+    kept = torch.zeros((1, 2, 100), dtype=torch.int32, device=cuda_device)
+    lens = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    B.asp_weight_evict(kv, w, 100, 100, dst.to(cuda_device), w, kept, lens, batch.ws)
+    assert B.asp_get_device_error(batch.ws) == B.ASP_DEVERR_PAGE_RANGE
+    assert lens.tolist() == [100] and kept[0, 0].tolist() == list(range(100, 200))
+
+
 def test_graph_replay(cuda_device):
     """Into other pages the call can be repeated: a graph of it, replayed, leaves the same."""
     batch = R.Batch(cuda_device, [500, 300], [0, 0], 2, 2, 64, 16, seed=7, max_pages=64)
