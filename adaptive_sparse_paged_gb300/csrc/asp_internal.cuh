@@ -312,6 +312,9 @@ __device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
                              *reinterpret_cast<__nv_bfloat162*>(&b));
   return *reinterpret_cast<uint32_t*>(&r);
 }
+// Two bf16 NaN: what a fold starts from, as the other operand of bmin2 and bmax2 then wins, and
+// what a channel that held nothing else ends as (minimum and maximum, like a bulk summary's).
+constexpr uint32_t kNanPair = 0x7fff7fffu;
 __device__ __forceinline__ uint2 vmin(uint2 a, uint2 b) {
   return make_uint2(bmin2(a.x, b.x), bmin2(a.y, b.y));
 }

@@ -345,6 +345,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const Params p
   constexpr int kTile = kMoveThreads / 32 * kWarpRows;
   constexpr int kIdx = (kWarpRows + 31) / 32;          // rows whose places a lane looks up
   __shared__ uint2 s_mn[P > kGroup ? kMoveThreads : 1], s_mx[P > kGroup ? kMoveThreads : 1];
+  __shared__ uint32_t s_have[P > kGroup ? kMoveThreads : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int seg = blockIdx.x, b = seg / p.Hkv, h = seg % p.Hkv;
   const bool is_k = (blockIdx.y & 1) == 0;
@@ -415,9 +416,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const Params p
         have |= 1u << u;
       }
     if (!is_k) continue;
-    const uint2 inf = make_uint2(0x7f807f80u, 0x7f807f80u);  // folding starts from +-infinity
-    const uint2 neg_inf = make_uint2(0xff80ff80u, 0xff80ff80u);
-    uint2 mn = inf, mx = neg_inf;
+    uint2 mn = make_uint2(kNanPair, kNanPair), mx = mn;
 #pragma unroll
     for (int u = 0; u < kGroup; ++u)
       if (have >> u & 1) {
@@ -429,18 +428,19 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const Params p
       // a page is P / 16 groups in a row: neighbouring lane groups, then warps
       s_mn[tid] = mn;
       s_mx[tid] = mx;
+      s_have[tid] = have;
       __syncthreads();
       if (first % P == 0) {
 #pragma unroll
         for (int k = 1; k < P / kGroup; ++k) {
           mn = vmin(mn, s_mn[tid + k * kLanes]);
           mx = vmax(mx, s_mx[tid + k * kLanes]);
+          have |= s_have[tid + k * kLanes];
         }
       }
       __syncthreads();
     }
-    const bool none = mn.x == inf.x && mn.y == inf.y && mx.x == neg_inf.x && mx.y == neg_inf.y;
-    if (first % P == 0 && first < n && !none) {  // none: no row of the page was moved
+    if (first % P == 0 && first < n && have) {  // 0: no row of the page was moved
       uint16_t* s = p.summ + ((size_t)seg * p.max_pages + first / P) * 2 * D + c0;
       *reinterpret_cast<uint2*>(s) = mn;
       *reinterpret_cast<uint2*>(s + D) = mx;

@@ -243,6 +243,58 @@ def test_entries_that_are_no_pages_are_not_shared(cuda_device):
     assert lens.tolist() == [100] and kept[0, 0].tolist() == list(range(100, 200))
 
 
+@pytest.mark.parametrize("d,P", [(64, 16), (128, 16), (128, 64)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_summaries_of_nan_keys(cuda_device, d, P, in_place):
+    """Channels that hold NaN in some rows of a page, or in all: as a bulk summary of them."""
+    t, keep = 6 * P, 4 * P - 3
+    n_new = -(-keep // P)
+    batch = R.Batch(cuda_device, [t], [0], 2, 2, d, P, seed=10)
+    rows = batch.rows(batch.k, 0).clone()
+    rows[:, :, 4:8] = math.nan
+    rows[::2, :, 20] = math.nan
+    rows[:, 1, 60] = math.nan
+    batch.put(batch.k, 0, rows)
+    for name in ("k", "v"):
+        c = getattr(batch, name)
+        setattr(batch, name, torch.cat([c, torch.zeros((n_new, 2, P, d), dtype=torch.bfloat16)]))
+    dst = torch.full((1, batch.max_pages), -1, dtype=torch.int32)
+    dst[0, :n_new] = torch.arange(batch.n_phys, batch.n_phys + n_new)
+    batch.n_phys += n_new
+    kv = batch.to_device()
+    batch.summ_dev.fill_(3.0)
+    w = torch.rand((1, 2, batch.max_pages * P), generator=batch.gen).to(cuda_device)
+    kept = torch.zeros((1, 2, keep), dtype=torch.int32, device=cuda_device)
+    lens = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    table = batch.table_dev if in_place else dst.to(cuda_device)
+    B.asp_weight_evict(kv, w, keep, 5, table, w, kept, lens, batch.ws)
+    got = batch.summ_dev.clone()
+    after = B.PagedKV(batch.k_dev, batch.v_dev, batch.summ_dev, table, lens, 2)
+    B.asp_page_summarize(after, B.ASP_SUMMARIZE_BULK, None, None, batch.ws)
+    assert B.asp_get_device_error(batch.ws) == 0
+    assert torch.equal(torch.isnan(got), torch.isnan(batch.summ_dev))
+    assert torch.equal(got.nan_to_num(0.5), batch.summ_dev.nan_to_num(0.5))
+
+
+@pytest.mark.parametrize("P", [16, 64])
+def test_a_page_without_rows_keeps_its_summary(cuda_device, P):
+    """Every row of it lay in pages that are not there: nothing moved, nothing is said of it."""
+    batch = R.Batch(cuda_device, [3 * P], [0], 2, 2, 64, P, seed=15)
+    batch.table[0, 1] = -1
+    kv = batch.to_device()
+    batch.summ_dev.fill_(3.0)
+    w = torch.rand((1, 2, batch.max_pages * P), device=cuda_device)
+    kept = torch.zeros((1, 2, 3 * P), dtype=torch.int32, device=cuda_device)
+    lens = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    B.asp_weight_evict(kv, w, 3 * P, 0, batch.table_dev, w, kept, lens, batch.ws)
+    assert B.asp_get_device_error(batch.ws) == B.ASP_DEVERR_PAGE_RANGE
+    assert bool((batch.summ_dev[:, :, 1] == 3.0).all())
+    for p in (0, 2):
+        part = batch.k[int(batch.table[0, p])].float()
+        assert torch.equal(batch.summ_dev[0, :, p, 0].float().cpu(), part.amin(1))
+        assert torch.equal(batch.summ_dev[0, :, p, 1].float().cpu(), part.amax(1))
+
+
 def test_graph_replay(cuda_device):
     """Into other pages the call can be repeated: a graph of it, replayed, leaves the same."""
     batch = R.Batch(cuda_device, [500, 300], [0, 0], 2, 2, 64, 16, seed=7, max_pages=64)
