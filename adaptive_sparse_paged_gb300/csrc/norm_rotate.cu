@@ -281,10 +281,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_rotate_kernel(const Para
     if (it.b < 0) break;
     const bool mapped = it.phys >= 0;
     const size_t k_block = mapped ? ((size_t)it.phys * p.Hkv + k0) * P : 0;
-    // folding starts from values that any key replaces
-    constexpr uint32_t kInf = 0x7f807f80u, kNegInf = 0xff80ff80u;
-    uint2 mn[2] = {make_uint2(kInf, kInf), make_uint2(kInf, kInf)};
-    uint2 mx[2] = {make_uint2(kNegInf, kNegInf), make_uint2(kNegInf, kNegInf)};
+    const uint2 start = make_uint2(kNanPair, kNanPair);  // any key replaces it
+    uint2 mn[2] = {start, start}, mx[2] = {start, start};
     for (int t = 0; t < it.cnt; ++t, ++tk) {
       const float2* turn = sh.turn[(blk - 1) & 1];
       if (t % kTurnTokens == 0) {

@@ -160,3 +160,24 @@ def test_bad_page_and_offsets(cuda_device):
         batch.offs_dev.copy_(torch.tensor(offs, dtype=torch.int32))
         B.asp_norm_rotate_append(*args)
         assert B.asp_get_device_error(batch.ws) & B.ASP_DEVERR_OFFSET_RANGE
+
+
+@pytest.mark.parametrize("tokens,new", [(1, 1), (40, 40), (37, 5), (33, 1)])
+def test_summaries_of_nan_keys(cuda_device, tokens, new):
+    """NaN in all keys of a page, or in its only one: as a bulk summary of them."""
+    batch = R.Batch(cuda_device, [tokens], [new], 8, 2, 64, 16, seed=3)
+    kv = batch.to_device()
+    old = torch.tensor([tokens - new], dtype=torch.int32, device=cuda_device)
+    before = B.PagedKV(batch.k_dev, batch.v_dev, batch.summ_dev, batch.table_dev, old, 8)
+    B.asp_page_summarize(before, B.ASP_SUMMARIZE_BULK, None, None, batch.ws)
+    qkv = torch.randn((new, 12, 64), generator=batch.gen).to(torch.bfloat16)
+    qkv[:, 8:10, 12:17] = math.nan
+    qkv[-1, 9] = math.nan
+    q_out = torch.zeros((new, 8, 64), dtype=torch.bfloat16, device=cuda_device)
+    B.asp_norm_rotate_append(kv, qkv.to(cuda_device), batch.offs_dev, None, None, None, 1e-6, None,
+                             False, q_out, batch.ws)
+    got = batch.summ_dev.clone()
+    B.asp_page_summarize(kv, B.ASP_SUMMARIZE_BULK, None, None, batch.ws)
+    assert B.asp_get_device_error(batch.ws) == 0
+    assert torch.equal(torch.isnan(got), torch.isnan(batch.summ_dev))
+    assert torch.equal(got.nan_to_num(0.5), batch.summ_dev.nan_to_num(0.5))
