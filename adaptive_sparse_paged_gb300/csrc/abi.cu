@@ -40,12 +40,15 @@ asp_status check_kv(const asp_paged_kv* kv) {
   return ASP_OK;
 }
 
-asp_status check_ws(const asp_paged_kv* kv, void* ws, size_t ws_bytes, WsLayout* lay) {
+// chunk: the call needs the joins and partials at the workspace's end, which only the chunk
+// calls do; a workspace that ends before them serves all others.
+asp_status check_ws(const asp_paged_kv* kv, void* ws, size_t ws_bytes, WsLayout* lay,
+                    bool chunk = false) {
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return ASP_EWORKSPACE;
   const int sms = current_device_sm_count();
   if (sms <= 0) return ASP_ECUDA;
   *lay = ws_layout(*kv, sms);
-  if (ws_bytes < lay->total) return ASP_EWORKSPACE;
+  if (ws_bytes < (chunk ? lay->total : lay->joins_off)) return ASP_EWORKSPACE;
   return ASP_OK;
 }
 
@@ -307,7 +310,7 @@ asp_status asp_chunk_attention(const asp_paged_kv* kv, const uint16_t* q,
   if (!q_offsets || !out || !lse || misaligned(out, 16)) return ASP_EINVAL;
   if (!(sm_scale > 0.0f) || !std::isfinite(sm_scale)) return ASP_EINVAL;
   WsLayout lay;
-  if ((st = check_ws(kv, ws, ws_bytes, &lay)) != ASP_OK) return st;
+  if ((st = check_ws(kv, ws, ws_bytes, &lay, true)) != ASP_OK) return st;
   if (num_tokens == 0) return ASP_OK;
   uint8_t* w = static_cast<uint8_t*>(ws);
   ChunkAttentionArgs a{kv, q, q_offsets, num_tokens, sm_scale, out, lse,
@@ -328,7 +331,7 @@ asp_status asp_chunk_weights(const asp_paged_kv* kv, const uint16_t* q, const in
   if (!q_offsets || !lse || !w_out) return ASP_EINVAL;
   if ((st = check_weights(sm_scale, decay, w_in, w_out)) != ASP_OK) return st;
   WsLayout lay;
-  if ((st = check_ws(kv, ws, ws_bytes, &lay)) != ASP_OK) return st;
+  if ((st = check_ws(kv, ws, ws_bytes, &lay, true)) != ASP_OK) return st;
   uint8_t* w = static_cast<uint8_t*>(ws);
   WeightArgs a{kv, q, q_offsets, num_tokens, nullptr, nullptr, nullptr, lse, sm_scale, decay,
                w_in, w_out, reinterpret_cast<ChunkJoin*>(w + lay.joins_off),

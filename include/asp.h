@@ -122,8 +122,10 @@ const char* asp_status_string(asp_status status);
 /*
  * Workspace bytes needed by every call below that takes one, for this shape on
  * the CURRENT device (the grids are sized from its SM count; the partial results
- * of asp_chunk_attention are most of it, 41 MB on 152 SMs at head_dim 128).
- * Writes the size to *bytes. The workspace is a caller-owned device buffer,
+ * of the chunk calls are most of it, 41 MB on 152 SMs at head_dim 128, and lie
+ * at its end: only asp_chunk_attention and asp_chunk_weights ask for them, and a
+ * workspace of the size that a build without those calls gave still serves all
+ * others). Writes the size to *bytes. The workspace is a caller-owned device buffer,
  * 256-byte aligned, that must be zeroed once with asp_workspace_init before
  * first use. It holds the device error word,
  * per-call scratch (page scores, the decode's partial results) that every
