@@ -68,6 +68,10 @@ asp_status check_weights(float sm_scale, float decay, const float* w_in, const f
   return misaligned(w_in, 16) || misaligned(w_out, 16) ? ASP_EINVAL : ASP_OK;
 }
 
+// The chunk form subtracts lse / sm_scale from a product: with any lse under 2^27 that stays
+// below fp32's largest value from here on.
+constexpr float kMinChunkScale = 0x1p-100f;
+
 asp_status from_cuda(cudaError_t e) { return e == cudaSuccess ? ASP_OK : ASP_ECUDA; }
 
 // One warp; thread 0 waits on a barrier that expects one arrival which never
@@ -330,6 +334,7 @@ asp_status asp_chunk_weights(const asp_paged_kv* kv, const uint16_t* q, const in
   if ((st = check_rows(num_tokens, q)) != ASP_OK) return st;
   if (!q_offsets || !lse || !w_out) return ASP_EINVAL;
   if ((st = check_weights(sm_scale, decay, w_in, w_out)) != ASP_OK) return st;
+  if (sm_scale < kMinChunkScale) return ASP_EINVAL;
   WsLayout lay;
   if ((st = check_ws(kv, ws, ws_bytes, &lay, true)) != ASP_OK) return st;
   uint8_t* w = static_cast<uint8_t*>(ws);

@@ -345,6 +345,7 @@ asp_status asp_chunk_attention(const asp_paged_kv* kv, const uint16_t* q,
  * (s >= T_b - n_b) had no weight before: w_in is not read there. A row whose
  * lse is -inf adds nothing.
  * q, q_offsets : as asp_chunk_attention; lse as it wrote it.
+ * sm_scale : at least 2^-100 here (lse / sm_scale is formed in fp32).
  * decay : >= 0 and finite; 1 sums over all rows ever seen.
  * w_in, w_out : fp32 [B, Hkv, max_pages * P], 16-byte aligned. w_in may be NULL
  *               (nothing before) or the same buffer as w_out.
@@ -365,7 +366,7 @@ asp_status asp_chunk_weights(const asp_paged_kv* kv, const uint16_t* q, const in
  *        asp_sparse_decode wrote it over the same lists.
  * lists, lens : as written by asp_coverage_select; each page at most once in a
  *        list. Both NULL: every page.
- * Other arguments and conditions as for asp_chunk_weights.
+ * Other arguments and conditions as for asp_chunk_weights; any sm_scale > 0.
  */
 asp_status asp_decode_weights(const asp_paged_kv* kv, const float* q, const int32_t* lists,
                               const int32_t* lens, const float* lse, float sm_scale, float decay,

@@ -172,6 +172,29 @@ def test_chunk_skipped_requests_among_many(cuda_device):
             R.close(w[b, :, :t].cpu(), want[b, :, :t], tol[b, :, :t], "weights")
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** -40, 2.0 ** 20])
+def test_chunk_extreme_scales(cuda_device, scale):
+    """Logits that vanish, and logits whose softmax is one key's alone."""
+    batch = R.Batch(cuda_device, [300, 131], [70, 131], 8, 2, 64, 16, seed=23)
+    batch.scale = scale
+    if scale > 1:  # small whole numbers: products and sums are exact, and so is the scale
+        batch.q = torch.randint(-2, 3, batch.q.shape, generator=batch.gen).to(torch.bfloat16)
+        for b, t in enumerate(batch.tokens):
+            batch.put(batch.k, b, torch.randint(-2, 3, (t, 2, 64), generator=batch.gen).to(torch.bfloat16))
+    kv = batch.to_device()
+    lse = lse_of(batch, batch.q)
+    if scale > 1:  # a row's largest logit: exact, where the sum's logarithm is under its last bit
+        lse = torch.where(torch.isnan(lse), lse, (lse.double() / scale).round().mul(scale).float())
+    want, tol = R.chunk_weights(batch, batch.q, lse, 1.0, None)
+    if scale > 1:  # one for each key that has its row's largest logit, nothing for the others
+        tol = torch.zeros_like(tol)
+    w = guards.guarded((2, 2, batch.max_pages * 16), torch.float32, cuda_device, fill=FILL)
+    B.asp_chunk_weights(kv, batch.q.to(cuda_device), batch.offs_dev, lse.to(cuda_device), scale, 1.0,
+                        None, w, batch.ws)
+    assert B.asp_get_device_error(batch.ws) == 0
+    check(batch, w, want, tol)
+
+
 # ------------------------------------------------------------------ decode form
 def decode_case(dev, tokens, Hq, Hkv, d, P, share, seed):
     news = [min(1, t) for t in tokens]

@@ -99,3 +99,12 @@ def test_too_many_rows(lib):
     n = B.ASP_MAX_NEW_TOKENS + 1
     for call in (norm, attend, chunk):
         assert call(lib, kv(), n=n) == B.ASP_EUNSUPPORTED
+
+
+def test_a_scale_that_overflows_the_chunk_weights(lib):
+    """lse / sm_scale is formed in fp32: a scale that could make it infinite is refused."""
+    for scale in (2.0 ** -101, 1e-38, 1e-45):
+        assert chunk(lib, kv(), scale=scale) == B.ASP_EINVAL
+    # the smallest one passes this check and meets the next
+    assert chunk(lib, kv(), scale=2.0 ** -100, ws=None) == B.ASP_EWORKSPACE
+    assert decode(lib, kv(), scale=1e-38, ws=None) == B.ASP_EWORKSPACE
