@@ -17,8 +17,10 @@
 // walks its slots alone, so that the order needs no word between CTAs. Into other
 // pages there is no order to keep, and the slots are split over CTAs too.
 //
-// Measured: 8 requests of 18-32k tokens (8 KV heads, d = 128) cut to 16k in 206 us, 5.45 TB/s
-// over both kernels (selection about 20 us, the move 6.0 TB/s); 2k cut to 1k in 10.7 us.
+// Measured: 8 requests of 18-32k tokens (8 KV heads, d = 128) cut to 16k in 207 us, 5.4 TB/s
+// over both kernels (selection about 20 us, of which 1 us looks for pages that both tables have;
+// the move 6.0 TB/s); 2k cut to 1k in 11 us. In place the same takes 420 us, and one request
+// of 32k 126 us (53 us into other pages): too few CTAs walk the rows for the memory's latency.
 #include <cooperative_groups.h>
 
 #include "asp_internal.cuh"
@@ -472,9 +474,10 @@ cudaError_t launch_t(const EvictArgs& a, cudaStream_t stream) {
   const int segments = kv.batch * kv.num_kv_heads;
   cudaError_t e = set_max_dynamic_smem((const void*)evict_select_kernel, 0);
   if (e != cudaSuccess) return e;
-  // CTAs of a segment: as many as the GPU holds at once, with 8192 slots each at least. In
-  // place the whole segment has to be in registers (a CTA writes slots that another reads);
-  // what is too long for that is left to one CTA.
+  // CTAs of a segment: as many as the GPU holds at once, with more than 4096 slots each. With
+  // the weights in place the whole segment has to be in registers (a CTA writes slots that
+  // another reads); a table too long for that leaves the segment to one CTA. Both go by the
+  // table's capacity, which the host knows, not by the lengths, which it does not.
   const long long capacity = (long long)kv.max_pages * P;
   int C = 1;
   while (C < 8 && 2 * C * segments <= a.num_sms && capacity > 8192ll * C) C *= 2;

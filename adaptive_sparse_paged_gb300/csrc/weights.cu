@@ -14,13 +14,15 @@
 // query tiles' loads are what bounds the kernel (1030 cycles a tile of 128 x 128,
 // whatever the products and sums take). A warpgroup sums one key tile's rows; three
 // products are in tensor memory at once. The rows' lse is subtracted by the product
-// itself: read from shared memory for every element it cost as much as the products. An item that several CTAs share leaves its partial sums in the
-// workspace; a second, small kernel adds them up.
+// itself: read from shared memory for every element it cost as much as the products. An
+// item that several CTAs share leaves its partial sums in the workspace; a second, small
+// kernel adds them up.
 //
 // Measured: 2048 rows over 32768 tokens (32 query, 8 KV heads, d = 128) in 0.38 ms, 1.40
 // PFLOP/s; a product of 128 x 128 takes some 85 cycles a step where 64 are the tensor cores'
 // own, the port of tensor memory being shared with the sums' reads. 733 us with keys in
-// shared memory and the lse read an element at a time.
+// shared memory and the lse read an element at a time. At d = 64 as long (0.39 ms, 0.69
+// PFLOP/s): the exponentials are as many, their pipe is 59% busy, the tensor pipe 37%.
 //
 // Decode form (decode_weights_kernel): one token a request, fp32 queries, page
 // lists. The keys are read once and the kernel is bound by HBM, so the tiles of
