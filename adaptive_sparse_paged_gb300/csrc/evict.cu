@@ -17,8 +17,8 @@
 // walks its slots alone, so that the order needs no word between CTAs. Into other
 // pages there is no order to keep, and the slots are split over CTAs too.
 //
-// Measured: 8 requests of 18-32k tokens (8 KV heads, d = 128) cut to 16k in 207 us, 5.4 TB/s
-// over both kernels (selection about 20 us, of which 1 us looks for pages that both tables have;
+// Measured: 8 requests of 18-32k tokens (8 KV heads, d = 128) cut to 16k in 208 us, 5.4 TB/s
+// over both kernels (selection about 20 us, of which 1.5 us look for pages that both tables have;
 // the move 6.0 TB/s); 2k cut to 1k in 11 us. In place the same takes 420 us, and one request
 // of 32k 126 us (53 us into other pages): too few CTAs walk the rows for the memory's latency.
 #include <cooperative_groups.h>
