@@ -253,8 +253,8 @@ class QuantPagedKV(PagedKV):
                        two, then the values'
     summaries, block_table, seq_lens, num_q_heads : as in PagedKV
 
-    The asp_q8_ calls work on it, and those that read no K or V: selection, page scores,
-    the workspace. The others refuse it.
+    The asp_q8_ calls work on it, and those whose results need no K or V: selection (which
+    then moves no pages into L2 for the decode), page scores, the workspace. The others refuse it.
     """
 
     def __init__(self, k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor,

@@ -28,7 +28,8 @@
 //      ties kept (lowest ids first) and its own output offset;
 //   6. every CTA writes its kept ids in ascending order at its offset, and
 //      asks L2 for the K/V of its first kept pages: the decode that follows
-//      reads them, and HBM is idle until its first copies.
+//      reads them, and HBM is idle until its first copies (bf16 pages only: of an
+//      8-bit cache, which comes without them, it fetches nothing).
 //
 // All branches before a barrier depend only on values that are the same in
 // the whole cluster, so every thread of every CTA reaches every barrier. The
@@ -41,6 +42,7 @@
 #include <type_traits>
 
 #include "score_common.cuh"
+#include "select_params.cuh"
 
 namespace asp {
 namespace {
@@ -60,30 +62,6 @@ constexpr int kRxBins = 256;                    // bins of one radix round
 constexpr int kLoBits = 19;                     // a weight is lo + hi << 19 in the histogram
 constexpr int kLimb = 14;                       // radix rounds: 3 limbs of 14 bits
 constexpr int kFine = 16;                       // histogram bins per coarse bin
-
-struct CsParams {
-  uint16_t* summ;  // written only by the append variant
-  const float* q;
-  const int32_t* seq_lens;
-  int32_t* lists;
-  int32_t* lens;
-  uint32_t* err;
-  int Hq, Hkv, P, max_pages;
-  float inv_sqrt_d;
-  float gamma;
-  int budget;
-  int pf_pieces;  // pieces per warp fetched into L2 before the predecessor ends
-  // K/V of kept pages fetched into L2 for the decode that follows: the first
-  // kv_pf_pages kept pages (in id order) of each CTA's range
-  const int32_t* bt;
-  uint16_t* k_cache;  // written only by the append variant
-  uint16_t* v_cache;
-  int num_phys;
-  int kv_pf_pages;
-  // append variant: the new token's K and V rows, bf16 [B, Hkv, d]
-  const uint16_t* k_new;
-  const uint16_t* v_new;
-};
 
 // Cluster exchange block, one per CTA. Every field a CTA reads after a
 // barrier was pushed into it (remote stores) before that barrier.
@@ -784,18 +762,6 @@ __global__ void __launch_bounds__(kCsThreads, 1)
   }
 }
 
-// Pieces per warp fetched into L2 before the previous kernel ends, and kept
-// pages per CTA whose K/V the kernel fetches into L2 for the decode (8 KiB
-// each at P = 16, d = 128). Outstanding bulk prefetches hold this kernel
-// open, so more pages make it slower than they make the decode faster. At
-// 128k, gamma = 0.99 on one GB300 (builds alternated on one box, steps/s):
-// (pages, pieces) = (0, 3) 365.5, (32, 3) 372.6, (64, 3) 369.1, (128, 3)
-// 364.9, (256, 3) 339.4; on a later build of the decode, (32, 3) 390.7,
-// (24, 6) 393.6, (28, 6) 393.6, (24, 8) 393.6, and on another box (16, 3)
-// 391.9, (48, 3) 391.9, (32, 4) 394.8, (24, 4) 395.3 against (32, 3) 393.7.
-constexpr int kCsPrefetchPieces = 6;
-constexpr int kCsKvPrefetchPages = 24;
-
 template <int D, int G, int C, bool Append>
 cudaError_t launch_cs(const SelectArgs& a, cudaStream_t stream) {
   const asp_paged_kv& kv = *a.kv;
@@ -809,10 +775,7 @@ cudaError_t launch_cs(const SelectArgs& a, cudaStream_t stream) {
                               (unsigned long long)kv.batch * kv.num_kv_heads * kv.max_pages, 64,
                               (unsigned)L::kRows);
   if (e != cudaSuccess) return e;
-  CsParams p{kv.summaries, a.q, kv.seq_lens, a.lists, a.lens, a.err, kv.num_q_heads,
-             kv.num_kv_heads, kv.page_size, kv.max_pages, 1.0f / sqrtf((float)D), a.gamma,
-             a.budget, kCsPrefetchPieces, kv.block_table, kv.k_cache, kv.v_cache,
-             kv.num_phys_pages, kCsKvPrefetchPages, a.k_new, a.v_new};
+  const CsParams p = cs_params(a);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kv.batch * kv.num_kv_heads * C);
   cfg.blockDim = dim3(kCsThreads);

@@ -83,8 +83,9 @@ def patches():
         ("  // ------------------------------------- 7. kept ids, ascending, per CTA\n",
          "  " + _stamp("sel", ns, 7) + "\n  " + _stamp("sel", ns, 8, value="1ull + nc")
          + "\n  // ------------------------------------- 7. kept ids, ascending, per CTA\n"),
-        ("      }\n    }\n  }\n}\n\n// Pieces per warp fetched",
-         "      }\n    }\n  }\n  __syncthreads();\n  " + _stamp("sel", ns, 6) + "\n}\n\n// Pieces per warp fetched"),
+        ("      }\n    }\n  }\n}\n\ntemplate <int D, int G, int C, bool Append>\ncudaError_t launch_cs(",
+         "      }\n    }\n  }\n  __syncthreads();\n  " + _stamp("sel", ns, 6)
+         + "\n}\n\ntemplate <int D, int G, int C, bool Append>\ncudaError_t launch_cs("),
     ]
     nd = len(DEC_SLOTS)
     smid = ("if (threadIdx.x == 0) { unsigned r_; asm(\"mov.u32 %0, %%smid;\" : \"=r\"(r_)); "

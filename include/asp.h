@@ -40,7 +40,7 @@
  * - Caches: k_cache and v_cache of asp_paged_kv may BOTH be NULL (a cache of 8-bit
  *   pages, asp_q8_pages below) in asp_workspace_size, asp_select_plan,
  *   asp_coverage_select, asp_coverage_select_noalloc, asp_page_scores and the
- *   asp_q8_ calls, which use neither; elsewhere a NULL one is ASP_EINVAL.
+ *   asp_q8_ calls, whose results need neither; elsewhere a NULL one is ASP_EINVAL.
  * - The current CUDA device when a call is made must be the device that owns
  *   the pointers.
  * - Tracing: every call opens an NVTX range named after itself (e.g.
@@ -185,8 +185,11 @@ asp_status asp_page_summarize(const asp_paged_kv* kv, int32_t mode,
  *          page ids in ascending order; entries past lens[b,h] are untouched.
  * lens   : int32 [B, Hkv] out; the kept count (0 only when T_b == 0).
  * Masses are summed in 64-bit fixed point, so the result is deterministic.
- * Reads summaries, seq_lens and q only (not block_table or the K/V pages):
- * run asp_page_summarize after any change to the cache first.
+ * The result depends on summaries, seq_lens and q only (not on block_table or
+ * the K/V pages): run asp_page_summarize after any change to the cache first.
+ * Where the caches are there, the one-pass kernel also moves the K and V of the
+ * first kept pages into L2 for the decode, by block_table; an entry out of range
+ * is left out without an error. A cache with NULL k_cache and v_cache: nothing.
  */
 asp_status asp_coverage_select(const asp_paged_kv* kv, const float* q, float gamma,
                                int32_t budget, int32_t* lists, int32_t* lens,
