@@ -81,30 +81,20 @@ struct Params {
   float eps;
 };
 
-// Work items are numbered so that request b's first is floor(off_b / P) + 2 b: n tokens touch
-// at most floor(n / P) + 2 pages, so the ranges do not overlap, and an item finds its request
-// from the offsets alone. One row per request: item b is request b.
-// ls: log2 of an item's slots.
-__device__ __forceinline__ int first_item(const Params& p, int b, int ls) {
-  return (min(max(p.q_offsets[b], 0), p.num_tokens) >> ls) + 2 * b;
-}
-
 struct Item {
   int b, page, lo, cnt;  // the new slots lo .. lo + cnt - 1, all in this page; b < 0: no more
   int row0, phys;        // the first's packed row; physical page, -1: none
 };
 
 // The first item from `it` on that has tokens, found by a whole warp; moves `it` behind it.
+// ls: log2 of an item's slots. One row per request: item b is request b.
 __device__ __forceinline__ Item find_item(const Params& p, int& it, int lane, int ls, int items) {
   for (; it < items; it += gridDim.x) {
     int b = it, page_of_b = 0;
-    if (p.q_offsets) {  // the last request whose first item is not past this one
-      int before = 0;
-      for (int y = lane; y < p.B; y += 32)
-        before += first_item(p, y, ls) <= it;
-      b = __reduce_add_sync(kFull, before) - 1;
-      if (b < 0) continue;  // offsets that do not ascend
-      page_of_b = it - first_item(p, b, ls);
+    if (p.q_offsets) {
+      b = request_of_item(p.q_offsets, p.B, p.num_tokens, ls, it, lane);
+      if (b < 0) continue;
+      page_of_b = it - first_item(p.q_offsets, b, p.num_tokens, ls);
     }
     uint32_t* err = lane == 0 ? p.err : nullptr;
     const int T = clamp_seq_len(p.seq_lens[b], p.max_pages, p.P, err);
@@ -115,7 +105,7 @@ __device__ __forceinline__ Item find_item(const Params& p, int& it, int lane, in
     const int at = (first >> ls) + page_of_b;  // the page, or block of slots
     x.lo = max(first, at << ls);
     x.cnt = min(T, (at + 1) << ls) - x.lo;
-    if (x.cnt <= 0 || page_of_b < 0) continue;
+    if (x.cnt <= 0) continue;
     x.page = x.lo >> p.lp;
     x.row0 = nr.row0 + (x.lo - first);
     x.phys = p.bt[(size_t)b * p.max_pages + x.page];  // checked by the caller

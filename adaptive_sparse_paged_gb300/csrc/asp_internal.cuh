@@ -153,6 +153,31 @@ __device__ __forceinline__ NewRows new_rows(const int32_t* q_offsets, int b, int
   return r;
 }
 
+// The work items of the calls that append: a page (or block of 2^ls slots) of one request each,
+// numbered so that request b's first is floor(off_b / 2^ls) + 2 b: n tokens touch at most
+// floor(n / 2^ls) + 2 of them, so that the ranges of requests whose offsets ascend do not
+// overlap, and an item finds its request from the offsets alone.
+__device__ __forceinline__ int held_offset(const int32_t* q_offsets, int b, int num_tokens) {
+  return min(max(q_offsets[b], 0), num_tokens);
+}
+__device__ __forceinline__ int first_item(const int32_t* q_offsets, int b, int num_tokens, int ls) {
+  return (held_offset(q_offsets, b, num_tokens) >> ls) + 2 * b;
+}
+// The request of item `it`, found by a whole warp: the last whose first item is not past it, -1
+// before the first. Only up to the first request whose offsets descend: it is skipped (new_rows),
+// and behind it the ranges may overlap others, so that those requests get no items at all.
+__device__ __forceinline__ int request_of_item(const int32_t* q_offsets, int B, int num_tokens,
+                                               int ls, int it, int lane) {
+  int end = B;  // the first request that the item lies before, or that is behind a descent
+  for (int y = lane; y < B; y += 32) {
+    const int off = held_offset(q_offsets, y, num_tokens);
+    const int last = held_offset(q_offsets, max(y - 1, 0), num_tokens);
+    const bool past = (off >> ls) + 2 * y > it, fell = off < last;
+    end = min(end, past | fell ? y : B);
+  }
+  return __reduce_min_sync(0xffffffffu, end) - 1;
+}
+
 // ------------------------------------------------------------------ mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));

@@ -57,15 +57,6 @@ struct Params {
   float eps;
 };
 
-// Work items are numbered so that request b's first is floor(off_b / P) + 2 b:
-// n tokens touch at most floor(n / P) + 2 pages, so the ranges do not overlap,
-// and an item finds its request from the offsets alone. One row per request:
-// item b is request b.
-template <int P>
-__device__ __forceinline__ int first_item(const int32_t* q_offsets, int b, int num_tokens) {
-  return min(max(q_offsets[b], 0), num_tokens) / P + 2 * b;
-}
-
 __device__ __forceinline__ float2 unpack(uint32_t x) {
   return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
 }
@@ -189,15 +180,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_rotate_kernel(const Para
     for (int it = blockIdx.x; ok; it += gridDim.x) {
       Item x{-1, 0, 0, 0, 0, -1};
       if (it < p.items) {
-        // the item's request: the last whose first item is not past it
-        int b = it, page_of_b = 0;
+        int b = it, page_of_b = 0;  // one row per request: item b is request b
         if (p.q_offsets) {
-          int before = 0;
-          for (int y = lane; y < p.B; y += 32)
-            before += first_item<P>(p.q_offsets, y, p.num_tokens) <= it;
-          b = __reduce_add_sync(kFull, before) - 1;
-          if (b < 0) continue;  // offsets that do not ascend
-          page_of_b = it - first_item<P>(p.q_offsets, b, p.num_tokens);
+          constexpr int kLog = P == 64 ? 6 : P == 32 ? 5 : 4;
+          b = request_of_item(p.q_offsets, p.B, p.num_tokens, kLog, it, lane);
+          if (b < 0) continue;
+          page_of_b = it - first_item(p.q_offsets, b, p.num_tokens, kLog);
         }
         uint32_t* err = lane == 0 ? p.err : nullptr;
         const int T = clamp_seq_len(p.seq_lens[b], p.max_pages, P, err);
@@ -206,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_rotate_kernel(const Para
         x.page = first / P + page_of_b;
         x.lo = max(first, x.page * P);
         x.cnt = min(T, (x.page + 1) * P) - x.lo;
-        if (x.cnt <= 0 || page_of_b < 0) continue;
+        if (x.cnt <= 0) continue;
         x.b = b;
         x.row0 = nr.row0 + (x.lo - first);
         x.phys = p.bt[(size_t)b * p.max_pages + x.page];
