@@ -117,14 +117,17 @@ __device__ __forceinline__ float4 own4(const Params& p, size_t at) {
 // The factors of a row's two parts, its (unnormalised) attention over the prefix, of which the
 // exponentials' sum is l at the reference `ref` (a natural logarithm), and its own attention:
 // prefix, own; and the lse of both. A part without tokens has an lse of -inf and the factor 0.
+// The factors come from the sum itself, not from the lse, whose rounding grows with its size: a
+// row without an own part is then divided by l. A call without own parts takes the same way.
 struct OwnPart {
   float prefix, own, lse;
   __device__ __forceinline__ OwnPart(float ref, float l, float own_lse) {
-    const float a = l == 0.f ? -INFINITY : ref + logf(l);
-    const float top = fmaxf(a, own_lse), at = top == -INFINITY ? 0.f : top;
-    lse = at + logf(expf(a - at) + expf(own_lse - at));
-    prefix = l == 0.f ? 0.f : expf(ref - lse);
-    own = own_lse == -INFINITY ? 0.f : expf(own_lse - lse);
+    const bool none = l == 0.f;
+    const float top = none ? own_lse : fmaxf(ref, own_lse), at = top == -INFINITY ? 0.f : top;
+    const float a = none ? 0.f : expf(ref - at), b = expf(own_lse - at), sum = fmaf(l, a, b);
+    lse = at + logf(sum);
+    prefix = none ? 0.f : a / sum;
+    own = own_lse == -INFINITY ? 0.f : b / sum;
   }
 };
 
@@ -595,8 +598,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (task.whole) {
         float inv = l > 0.f ? 1.0f / l : l;  // a NaN sum stays NaN, an empty row gives 0
         float lse = l == 0.f ? -INFINITY : m * p.scale + logf(l), own = 0.f;
-        if (kPrefix && p.own_lse && mine) {
-          const OwnPart part(m * p.scale, l, p.own_lse[at]);
+        if (kPrefix) {
+          const OwnPart part(m * p.scale, l, p.own_lse && mine ? p.own_lse[at] : -INFINITY);
           inv = part.prefix, own = part.own, lse = part.lse;
         }
         // Four lanes exchange 16-byte pieces so that a row's 64 bytes leave together: a
@@ -869,15 +872,12 @@ __global__ void __launch_bounds__(256, 2) prefix_join_kernel(const Params p, int
       }
     }
     const float ref = M == -INFINITY ? 0.f : M * 0.69314718055994530942f;
-    float a = L > 0.f ? 1.0f / L : L, b = 0.f, lse = L == 0.f ? -INFINITY : ref + logf(L);
-    if (p.own_lse) {
-      const OwnPart part(ref, L, own_lse);
-      a = part.prefix, b = part.own, lse = part.lse;
-    }
+    const OwnPart part(ref, L, own_lse);
+    const float a = part.prefix, b = part.own;
     *reinterpret_cast<uint2*>(tile + lane * kPitch + 4 * warp) =
         make_uint2(pack_bf16(fmaf(acc.x, a, own.x * b), fmaf(acc.y, a, own.y * b)),
                    pack_bf16(fmaf(acc.z, a, own.z * b), fmaf(acc.w, a, own.w * b)));
-    if (warp == 0 && there && col0 == 0) p.lse[at] = lse;
+    if (warp == 0 && there && col0 == 0) p.lse[at] = part.lse;
     __syncthreads();
     constexpr int kPieces = kWide / 8;  // of 16 bytes
     if (tid < 32 * kPieces) {

@@ -1,0 +1,72 @@
+"""asp_prefix_attention's join of a row's two parts, where their sizes are extreme."""
+
+import math
+
+import pytest
+import torch
+
+from adaptive_sparse_paged_gb300 import binding as B
+from tests import guards
+from tests import prompt_ref as R
+from tests import test_gpu_prefix as TP
+
+pytestmark = pytest.mark.gpu
+
+
+def outputs(batch):
+    out = guards.guarded((batch.N, batch.Hq, batch.d), torch.bfloat16, batch.dev, fill=7.0, what="out")
+    lse = guards.guarded((batch.N, batch.Hq), torch.float32, batch.dev, fill=7.0, what="lse")
+    return out, lse
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tokens,rows", [([3000], [5]), ([40, 0], [700, 3]), ([2100, 900], [100, 300])])
+@pytest.mark.parametrize("q_size", [1.0, 300.0, 30000.0])
+def test_no_own_tokens_is_no_own_part(cuda_device, d, tokens, rows, q_size):
+    """Rows whose own lse is -inf: bit for bit what the call gives without own parts, however
+    large the logits (pieces that are whole items, and that are joined)."""
+    batch = R.Batch(cuda_device, tokens, rows, 8, 2, d, 16, seed=d)
+    kv = batch.to_device()
+    q = (batch.q.float() * q_size).to(torch.bfloat16).to(cuda_device)
+    own_out = torch.full((batch.N, 8, d), math.nan, device=cuda_device)
+    own_lse = torch.full((batch.N, 8), -math.inf, device=cuda_device)
+    got = []
+    for own in ((None, None), (own_out, own_lse)):
+        out, lse = outputs(batch)
+        B.asp_prefix_attention(kv, q, batch.offs_dev, batch.scale, *own, out, lse, batch.ws)
+        got.append((out, lse))
+    assert B.asp_get_device_error(batch.ws) == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [1, 40, 5000])
+@pytest.mark.parametrize("base", [0.0, 40000.0, 1e6, -1e6])
+def test_weights_sum_to_one(cuda_device, d, T, base):
+    """Both parts are one bf16 vector, so that the result is: however large the logits, from whose
+    rounded lse the weights would be off by 2^-24 of it each.
+
+    All keys are equal and a logit times log2(e) is a whole number that fp32 holds, so that every
+    probability is 1, the prefix's sum T and its O T times the vector, all exactly. The rest, two
+    exponentials, their sum, two divisions and one multiply-add, is under 2^-20 of the vector:
+    less than half a step of bf16."""
+    batch = R.Batch(cuda_device, [T], [4], 8, 2, d, 16, seed=T)
+    value = torch.linspace(-3, 3, d).to(torch.bfloat16)
+    key = torch.zeros((T, 2, d), dtype=torch.bfloat16)
+    key[..., 0] = 1.0
+    batch.put(batch.k, 0, key)
+    batch.put(batch.v, 0, value.expand(T, 2, d))
+    kv = batch.to_device()
+    q = torch.zeros((4, 8, d), dtype=torch.bfloat16)
+    q[..., 0] = 8 * base
+    scale = float(torch.tensor(math.log(2.0), dtype=torch.float32)) / 8
+    pre = float(q[0, 0, 0]) * scale + math.log(T)
+    own_lse = (pre + torch.tensor([1.0, -1.0, 0.0, 3.0])[:, None]).expand(4, 8).float().contiguous()
+    own_out = value.float().expand(4, 8, d).contiguous()
+    out, lse = outputs(batch)
+    B.asp_prefix_attention(kv, q.to(cuda_device), batch.offs_dev, scale, own_out.to(cuda_device),
+                           own_lse.to(cuda_device), out, lse, batch.ws)
+    assert B.asp_get_device_error(batch.ws) == 0
+    assert torch.equal(out.cpu(), value.expand(4, 8, d))
+    both = torch.logaddexp(torch.full((4, 8), pre, dtype=torch.float64), own_lse.double())
+    R.close(lse, both, 4 * R.FP32 * both.abs() + 2.0 ** -18, "lse")
