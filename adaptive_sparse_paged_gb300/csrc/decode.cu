@@ -335,9 +335,9 @@ struct Q8Pages {
     const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
     lo = pack_f16(x - h.x, y - h.y);
   }
-  // 2^e of a scale byte e + 127 (255: NaN; 0, which no append writes, counts as 0), and e.
+  // 2^e of a scale byte e + 127 (255: NaN; 0, which no append writes, is 2^-127), and e.
   static __device__ __forceinline__ float power(uint32_t c) {
-    return __uint_as_float((c << 23) + (((c + 1) & 256) << 14));
+    return __uint_as_float(max(c << 23, 1u << 22) + (((c + 1) & 256) << 14));
   }
   static __device__ __forceinline__ float exponent(uint32_t c) {
     return c == 255 ? __uint_as_float(0x7fc00000u) : (float)((int)c - 127);
