@@ -243,12 +243,14 @@ struct Bf16Pages {
 // m16n8k16: fp32 accumulators, queries and probabilities as two fp16 terms each (a bf16
 // product could hold neither those terms' range nor, for the same work, their bits).
 //   S^T[t] = 2^ek[t] * (K8 . (Q hi + Q lo)^T),  Q scaled by a power of two to below 2^15
-//   O^T   += V8^T . (P hi + P lo)^T,            P = 2^(s + ev - R + 7)
-// The values' powers of two go into the probabilities, which have a reference R of their own
-// (of s + ev), apart from m (of s), which the sum's terms go by: neither then depends on how
-// the scales of different tokens lie. The references move only when a score is more than 2^8
-// above them; until then O stays untouched. Groups of up to four heads are packed: the two
-// terms are columns 0 - 3 and 4 - 7 of one product.
+//   O^T   += V8^T . (P hi + P lo)^T,            P = 2^((s - m) + ev - r + 7)
+// The values' powers of two go into the probabilities, which have a reference r of their own
+// (of s - m + ev), apart from m (of s), which the sum's terms go by: neither the sum nor the
+// largest terms of O then depend on how the scales of different tokens lie. All of it is formed
+// from s - m, which is exact where it counts: s + ev would round ev off large logits. The
+// references move only when a score is more than 2^8 above them; until then O stays untouched.
+// Groups of up to four heads are packed: the two terms are columns 0 - 3 and 4 - 7 of one
+// product.
 //
 // Fragments are read with wide loads, not ldmatrix: a lane's 16 bytes of a K row are four
 // k-steps (which channels a k-step holds is free, so long as Q agrees), and 16 bytes of
@@ -278,7 +280,7 @@ struct Q8Pages {
   // A CTA takes a stage for each of its warps at least: short lists go to fewer CTAs, whose
   // parts take less time to join (2k tokens of two heads: 17.9 us over all CTAs, 10.8 so).
   static constexpr int kMinPages = kWarps / kSubs;
-  static constexpr float kMove = 8.f;  // m and R move when a score is more than 2^8 above them
+  static constexpr float kMove = 8.f;  // m and r move when a score is more than 2^8 above them
   static constexpr float kTop = 7.f;   // 2^(7 + 8) is below fp16's largest number
 
   static __device__ __forceinline__ void issue(uint8_t* dst, uint8_t* extra, const CUtensorMap& tmK,
@@ -346,7 +348,7 @@ struct Q8Pages {
   struct State {
     float m0, m1, l0, l1;
     float o[D / 16][4];
-    float r0, r1;        // R of the two columns
+    float u0, u1;        // kTop - r of the two columns
     float qs0, qs1;      // the power of two that their queries were divided by
     uint32_t qf[D / 16][2];                // the first terms; packed: of columns 4 .. 7 the second
     uint32_t qlo[kPack ? 1 : D / 16][2];   // the second terms
@@ -392,7 +394,7 @@ struct Q8Pages {
     }
 
     __device__ __forceinline__ void start() {
-      m0 = m1 = r0 = r1 = -INFINITY, l0 = l1 = 0.f;
+      m0 = m1 = -INFINITY, u0 = u1 = INFINITY, l0 = l1 = 0.f;
 #pragma unroll
       for (int dt = 0; dt < D / 16; ++dt) o[dt][0] = o[dt][1] = o[dt][2] = o[dt][3] = 0.f;
     }
@@ -441,13 +443,18 @@ struct Q8Pages {
         float ev = exponent(extra[16 + t]);
         float x0 = ((low ? sv[0] : sv[2]) + g0) * (qs0 * k), x1 = ((low ? sv[1] : sv[3]) + g1) * (qs1 * k);
         if (t >= ntok) x0 = x1 = -INFINITY, ev = 0.f;
-        const float y0 = x0 + ev, y1 = x1 + ev;
-        const bool moves = fmaxf(fmaxf(x0 - m0, x1 - m1), fmaxf(y0 - r0, y1 - r1)) > kMove;
-        if (__any_sync(kFull, moves)) move(x0, x1, y0, y1);
-        l0 += ex2(x0 - m0);
-        l1 += ex2(x1 - m1);
+        float t0 = x0 - m0, t1 = x1 - m1, y0 = t0 + (ev + u0), y1 = t1 + (ev + u1);
+        const bool moves = fmaxf(fmaxf(t0, t1), fmaxf(y0, y1) - kTop) > kMove;
+        if (__any_sync(kFull, moves)) {
+          move_m(x0, x1);
+          t0 = x0 - m0, t1 = x1 - m1;
+          move_r(t0 + ev, t1 + ev);
+          y0 = t0 + (ev + u0), y1 = t1 + (ev + u1);
+        }
+        l0 += ex2(t0);
+        l1 += ex2(t1);
         uint32_t hi, lo;
-        split(ex2(y0 - r0 + kTop), ex2(y1 - r1 + kTop), hi, lo);
+        split(ex2(y0), ex2(y1), hi, lo);
         const uint32_t got = __shfl_xor_sync(kFull, low ? lo : hi, 2);
         h0 = movm_t(low ? hi : got), h1 = movm_t(low ? got : lo);
       } else {
@@ -456,15 +463,24 @@ struct Q8Pages {
         sv[0] *= qs0 * k0, sv[1] *= qs1 * k0, sv[2] *= qs0 * k1, sv[3] *= qs1 * k1;
         if (tok >= ntok) sv[0] = sv[1] = -INFINITY, e0 = 0.f;
         if (tok + 8 >= ntok) sv[2] = sv[3] = -INFINITY, e1 = 0.f;
-        const float b0 = fmaxf(sv[0], sv[2]), b1 = fmaxf(sv[1], sv[3]);
-        const float c0 = fmaxf(sv[0] + e0, sv[2] + e1), c1 = fmaxf(sv[1] + e0, sv[3] + e1);
-        const bool moves = fmaxf(fmaxf(b0 - m0, b1 - m1), fmaxf(c0 - r0, c1 - r1)) > kMove;
-        if (__any_sync(kFull, moves)) move(b0, b1, c0, c1);
-        l0 += ex2(sv[0] - m0) + ex2(sv[2] - m0);
-        l1 += ex2(sv[1] - m1) + ex2(sv[3] - m1);
-        const float t0 = kTop - r0, t1 = kTop - r1;
-        split(ex2(sv[0] + (e0 + t0)), ex2(sv[1] + (e0 + t1)), h0, w0);
-        split(ex2(sv[2] + (e1 + t0)), ex2(sv[3] + (e1 + t1)), h1, w1);
+        float t[4], y[4];
+        auto terms = [&]() {
+          t[0] = sv[0] - m0, t[1] = sv[1] - m1, t[2] = sv[2] - m0, t[3] = sv[3] - m1;
+          y[0] = t[0] + (e0 + u0), y[1] = t[1] + (e0 + u1);
+          y[2] = t[2] + (e1 + u0), y[3] = t[3] + (e1 + u1);
+        };
+        terms();
+        const bool moves = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])),
+                                 fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) - kTop) > kMove;
+        if (__any_sync(kFull, moves)) {
+          move_m(fmaxf(sv[0], sv[2]), fmaxf(sv[1], sv[3]));
+          move_r(fmaxf(sv[0] - m0 + e0, sv[2] - m0 + e1), fmaxf(sv[1] - m1 + e0, sv[3] - m1 + e1));
+          terms();
+        }
+        l0 += ex2(t[0]) + ex2(t[2]);
+        l1 += ex2(t[1]) + ex2(t[3]);
+        split(ex2(y[0]), ex2(y[1]), h0, w0);
+        split(ex2(y[2]), ex2(y[3]), h1, w1);
         h0 = movm_t(h0), h1 = movm_t(h1), w0 = movm_t(w0), w1 = movm_t(w1);
       }
       // ---- O^T[d x 8] += V^T[d x 16] . P^T[16 x 8]
@@ -494,20 +510,24 @@ struct Q8Pages {
       }
     }
 
-    // New references m and R: the largest score, and score with its value's scale, so far; b, c:
-    // this lane's of the stage.
-    __device__ __forceinline__ void move(float b0, float b1, float c0, float c1) {
+    // The largest of a column's tokens; x: this lane's of the stage.
+    static __device__ __forceinline__ float of_column(float x) {
 #pragma unroll
-      for (int off = kPack ? 2 : 4; off < 32; off <<= 1) {
-        b0 = fmaxf(b0, __shfl_xor_sync(kFull, b0, off));
-        b1 = fmaxf(b1, __shfl_xor_sync(kFull, b1, off));
-        c0 = fmaxf(c0, __shfl_xor_sync(kFull, c0, off));
-        c1 = fmaxf(c1, __shfl_xor_sync(kFull, c1, off));
-      }
-      b0 = fmaxf(m0, b0), b1 = fmaxf(m1, b1), c0 = fmaxf(r0, c0), c1 = fmaxf(r1, c1);
+      for (int off = kPack ? 2 : 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, off));
+      return x;
+    }
+    // A new reference m: the largest score so far. r is of what lies above m: it moves against it.
+    __device__ __forceinline__ void move_m(float b0, float b1) {
+      b0 = fmaxf(m0, of_column(b0)), b1 = fmaxf(m1, of_column(b1));
       l0 *= exp2f(m0 - b0), l1 *= exp2f(m1 - b1);
-      const float f0 = exp2f(r0 - c0), f1 = exp2f(r1 - c1);
-      m0 = b0, m1 = b1, r0 = c0, r1 = c1;
+      u0 += b0 - m0, u1 += b1 - m1;
+      m0 = b0, m1 = b1;
+    }
+    // A new reference r, after m: the largest score above m with its value's scale so far.
+    __device__ __forceinline__ void move_r(float c0, float c1) {
+      c0 = fminf(u0, kTop - of_column(c0)), c1 = fminf(u1, kTop - of_column(c1));
+      const float f0 = exp2f(c0 - u0), f1 = exp2f(c1 - u1);
+      u0 = c0, u1 = c1;
 #pragma unroll
       for (int dt = 0; dt < D / 16; ++dt) {
         o[dt][0] *= f0;
@@ -517,7 +537,8 @@ struct Q8Pages {
       }
     }
 
-    // O to the scale of m. A NaN sum keeps a finite m, so that the merges carry it on.
+    // O to the scale of m. A NaN sum keeps a finite m, so that the merges carry it on. 2^-u may
+    // be as small as fp32 holds no more in full (values of the smallest scales): two steps.
     __device__ __forceinline__ void end() {
       if (kPack) {
         l0 += __shfl_xor_sync(kFull, l0, 2);
@@ -525,17 +546,21 @@ struct Q8Pages {
       }
       if (l0 != l0) m0 = 0.f;
       if (l1 != l1) m1 = 0.f;
-      const float f0 = r0 == -INFINITY ? 1.f : exp2f(r0 - m0 - kTop);
-      const float f1 = r1 == -INFINITY ? 1.f : exp2f(r1 - m1 - kTop);
+      float f[2], g[2];  // of each column: the fraction and half of the power, the other half
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float u = i ? u1 : u0, x = u == INFINITY ? 0.f : -u, whole = rintf(x);
+        const int n = (int)fminf(fmaxf(whole, -200.f), 200.f), half = n >> 1;
+        f[i] = exp2f(x - whole) * __int_as_float((127 + half) << 23);
+        g[i] = __int_as_float((127 + n - half) << 23);
+      }
 #pragma unroll
       for (int dt = 0; dt < D / 16; ++dt) {
-        o[dt][0] *= f0;
-        o[dt][1] *= f1;
-        o[dt][2] *= f0;
-        o[dt][3] *= f1;
-        if (kPack) {  // the two terms' columns
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[dt][i] += __shfl_xor_sync(kFull, o[dt][i], 2);
+        for (int i = 0; i < 4; ++i) {
+          o[dt][i] *= f[i & 1];
+          o[dt][i] *= g[i & 1];
+          if (kPack) o[dt][i] += __shfl_xor_sync(kFull, o[dt][i], 2);  // the two terms' columns
         }
       }
     }

@@ -48,3 +48,36 @@ def test_smallest_scales_of_keys(cuda_device, Hq, Hkv, d, bytes_):
     assert B.asp_get_device_error(batch.ws) == 0
     for b, t in enumerate(batch.tokens):
         assert torch.equal(batch.rows(k.cpu(), b), batch.rows(batch.k, b))
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 64), (8, 2, 128), (8, 1, 128), (8, 1, 64)])
+@pytest.mark.parametrize("bytes_", [[0], [0, 3, 9], [240, 244]])
+def test_smallest_and_largest_scales_of_values(cuda_device, Hq, Hkv, d, bytes_):
+    """Outputs keep their precision where a power of two of theirs is below fp32's normal numbers,
+    or its square above the largest."""
+    batch = Q.Q8Batch(cuda_device, [40, 17], [0, 0], Hq, Hkv, d, 16, seed=d + Hkv)
+    small_rows(batch, 1, bytes_)
+    TD.run(batch, *TD.random_lists(batch, 1.0))
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 64), (8, 2, 128), (8, 1, 128), (8, 1, 64)])
+@pytest.mark.parametrize("T", [1, 17, 700])
+@pytest.mark.parametrize("size", [1.0, 1e3, 1e5, 1e9])
+def test_one_token_with_all_the_weight(cuda_device, Hq, Hkv, d, T, size):
+    """Its value row comes out as it is, however large its logit: the others are 60 and more below
+    it, 2^-86 of its weight. Bound: the exponentials of two numbers that cancel, the sums and the
+    division, a few fp32 steps; the others' weights, and what the fp16 terms leave of them."""
+    batch = Q.Q8Batch(cuda_device, [T], [0], Hq, Hkv, d, 16, seed=T)
+    heavy = T // 3
+    key = torch.zeros((T, Hkv, d), dtype=torch.float64)
+    key[heavy, :, 0] = 1.0
+    batch.put8(0, 0, key)
+    q = torch.zeros((1, Hq, d))
+    q[..., 0] = 60.0 * size / batch.scale
+    lists, lens = TD.random_lists(batch, 1.0)
+    out, lse = TD.run(batch, lists, lens, q=q)
+    want = batch.rows(batch.v, 0)[heavy].double().repeat_interleave(Hq // Hkv, 0)
+    rest = T * 2.0 ** -31 * batch.rows(batch.v, 0).double().abs().amax()
+    R.close(out[0], want, 2.0 ** -20 * want.abs() + (0 if T == 1 else rest), "out")
+    R.close(lse[0], 60.0 * size * torch.ones(Hq, dtype=torch.float64),
+            torch.full((Hq,), 2.0 ** -20 * 60 * size, dtype=torch.float64), "lse")
