@@ -249,8 +249,11 @@ struct Bf16Pages {
 // largest terms of O then depend on how the scales of different tokens lie. All of it is formed
 // from s - m, which is exact where it counts: s + ev would round ev off large logits. The
 // references move only when a score is more than 2^8 above them; until then O stays untouched.
-// Groups of up to four heads are packed: the two terms are columns 0 - 3 and 4 - 7 of one
-// product.
+// P's terms end at fp16's smallest step, 2^-25 where the largest P is 2^7 at least: a token
+// whose P lies 2^-d below it keeps 32 - d bits, where an fp32 product would keep 24. Products
+// of a narrower range (P scaled a stage at a time) would cost an fp32 multiply-add of all of O
+// a stage. Groups of up to four heads are packed: the two terms are columns 0 - 3 and 4 - 7 of
+// one product.
 //
 // Fragments are read with wide loads, not ldmatrix: a lane's 16 bytes of a K row are four
 // k-steps (which channels a k-step holds is free, so long as Q agrees), and 16 bytes of

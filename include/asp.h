@@ -499,10 +499,16 @@ asp_status asp_q8_read(const asp_paged_kv* kv, const asp_q8_pages* pages, uint16
  *   out[b,h,:] = sum_t softmax_t(sm_scale * q[b,h].k_t) v_t
  *   lse[b,h]   = log sum_t exp(sm_scale * q[b,h].k_t)
  * over the valid tokens of the listed pages, with the values that the stored elements stand
- * for. Queries and probabilities enter the products as two fp16 terms each (22 bits and
- * more), so out and lse are as exact as fp32 sums. A segment with lens 0 gets out = 0,
- * lse = -inf; a NaN key among the listed tokens makes out and lse of its head's group
- * NaN, a NaN value row out. Other arguments and conditions as for asp_sparse_decode.
+ * for. Queries and probabilities enter the products as two fp16 terms each: lse is as exact
+ * as fp32 sums, and out, but for one thing. A token's weight p_t 2^e_t (its probability and
+ * its value row's power of two) is good to 2^-22 of itself and to 2^-32 of the largest such
+ * weight of its head, so that channel c of out is off by up to
+ *   2^-32 max_t(p_t 2^e_t) sum_t |element of v_t in c|
+ * besides the steps of fp32 sums. That shows only in a channel in which the rows of the
+ * largest weights have (next to) nothing: tokens 2^20 below them count there to 12 bits.
+ * A segment with lens 0 gets out = 0, lse = -inf; a NaN key among the listed tokens makes out
+ * and lse of its head's group NaN, a NaN value row out. Other arguments and conditions as for
+ * asp_sparse_decode.
  */
 asp_status asp_q8_decode(const asp_paged_kv* kv, const asp_q8_pages* pages, const float* q,
                          const int32_t* lists, const int32_t* lens, float sm_scale, float* out,

@@ -81,3 +81,36 @@ def test_one_token_with_all_the_weight(cuda_device, Hq, Hkv, d, T, size):
     R.close(out[0], want, 2.0 ** -20 * want.abs() + (0 if T == 1 else rest), "out")
     R.close(lse[0], 60.0 * size * torch.ones(Hq, dtype=torch.float64),
             torch.full((Hq,), 2.0 ** -20 * 60 * size, dtype=torch.float64), "lse")
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 64), (8, 2, 128), (8, 1, 128), (8, 1, 64)])
+@pytest.mark.parametrize("above", [0, 10, 20, 30])
+def test_channels_without_the_heavy_row(cuda_device, Hq, Hkv, d, above):
+    """One row has a single channel, 2^above larger than all others' values: the other channels are
+    held to their own mass and to the stated 2^-32 of the largest weight for each token. (The
+    bound by whole rows that other tests use would let the heavy channel excuse them.)"""
+    batch = Q.Q8Batch(cuda_device, [90, 33], [0, 0], Hq, Hkv, d, 16, seed=above, spread=0)
+    for b, at in ((0, 41), (1, 7)):
+        row = torch.zeros((1, Hkv, d), dtype=torch.float64)
+        row[..., 3] = 3.0 * 2.0 ** above
+        batch.put8(b, 1, row, start=at)
+    q = torch.randn((2, Hq, d), generator=batch.gen)
+    lists, lens = TD.random_lists(batch, 1.0)
+    out, _ = TD.run(batch, lists, lens, q=q)
+    o, _, _, _ = TD.definition(batch, q, lists, lens, batch.scale)
+    step = 2.0 ** -23
+    for b, n in enumerate(batch.tokens):
+        k, v = (batch.rows(x, b).double() for x in (batch.k, batch.v))
+        slots = torch.arange(n)
+        ph = batch.table[b, slots // batch.P].long()
+        power = torch.exp2(batch.scales[ph, :, 1, slots % batch.P].double() - 127)
+        codes = (v / power[..., None]).abs()
+        for head in range(Hq):
+            h = head // batch.g
+            x = k[:, h] @ q[b, head].double() * batch.scale
+            size = (k[:, h].abs() @ q[b, head].double().abs() * batch.scale).max()
+            p = torch.softmax(x, 0)
+            dx = ((d + 8) * step + 2.0 ** -22) * size + 2.0 ** -20 + n * step
+            tol = (2 * dx + n * step) * (p @ v[:, h].abs()) + \
+                2.0 ** -32 * (p * power[:, h]).max() * codes[:, h].sum(0)
+            R.close(out[b, head], o[b, head], tol, f"out {b} {head}")
