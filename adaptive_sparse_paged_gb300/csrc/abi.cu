@@ -58,6 +58,12 @@ bool misaligned(const void* p, uintptr_t bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
 }
 
+// Whether n elements of `bytes` bytes each from a and m of `mbytes` from b have one in common.
+bool overlap(const void* a, size_t n, size_t bytes, const void* b, size_t m, size_t mbytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && n && m && x < y + m * mbytes && y < x + n * bytes;
+}
+
 asp_status check_q8(const asp_paged_kv* kv, const asp_q8_pages* pages) {
   const asp_status st = check_kv(kv, false);
   if (st != ASP_OK) return st;
@@ -435,8 +441,15 @@ asp_status asp_prefix_attention(const asp_paged_kv* kv, const uint16_t* q,
   if ((st = check_rows(num_rows, q)) != ASP_OK) return st;
   if (!row_offsets || !out || !lse || misaligned(out, 16)) return ASP_EINVAL;
   if ((own_out == nullptr) != (own_lse == nullptr) || misaligned(own_out, 16)) return ASP_EINVAL;
-  if ((own_bf16 != 0 && own_bf16 != 1) || lse == own_lse) return ASP_EINVAL;
+  if (own_bf16 != 0 && own_bf16 != 1) return ASP_EINVAL;
   if (!(sm_scale > 0.0f) || !std::isfinite(sm_scale)) return ASP_EINVAL;
+  if (!ws || misaligned(ws, 256)) return ASP_EWORKSPACE;
+  // A row's parts are read by other blocks than those that write it, but for a bf16 own part,
+  // which only the block that replaces it reads.
+  const size_t rows = (size_t)num_rows * kv->num_q_heads, all = rows * kv->head_dim;
+  if (overlap(out, all, 2, q, all, 2) || overlap(lse, rows, 4, own_lse, rows, 4) ||
+      (!(own_bf16 && out == own_out) && overlap(out, all, 2, own_out, all, own_bf16 ? 2 : 4)))
+    return ASP_EINVAL;
   WsLayout lay;
   if ((st = check_ws(kv, ws, ws_bytes, &lay, true)) != ASP_OK) return st;
   if (num_rows == 0) return ASP_OK;

@@ -532,9 +532,10 @@ asp_status asp_q8_decode(const asp_paged_kv* kv, const asp_q8_pages* pages, cons
  * own_lse : fp32 [num_rows, Hq], with it: both over the rows' own tokens, rotated to positions
  *           behind the prefix. Where own_lse is -inf, own_out is not used. Both NULL: the
  *           prefix alone.
- * out     : bf16 [num_rows, Hq, d], 16-byte aligned, not overlapping q (it may be a bf16
- *           own_out itself); lse : fp32 [num_rows, Hq], not the own_lse buffer. Rows outside [row_offsets[0],
- *           row_offsets[batch]) are neither read nor written.
+ * out     : bf16 [num_rows, Hq, d], 16-byte aligned, not overlapping q or own_out (it may be a
+ *           bf16 own_out itself); lse : fp32 [num_rows, Hq], not overlapping own_lse: else
+ *           ASP_EINVAL. Rows outside [row_offsets[0], row_offsets[batch]) are neither read nor
+ *           written.
  * A row without any token gets out = 0, lse = -inf. Pages, errors, roundings and the finite V
  * of the prefixes' tokens as for asp_chunk_attention. ws: a workspace of the prefixes' shape (one
  * of the own caches' shape has the decode's arrival counts where this call's parts would go).

@@ -70,3 +70,23 @@ def test_weights_sum_to_one(cuda_device, d, T, base):
     assert torch.equal(out.cpu(), value.expand(4, 8, d))
     both = torch.logaddexp(torch.full((4, 8), pre, dtype=torch.float64), own_lse.double())
     R.close(lse, both, 4 * R.FP32 * both.abs() + 2.0 ** -18, "lse")
+
+
+def test_no_rows_with_own_parts(cuda_device):
+    """A call without rows, own parts or not, is fine; buffers that overlap are refused."""
+    batch = R.Batch(cuda_device, [20, 7], [3, 1], 8, 2, 64, 16, seed=1)
+    kv = batch.to_device()
+    none = torch.zeros(3, dtype=torch.int32, device=cuda_device)
+    rows, lse = torch.zeros((0, 8, 64), device=cuda_device), torch.zeros((0, 8), device=cuda_device)
+    half = rows.to(torch.bfloat16)
+    for own in (rows, half):
+        B.asp_prefix_attention(kv, half, none, 0.1, own, lse, half.clone(), lse.clone(), batch.ws)
+    assert B.asp_get_device_error(batch.ws) == 0
+    q, own_lse = batch.q.to(cuda_device), torch.zeros((4, 8), device=cuda_device)
+    both = torch.zeros((4, 8, 64), device=cuda_device)
+    inside = both.view(torch.bfloat16).view(-1)[:2048].view(4, 8, 64)
+    for out, lse in ((inside, torch.zeros_like(own_lse)), (q, torch.zeros_like(own_lse)),
+                     (torch.zeros_like(q), own_lse)):
+        with pytest.raises(B.AspError) as e:
+            B.asp_prefix_attention(kv, q, batch.offs_dev, 0.1, both, own_lse, out, lse, batch.ws)
+        assert e.value.status == B.ASP_EINVAL
