@@ -43,7 +43,7 @@ asp_status check_kv(const asp_paged_kv* kv, bool bf16_pages = true) {
 }
 
 // chunk: the call needs the joins and partials at the workspace's end, which only the chunk
-// calls do; a workspace that ends before them serves all others.
+// calls and the prefix call do; a workspace that ends before them serves all others.
 asp_status check_ws(const asp_paged_kv* kv, void* ws, size_t ws_bytes, WsLayout* lay,
                     bool chunk = false) {
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return ASP_EWORKSPACE;

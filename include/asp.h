@@ -128,9 +128,9 @@ const char* asp_status_string(asp_status status);
  * Workspace bytes needed by every call below that takes one, for this shape on
  * the CURRENT device (the grids are sized from its SM count; the partial results
  * of the chunk calls are most of it, 41 MB on 152 SMs at head_dim 128, and lie
- * at its end: only asp_chunk_attention and asp_chunk_weights ask for them, and a
- * workspace of the size that a build without those calls gave still serves all
- * others). Writes the size to *bytes. The workspace is a caller-owned device buffer,
+ * at its end: only asp_chunk_attention, asp_chunk_weights and asp_prefix_attention
+ * ask for them, and a workspace of the size that a build without those calls gave
+ * still serves all others). Writes the size to *bytes. The workspace is a caller-owned device buffer,
  * 256-byte aligned, that must be zeroed once with asp_workspace_init before
  * first use. It holds the device error word,
  * per-call scratch (page scores, the decode's partial results) that every
@@ -537,8 +537,9 @@ asp_status asp_q8_decode(const asp_paged_kv* kv, const asp_q8_pages* pages, cons
  *           ASP_EINVAL. Rows outside [row_offsets[0], row_offsets[batch]) are neither read nor
  *           written.
  * A row without any token gets out = 0, lse = -inf. Pages, errors, roundings and the finite V
- * of the prefixes' tokens as for asp_chunk_attention. ws: a workspace of the prefixes' shape (one
- * of the own caches' shape has the decode's arrival counts where this call's parts would go).
+ * of the prefixes' tokens as for asp_chunk_attention. ws: as long as asp_workspace_size says for
+ * the prefixes' shape; it may be the workspace of the own caches, whose calls are ordered with
+ * this one on one stream: this call's parts lie behind every shape's arrival counts.
  */
 asp_status asp_prefix_attention(const asp_paged_kv* kv, const uint16_t* q,
                                 const int32_t* row_offsets, int32_t num_rows, float sm_scale,

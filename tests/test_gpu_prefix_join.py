@@ -8,7 +8,8 @@ import torch
 from adaptive_sparse_paged_gb300 import binding as B
 from tests import guards
 from tests import prompt_ref as R
-from tests import test_gpu_prefix as TP
+from tests import q8_ref as Q
+from tests import test_gpu_q8_decode as TD
 
 pytestmark = pytest.mark.gpu
 
@@ -70,6 +71,31 @@ def test_weights_sum_to_one(cuda_device, d, T, base):
     assert torch.equal(out.cpu(), value.expand(4, 8, d))
     both = torch.logaddexp(torch.full((4, 8), pre, dtype=torch.float64), own_lse.double())
     R.close(lse, both, 4 * R.FP32 * both.abs() + 2.0 ** -18, "lse")
+
+
+def test_one_workspace_for_the_own_caches_too(cuda_device):
+    """The prefix call in the workspace of the decode whose results it joins, of another shape:
+    both give what they give in workspaces of their own, call after call."""
+    own = Q.Q8Batch(cuda_device, [4000] + [60] * 90, [0] * 91, 8, 2, 64, 16, seed=2)
+    batch = R.Batch(cuda_device, [2500, 40], [90, 1], 8, 2, 64, 16, seed=3)
+    kv, pkv = own.to_device(), batch.to_device()
+    lists, lens = (x.to(cuda_device) for x in TD.random_lists(own, 1.0))
+    q = batch.q.to(cuda_device)
+    shared = guards.guarded((max(own.ws.numel(), batch.ws.numel()),), torch.uint8, cuda_device,
+                            what="one workspace")
+    B.asp_workspace_init(shared)
+    results = []
+    for ws, pws in ((own.ws, batch.ws), (shared, shared)):
+        for _ in range(3):
+            o, ol = torch.zeros((91, 8, 64), device=cuda_device), torch.zeros((91, 8), device=cuda_device)
+            out, lse = outputs(batch)
+            B.asp_q8_decode(kv, q.float(), lists, lens, 0.125, o, ol, ws)
+            B.asp_prefix_attention(pkv, q, batch.offs_dev, 0.125, o, ol, out, lse, pws)
+            assert B.asp_get_device_error(ws) == 0 and B.asp_get_device_error(pws) == 0
+            results.append([x.clone() for x in (o, ol, out, lse)])
+    for r in results[1:]:
+        for x, y in zip(r, results[0]):
+            assert torch.equal(x, y)
 
 
 def test_no_rows_with_own_parts(cuda_device):

@@ -35,3 +35,20 @@ def test_selection_prefetches_only_pages_that_are_there(probe, over, pages):
     n = probe.select_prefetch(ctypes.byref(kv(**over)), *(ctypes.byref(x) for x in there))
     assert [x.value for x in there] == [int(pages)] * 2
     assert (n > 0) == pages
+
+
+def test_chunk_parts_lie_behind_all_arrival_counts(probe):
+    """The chunk calls' and the prefix call's parts, of whatever shape, never lie where a decode of
+    another shape keeps its arrival counts between calls: one workspace can serve both."""
+    def parts(**shape):
+        at = (ctypes.c_longlong * 4)()
+        probe.workspace_parts(ctypes.byref(kv(**shape)), 152, at)
+        return list(at)
+
+    shapes = [dict(batch=b, num_kv_heads=h, num_q_heads=h, head_dim=d, max_pages=n)
+              for b in (1, 3, 64, 512) for h in (1, 8) for d in (64, 128) for n in (1, 17, 8192)]
+    got = [parts(**s) for s in shapes]
+    last = max(end for _, end, _, _ in got)
+    assert last == 256 + 4 * 4096  # the most segments a call may have
+    for begin, end, joins, total in got:
+        assert begin == 256 and last <= joins < total
