@@ -22,6 +22,14 @@ def _check_shape(name, t, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _quant(kvs):
+    """Whether the layers are QuantPagedKV: all of them or none."""
+    quant = isinstance(kvs[0], B.QuantPagedKV)
+    if any(isinstance(kv, B.QuantPagedKV) != quant for kv in kvs):
+        raise ValueError("8-bit and bf16 layers do not mix in a step")
+    return quant
+
+
 class DecodeStep:
     def __init__(self, kvs, q, gamma: float, budget: int = 0, sm_scale: float | None = None,
                  append=None, weights=None, decay: float = 1.0, prefix=None):
@@ -58,7 +66,7 @@ class DecodeStep:
         if weights is not None:
             _check_shape("weights", weights, (L,) + tuple(B.weights_shape(kv0)))
         self.weights, self.decay = weights, float(decay)
-        self.quant = isinstance(kv0, B.QuantPagedKV)
+        self.quant = _quant(self.kvs)
         if self.quant and (append is not None or weights is not None):
             raise ValueError("append and weights want bf16 pages")
         self.prefix = prefix
@@ -256,8 +264,8 @@ class ChunkStep:
         bf16 [L, d] or None; positions: int32 [N] or None (the slots); weights: fp32
         [L, B, Hkv, max_pages * P] or None, becomes decay * weights + what the chunk gave (not of
         8-bit layers); pair_axis: int32 [rotary_dim / 2], positions then int32 [num_axes, N];
-        staging: for QuantPagedKV layers a PagedKV of their batch, seq_lens and sizes, whose
-        pages each layer's tokens are read back into."""
+        staging: for QuantPagedKV layers a PagedKV of their batch, sizes and seq_lens (one buffer
+        for all layers and staging), whose pages each layer's tokens are read back into."""
         self.kvs = list(kvs)
         if not self.kvs:
             raise ValueError("kvs must hold at least one layer")
@@ -271,14 +279,16 @@ class ChunkStep:
                 _check_shape(name, w, (L, kv0.head_dim))
         if weights is not None:
             _check_shape("weights", weights, (L,) + tuple(B.weights_shape(kv0)))
-        self.quant = isinstance(kv0, B.QuantPagedKV)
+        self.quant = _quant(self.kvs)
         if self.quant:
             if weights is not None:
                 raise ValueError("weights want bf16 pages")
-            if staging is None or (staging.batch, staging.max_pages) != (kv0.batch, kv0.max_pages):
-                raise ValueError("8-bit layers need a staging cache of their batch and max_pages")
-            if staging.seq_lens.data_ptr() != kv0.seq_lens.data_ptr():
-                raise ValueError("staging must have the layers' own seq_lens")
+            # a layer is read back by its own table and lengths, and attended over by staging's
+            for kv in self.kvs:
+                if staging is None or (staging.batch, staging.max_pages) != (kv.batch, kv.max_pages):
+                    raise ValueError("8-bit layers need a staging cache of their batch and max_pages")
+                if staging.seq_lens.data_ptr() != kv.seq_lens.data_ptr():
+                    raise ValueError("staging must have every layer's own seq_lens")
         self.pair_axis, self.staging = pair_axis, staging
         self.qkv, self.q_offsets, self.inv_freq = qkv, q_offsets, inv_freq
         self.q_weight, self.k_weight, self.positions = q_weight, k_weight, positions
