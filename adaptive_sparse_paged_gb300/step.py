@@ -42,7 +42,7 @@ class DecodeStep:
         weights: optional fp32 [L, B, Hkv, max_pages * P], the attention weight every
         cached token has received so far: after each layer's attention it becomes
         decay * weights + what this step gave (asp_decode_weights, in place; a
-        replay adds again).
+        replay adds again). With a prefix, what it gave is of the attention over both.
         prefix: optional (prefix_kvs, row_offsets, q_bf16): the requests row_offsets[i] ..
         row_offsets[i + 1] - 1 (int32 [groups + 1]) share prefix i of prefix_kvs (a PagedKV per
         layer); kvs hold only what is their own. q_bf16: bf16 [L, B, Hq, d], the same queries.
@@ -120,8 +120,9 @@ class DecodeStep:
         if events is not None:
             events[2].record(stream)
         if self.weights is not None:
-            B.asp_decode_weights(kv, self.q[l], self.lists[l], self.lens[l], self.lse[l],
-                                 self.sm_scale, self.decay, self.weights[l],
+            lse = self.lse[l] if self.prefix is None else self.joined_lse[l]
+            B.asp_decode_weights(kv, self.q[l], self.lists[l], self.lens[l], lse, self.sm_scale,
+                                 self.decay, self.weights[l],
                                  self.weights[l] if w_out is None else w_out, self.ws, stream)
 
     def run(self, stream=None):

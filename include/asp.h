@@ -372,7 +372,8 @@ asp_status asp_chunk_weights(const asp_paged_kv* kv, const uint16_t* q, const in
  * for the tokens s < T_b of the listed pages, and decay * w_in for the others;
  * w_in is not read for the token being decoded (s = T_b - 1).
  * q    : fp32 [B, Hq, d], 16-byte aligned; lse : fp32 [B, Hq], as
- *        asp_sparse_decode wrote it over the same lists.
+ *        asp_sparse_decode wrote it over the same lists, or as asp_prefix_attention
+ *        joined it with a prefix's (the weights are then of the attention over both).
  * lists, lens : as written by asp_coverage_select; each page at most once in a
  *        list. Both NULL: every page.
  * Other arguments and conditions as for asp_chunk_weights; any sm_scale > 0.

@@ -1,10 +1,11 @@
-"""DecodeStep and ChunkStep where layers or caches do not fit together."""
+"""DecodeStep and ChunkStep where layers or caches do not fit together, and weights behind a prefix."""
 
 import pytest
 import torch
 
 from adaptive_sparse_paged_gb300 import binding as B
 from adaptive_sparse_paged_gb300.step import ChunkStep, DecodeStep
+from tests import prompt_ref as R
 from tests import q8_ref as Q
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +36,49 @@ def test_staging_goes_with_every_layer(cuda_device):
     q = torch.zeros((2, 2, 8, 64), device=dev)
     with pytest.raises(ValueError, match="8-bit"):
         DecodeStep([kvs[0], plain], q, 0.9)
+
+
+@pytest.mark.parametrize("d,gamma", [(64, 0.9), (128, 1.0)])
+def test_weights_behind_a_prefix(cuda_device, d, gamma):
+    """What every cached token received of attention over the prefix and the own tokens together:
+    its probability among both, which the own tokens' lse alone would make too large.
+
+    Bound: a weight is exp(s - lse). s is d products in fp32 of bf16 numbers, the queries in three
+    bf16 terms (24 bits); the own lse has them in two (2^-17), the prefix's as they are (bf16
+    numbers here); sums of under 300 terms, logarithms and exponentials are a few fp32 steps."""
+    dev = cuda_device
+    own = [R.Batch(dev, [70, 33, 5], [0] * 3, 8, 2, d, 16, seed=s) for s in (1, 2)]
+    pre = [R.Batch(dev, [200, 1], [2, 1], 8, 2, d, 16, seed=s) for s in (3, 4)]
+    kvs, pkvs = [b.to_device() for b in own], [b.to_device() for b in pre]
+    for b, kv in zip(own, kvs):
+        B.asp_page_summarize(kv, B.ASP_SUMMARIZE_BULK, None, None, b.ws)
+    rows = torch.tensor([0, 2, 3], dtype=torch.int32, device=dev)
+    q16 = torch.randn((2, 3, 8, d), generator=own[0].gen).to(torch.bfloat16)
+    q32 = q16.float()
+    weights = torch.zeros((2,) + tuple(kvs[0].weights_shape), device=dev)
+    step = DecodeStep(kvs, q32.to(dev), gamma, weights=weights,
+                      prefix=(pkvs, rows, q16.to(dev)))
+    step.run()
+    assert B.asp_get_device_error(step.ws) == 0 and B.asp_get_device_error(step.prefix_ws) == 0
+    lists, counts = step.lists.cpu(), step.lens.cpu()
+    for l in range(2):
+        for r in range(3):
+            group, T = (0, 0, 1)[r], own[l].tokens[r]
+            for h in range(2):
+                ids = lists[l, r, h, :int(counts[l, r, h])].long()
+                at = (ids[:, None] * 16 + torch.arange(16)).flatten()
+                at = at[at < T]
+                heads = slice(4 * h, 4 * h + 4)
+                q = q32[l, r, heads].double()
+                k = own[l].rows(own[l].k, r)[at, h].double()
+                pk = pre[l].rows(pre[l].k, group)[:, h].double()
+                x, px = q @ k.T * step.sm_scale, q @ pk.T * step.sm_scale
+                size = torch.cat([(q.abs() @ y.abs().T * step.sm_scale).flatten() for y in (k, pk)]).max()
+                lse = torch.logsumexp(torch.cat([x, px], 1), 1)
+                want = torch.zeros(T, dtype=torch.float64)
+                want[at] = torch.exp(x - lse[:, None]).sum(0)
+                dx = (2 * (d + 8) * 2.0 ** -23 + 2.0 ** -17) * size + 2.0 ** -18 + 300 * 2.0 ** -23
+                R.close(weights[l, r, h, :T], want, 2 * dx * want + 1e-30, f"weights {l} {r} {h}")
+                if group == 0:  # the prefix of one token takes little
+                    alone = torch.exp(x - torch.logsumexp(x, 1)[:, None]).sum(0)
+                    assert bool((alone > want[at] * (1 + 4 * dx)).all())
