@@ -46,7 +46,9 @@ class DecodeStep:
         prefix: optional (prefix_kvs, row_offsets, q_bf16): the requests row_offsets[i] ..
         row_offsets[i + 1] - 1 (int32 [groups + 1]) share prefix i of prefix_kvs (a PagedKV per
         layer); kvs hold only what is their own. q_bf16: bf16 [L, B, Hq, d], the same queries.
-        The attention over both is left in `joined` (bf16) and `joined_lse`.
+        The attention over both is left in `joined` (bf16) and `joined_lse`. Requests that
+        row_offsets leaves out when the step is made have their own attention there, which costs a
+        step two copies a layer; offsets that name them all have to go on doing so.
         """
         self.kvs = list(kvs)
         if not self.kvs:
@@ -78,6 +80,7 @@ class DecodeStep:
             self.joined = torch.zeros(tuple(q.shape), dtype=torch.bfloat16, device=dev)
             self.joined_lse = torch.zeros(tuple(q.shape[:3]), dtype=torch.float32, device=dev)
             self.prefix_ws = B.new_workspace(prefix[0][0])
+            self.left_out = prefix[1][[0, -1]].tolist() != [0, kv0.batch]
         self.lists = torch.zeros((L, kv0.batch, kv0.num_kv_heads, kv0.max_pages), dtype=torch.int32,
                                  device=dev)
         self.lens = torch.zeros((L, kv0.batch, kv0.num_kv_heads), dtype=torch.int32, device=dev)
@@ -90,12 +93,13 @@ class DecodeStep:
     # kernel launches of one step, per layer: the selection's (one cluster
     # kernel, or a score pass and a select kernel; select alone at gamma = 1),
     # the decode, the append kernel when enabled, the two of the weights and the two of a prefix
+    # (with the two copies for requests that have none)
     @property
     def launches_per_step(self) -> int:
         per, _ = B.asp_select_plan(self.kvs[0], self.gamma, self.budget)
         return len(self.kvs) * (per + 1 + (1 if self.append is not None else 0) +
                                 (2 if self.weights is not None else 0) +
-                                (2 if self.prefix is not None else 0))
+                                (0 if self.prefix is None else 4 if self.left_out else 2))
 
     def run_layer(self, l: int, stream=None, events=None, w_out=None):
         """w_out: where layer l's weights go instead of back to where they come from."""
@@ -114,6 +118,10 @@ class DecodeStep:
                self.ws, stream)
         if self.prefix is not None:
             prefix_kvs, offsets, q = self.prefix
+            if self.left_out:
+                with torch.cuda.stream(stream):
+                    self.joined[l].copy_(self.out[l])
+                    self.joined_lse[l].copy_(self.lse[l])
             B.asp_prefix_attention(prefix_kvs[l], q[l], offsets, self.sm_scale, self.out[l],
                                    self.lse[l], self.joined[l], self.joined_lse[l], self.prefix_ws,
                                    stream)

@@ -82,3 +82,34 @@ def test_weights_behind_a_prefix(cuda_device, d, gamma):
                 if group == 0:  # the prefix of one token takes little
                     alone = torch.exp(x - torch.logsumexp(x, 1)[:, None]).sum(0)
                     assert bool((alone > want[at] * (1 + 4 * dx)).all())
+
+
+@pytest.mark.parametrize("offsets,weights", [([0, 3], True), ([1, 3], True), ([0, 2], False), ([2, 2], True)])
+def test_requests_without_a_group(cuda_device, offsets, weights):
+    """Requests that row_offsets leaves out have no prefix: what is joined is their own attention,
+    rounded once, and their weights go by it."""
+    dev = cuda_device
+    own = R.Batch(dev, [70, 33, 5], [0] * 3, 8, 2, 64, 16, seed=1)
+    pre = R.Batch(dev, [200], [1], 8, 2, 64, 16, seed=3)
+    kv, pkv = own.to_device(), pre.to_device()
+    B.asp_page_summarize(kv, B.ASP_SUMMARIZE_BULK, None, None, own.ws)
+    q16 = torch.randn((1, 3, 8, 64), generator=own.gen).to(torch.bfloat16).to(dev)
+    rows = torch.tensor(offsets, dtype=torch.int32, device=dev)
+    got = []
+    for prefix in ((([pkv]), rows, q16), None):
+        w = torch.zeros((1,) + tuple(kv.weights_shape), device=dev) if weights else None
+        step = DecodeStep([kv], q16.float(), 0.9, weights=w, prefix=prefix)
+        step.capture()
+        for _ in range(2):
+            if w is not None:
+                w.zero_()
+            step.replay()
+        assert B.asp_get_device_error(step.ws) == 0
+        assert prefix is None or B.asp_get_device_error(step.prefix_ws) == 0
+        got.append((step, w))
+    (step, w), (plain, w0) = got
+    for r in range(3):
+        joined = offsets[0] <= r < offsets[1]
+        same = torch.equal(step.joined[0, r], plain.out[0, r].to(torch.bfloat16))
+        assert same != joined and torch.equal(step.joined_lse[0, r], plain.lse[0, r]) != joined
+        assert w is None or torch.equal(w[0, r], w0[0, r]) != joined
