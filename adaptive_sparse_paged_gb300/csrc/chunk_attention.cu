@@ -598,8 +598,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (task.whole) {
         float inv = l > 0.f ? 1.0f / l : l;  // a NaN sum stays NaN, an empty row gives 0
         float lse = l == 0.f ? -INFINITY : m * p.scale + logf(l), own = 0.f;
+        bool has_own = false;  // its NaN counts even where its weight is none
         if (kPrefix) {
-          const OwnPart part(m * p.scale, l, p.own_lse && mine ? p.own_lse[at] : -INFINITY);
+          const float own_lse = p.own_lse && mine ? p.own_lse[at] : -INFINITY;
+          has_own = own_lse != -INFINITY;
+          const OwnPart part(m * p.scale, l, own_lse);
           inv = part.prefix, own = part.own, lse = part.lse;
         }
         // Four lanes exchange 16-byte pieces so that a row's 64 bytes leave together: a
@@ -616,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < D / 32 && n > 0; ++i) {
           uint32_t o[32], y[4][4];  // y[piece][word]
           load_o(i, o);
-          if (kPrefix && own != 0.f) {
+          if (kPrefix && has_own) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const float4 x = own4(p, at * D + 32 * i + 4 * e);

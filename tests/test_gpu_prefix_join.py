@@ -73,6 +73,28 @@ def test_weights_sum_to_one(cuda_device, d, T, base):
     R.close(lse, both, 4 * R.FP32 * both.abs() + 2.0 ** -18, "lse")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tokens,rows", [([3000], [5]), ([40], [700])])
+def test_nan_of_an_own_part_shows(cuda_device, d, tokens, rows):
+    """A NaN in own_out counts wherever its row has own tokens, be their weight too small for fp32:
+    in items that are joined and in whole ones alike. Where own_lse is -inf it does not."""
+    batch = R.Batch(cuda_device, tokens, rows, 8, 2, d, 16, seed=d)
+    kv = batch.to_device()
+    own_out = torch.zeros((batch.N, 8, d), device=cuda_device)
+    own_out[..., 7] = math.nan
+    own_lse = torch.full((batch.N, 8), -300.0, device=cuda_device)
+    own_lse[1::2] = -math.inf
+    for half in (False, True):
+        out, lse = outputs(batch)
+        part = own_out.to(torch.bfloat16) if half else own_out
+        B.asp_prefix_attention(kv, batch.q.to(cuda_device), batch.offs_dev, batch.scale, part, own_lse,
+                               out, lse, batch.ws)
+        assert B.asp_get_device_error(batch.ws) == 0
+        nan = torch.zeros((batch.N, 8, d), dtype=torch.bool)
+        nan[0::2, :, 7] = True
+        assert torch.equal(out.isnan().cpu(), nan) and bool(lse.isfinite().all())
+
+
 def test_one_workspace_for_the_own_caches_too(cuda_device):
     """The prefix call in the workspace of the decode whose results it joins, of another shape:
     both give what they give in workspaces of their own, call after call."""
