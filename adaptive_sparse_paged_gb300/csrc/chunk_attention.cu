@@ -125,9 +125,10 @@ struct OwnPart {
     const bool none = l == 0.f;
     const float top = none ? own_lse : fmaxf(ref, own_lse), at = top == -INFINITY ? 0.f : top;
     const float a = none ? 0.f : expf(ref - at), b = expf(own_lse - at), sum = fmaf(l, a, b);
+    const float inv = 1.0f / sum;
     lse = at + logf(sum);
-    prefix = none ? 0.f : a / sum;
-    own = own_lse == -INFINITY ? 0.f : b / sum;
+    prefix = none ? 0.f : a * inv;
+    own = own_lse == -INFINITY ? 0.f : b * inv;
   }
 };
 
