@@ -28,13 +28,14 @@
 // the integer position wraps exactly modulo one turn; what it is past the nearest quarter turn
 // goes into the series of sine and cosine, so that they keep fp32's full precision.
 //
-// Measured: 18k tokens of 48 heads (d = 128) into 8-bit pages in 76 us, 5.3 TB/s read and
+// Measured: 18k tokens of 48 heads (d = 128) into 8-bit pages in 77 us, 5.3 TB/s read and
 // written (the copy of the same bytes would take 60); 7k tokens on three axes into bf16 in 37 us
 // (26), of which a seventh is SMs that make a round less. 59 us without the queries' norm,
 // rotation and stores: what is left is some 230 instructions for four rows, at 60% of the issue
 // slots. Two rows a warp (16 lanes each) took 108 us, rows loaded from global memory by each
 // warp 111, the key heads' minima in registers, ten more than there are, 89. 64 decoded tokens:
-// 5.5 us.
+// 5.5 us. Half of the channels turned (rotary_dim 64): 87 and 41 us (pairs side by side 81 and
+// 37), with accesses of 8 bytes instead of 16 and up to 20 bytes of spills.
 #include <cuda_fp16.h>
 
 #include "tc.cuh"

@@ -1175,9 +1175,9 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   if (d == 64 && P == 64) return launch_decode_dp<64, 64>(a, stream);
   return cudaErrorInvalidValue;
 }
-// Groups of up to four heads are packed: all of 4 x 128k tokens, four heads a group, in 98.1 us
-// instead of 105.7 at d = 64 and 145.7 instead of 147.1 at d = 128; 2k tokens of d = 64, all
-// latency, in 11.2 instead of 10.7.
+// Groups of up to four heads are packed: all of 4 x 128k tokens, four heads a group, in 96.8 us
+// instead of 105.0 at d = 64 and 144.0 instead of 144.5 at d = 128; 2k tokens of d = 64, all
+// latency, in 11.4 instead of 10.9.
 cudaError_t launch_q8_decode(const DecodeArgs& a, cudaStream_t stream) {
   return a.kv->num_q_heads / a.kv->num_kv_heads <= 4 ? launch_q8<true>(a, stream)
                                                      : launch_q8<false>(a, stream);

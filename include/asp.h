@@ -21,9 +21,10 @@
  * --------------------------------
  * - Pointers: every tensor pointer is a DEVICE pointer (cudaMalloc'd or
  *   equivalent) that the caller owns. The library never allocates or frees
- *   memory and never synchronises inside the hot calls (asp_page_summarize,
- *   asp_coverage_select, asp_sparse_decode), so they may be captured into a
- *   CUDA graph. All work is enqueued on `stream`.
+ *   memory and never synchronises, but in asp_get_device_error: every other
+ *   call that takes a stream may be captured into a CUDA graph (its first call
+ *   on a device loads its kernels: make that one before). All work is enqueued
+ *   on `stream`.
  * - bf16 tensors are passed as uint16_t bit patterns.
  * - Errors: arguments are checked on the host before any launch; a bad one
  *   returns a negative asp_status and launches nothing. Problems that only
@@ -85,16 +86,19 @@ typedef void* asp_stream;
  * Paged KV cache of ONE layer, plus its page summaries.
  *
  *   k_cache, v_cache : bf16 [num_phys_pages, Hkv, P, d]. The (page, head) block
- *                      of P*d values is contiguous. Only asp_page_summarize in
- *                      APPEND mode writes them.
+ *                      of P*d values is contiguous. Written by the calls that
+ *                      append (asp_page_summarize in APPEND mode,
+ *                      asp_coverage_select_append, asp_norm_rotate_append and
+ *                      asp_norm_rotate_axes_append) and by asp_weight_evict.
  *   summaries        : bf16 [batch, Hkv, max_pages, 2, d], in LOGICAL page
  *                      order: entry (b, h, p) summarises logical page p < N_b
  *                      of request b for KV head h; row 0 is the channel
  *                      minimum of K over the page's valid tokens, row 1 the
  *                      maximum. Each (request, KV head) segment's summaries
  *                      are one contiguous run, so the estimate pass streams
- *                      them sequentially. Written by asp_page_summarize, read
- *                      by asp_coverage_select.
+ *                      them sequentially. Written by asp_page_summarize, the
+ *                      calls that append and asp_weight_evict, read by
+ *                      asp_coverage_select.
  *   block_table      : int32 [batch, max_pages]; entry (b, p) is the physical
  *                      page holding logical page p of request b. Shared by all
  *                      heads and layers. Only entries p < N_b are read.
@@ -309,7 +313,7 @@ asp_status asp_sparse_decode(const asp_paged_kv* kv, const float* q,
  * rotary_dim : 0 (no rotation) to d, a multiple of 8.
  * q_out, q_out_f32 : [num_tokens, Hq, d] out, in bf16 (for asp_chunk_attention)
  *              or fp32 (for asp_coverage_select and asp_sparse_decode); either
- *              may be NULL, not both. 16-byte aligned.
+ *              may be NULL, not both. 16-byte aligned, not overlapping qkv.
  * K (rounded once to bf16) and V go to slot (T_b - n_b + i) of their request;
  * a page whose slot 0 is among them starts its summary afresh, the others fold
  * into theirs. Idempotent. A physical page that takes new tokens belongs to one
@@ -435,7 +439,9 @@ asp_status asp_weight_evict(const asp_paged_kv* kv, const float* weights, int32_
  *             frequencies, axes in turn or any other order. NULL: all of axis 0. An
  *             entry outside [0, num_axes) sets ASP_DEVERR_AXIS_RANGE; that pair is
  *             not turned.
- * Everything else as for asp_norm_rotate_append, which this is when num_axes is 1.
+ * Everything else as for asp_norm_rotate_append, which this is, bit for bit, when
+ * num_axes is 1 and pair_axis NULL; a pair_axis that names axis 0 throughout asks for
+ * the same numbers of another kernel, whose last bits may differ.
  */
 #define ASP_MAX_AXES 8
 asp_status asp_norm_rotate_axes_append(const asp_paged_kv* kv, const uint16_t* qkv,
