@@ -289,7 +289,8 @@ asp_status asp_sparse_decode(const asp_paged_kv* kv, const float* q,
  * more rows than seq_lens[b], set ASP_DEVERR_OFFSET_RANGE: that request is
  * skipped (nothing of it is written, its weights neither), and others of the
  * call may be: the calls that append skip every request behind the first whose
- * offsets descend, whole. num_tokens may be 0; at most ASP_MAX_NEW_TOKENS.
+ * offsets, held to [0, num_tokens], descend, whole. num_tokens may be 0; at most
+ * ASP_MAX_NEW_TOKENS.
  * ------------------------------------------------------------------------
  */
 #define ASP_MAX_NEW_TOKENS (1 << 22)
